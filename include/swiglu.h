@@ -430,6 +430,60 @@ swiglu_status swiglu_mlp_unfused(const swiglu_bf16 *A, const swiglu_bf16 *W1g,
                                  int64_t K, int64_t N, void *workspace,
                                  size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Training.  With G = A W1, U = A W2, s = 1 / (1 + e^-G), h = G s, Y = h U, a
+ * gradient dY [M,N] of a scalar gives
+ *     dU = dY h,  dG = dY U s (1 + G (1 - s)),
+ *     dA = dG W1^T + dU W2^T,  dW1 = A^T dG,  dW2 = A^T dU,
+ * and for the block Z = Y W3 (W3 [N,K]) a gradient dZ [M,K] gives dY = dZ W3^T
+ * and dW3 = Y^T dZ.  Everything is bf16 in memory and row-major; weights are
+ * taken as the optimizer holds them, without packing.  Sums are fp32; dG and dU
+ * are rounded to bf16 once, as operands of the matrix cores; each output is
+ * rounded once.  Sums are added in a fixed order: a call repeated on the same
+ * inputs gives the same bits.
+ *
+ * swiglu_train_workspace_bytes: workspace of the backward calls at (M,K,N):
+ *   [dG | dU] (4 M N bytes) and, for small products, fp32 sums of splits of the
+ *   contraction; enough for the forward call too.  0 for an invalid shape and
+ *   for M == 0.
+ * swiglu_train_forward_workspace_bytes: workspace of the forward call alone
+ *   (sums of splits; 0 where it needs none).
+ * swiglu_train_forward: Y = SiLU(G) U, and G and U rounded to bf16 (each [M,N]),
+ *   which the backward calls take.
+ * swiglu_train_backward: dA [M,K], dW1, dW2 [K,N].  G and U kept by the forward
+ *   call, or both NULL: computed again from A, W1 and W2 (never written).  dA
+ *   may be NULL (not wanted), and so may dW1 and dW2, together.
+ * swiglu_mlp_train_backward: dA, dW1, dW2, dW3 [N,K] from dZ and the kept G, U
+ *   and Y.  dA may be NULL; dW1, dW2, dW3 may be NULL together (Y is then not
+ *   read and may be NULL too).
+ * All: K and N multiples of 8 and at most 2^20, pointers 16-byte aligned;
+ * inputs may overlap each other, outputs and the workspace nothing; the
+ * workspace's contents on entry do not matter, and calls that may run
+ * concurrently must not share one (ERR_WORKSPACE if it is smaller than needed).
+ * M == 0: the forward call does nothing; the backward calls set the weight
+ * gradients they are given to zero and read nothing.
+ * ---------------------------------------------------------------------- */
+size_t swiglu_train_workspace_bytes(int64_t M, int64_t K, int64_t N);
+size_t swiglu_train_forward_workspace_bytes(int64_t M, int64_t K, int64_t N);
+swiglu_status swiglu_train_forward(const swiglu_bf16 *A, const swiglu_bf16 *W1,
+                                   const swiglu_bf16 *W2, swiglu_bf16 *Y,
+                                   swiglu_bf16 *G, swiglu_bf16 *U, int64_t M,
+                                   int64_t K, int64_t N, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+swiglu_status swiglu_train_backward(const swiglu_bf16 *dY, const swiglu_bf16 *A,
+                                    const swiglu_bf16 *W1, const swiglu_bf16 *W2,
+                                    const swiglu_bf16 *G, const swiglu_bf16 *U,
+                                    swiglu_bf16 *dA, swiglu_bf16 *dW1,
+                                    swiglu_bf16 *dW2, int64_t M, int64_t K,
+                                    int64_t N, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+swiglu_status swiglu_mlp_train_backward(
+    const swiglu_bf16 *dZ, const swiglu_bf16 *A, const swiglu_bf16 *W1,
+    const swiglu_bf16 *W2, const swiglu_bf16 *W3, const swiglu_bf16 *G,
+    const swiglu_bf16 *U, const swiglu_bf16 *Y, swiglu_bf16 *dA,
+    swiglu_bf16 *dW1, swiglu_bf16 *dW2, swiglu_bf16 *dW3, int64_t M, int64_t K,
+    int64_t N, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -67,6 +67,11 @@ SIGNATURES = {
     "swiglu_mlp_unfused": ([_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P],
                            ctypes.c_int),
     "swiglu_mlp_down": ([_P, _P, _P, _I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_train_workspace_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "swiglu_train_forward_workspace_bytes": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "swiglu_train_forward": ([_P] * 6 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_train_backward": ([_P] * 9 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_mlp_train_backward": ([_P] * 12 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     # include/swiglu_probe.h (diagnostic ceilings)
     "swiglu_probe_mfma": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_read": ([_P, ctypes.c_size_t, _P, ctypes.c_int, _P], ctypes.c_int),
@@ -655,3 +660,8 @@ def swiglu_probe_read(src: torch.Tensor, sink: torch.Tensor, blocks: int, stream
         raise ValueError("sink must be a GPU int32 tensor of >= blocks*256 elements")
     _check("swiglu_probe_read", lib().swiglu_probe_read(src.data_ptr(), nbytes, sink.data_ptr(), blocks,
                                                         _stream(stream)))
+
+
+# training (gradients and differentiable forms of the product and the block)
+from .train import (swiglu, swiglu_mlp, swiglu_mlp_train_backward, swiglu_train_backward,  # noqa: E402,F401
+                    swiglu_train_forward, swiglu_train_forward_workspace_bytes, swiglu_train_workspace_bytes)

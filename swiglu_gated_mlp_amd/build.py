@@ -2,8 +2,10 @@
 
     python -m swiglu_gated_mlp_amd.build
 
-The library is one translation unit: csrc/swiglu_api.hip includes the kernels
-from csrc/fused_kernels.hpp and exports the C ABI of include/swiglu.h.
+Two translation units, compiled side by side, export the C ABI of
+include/swiglu.h: csrc/swiglu_api.hip (the products, kernels in
+csrc/fused_kernels.hpp) and csrc/train_api.hip (training, kernels in
+csrc/train_kernels.hpp).
 """
 from __future__ import annotations
 
@@ -11,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libswiglu.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = [os.path.join(CSRC, "swiglu_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("swiglu_api.hip", "train_api.hip")]
 ARCH = os.environ.get("SWIGLU_OFFLOAD_ARCH", "gfx950")
 
 
@@ -31,7 +35,7 @@ def hipcc() -> str:
 
 def compile_flags():
     return [
-        "--offload-arch=%s" % ARCH, "-O3", "-std=c++17", "-fPIC", "-shared",
+        "--offload-arch=%s" % ARCH, "-O3", "-std=c++17", "-fPIC",
         # no packed-fp32 instructions in device code
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall", "-Wno-unused-result", "-I", INCLUDE, "-I", CSRC,
@@ -44,10 +48,7 @@ def link_flags():
     return []
 
 
-def build(verbose: bool = False) -> str:
-    """Compile the library (always recompiles) and return its path."""
-    tmp = LIB_PATH + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *compile_flags(), "-o", tmp, *SOURCES, *link_flags()]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -57,6 +58,17 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError("hipcc failed (%d):\n%s" % (res.returncode, out))
     if verbose and out.strip():
         print(out, flush=True)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile the library (always recompiles) and return its path."""
+    tmp = LIB_PATH + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory(prefix="swiglu_build") as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(len(SOURCES)) as pool:
+            list(pool.map(lambda so: _run([hipcc(), *compile_flags(), "-c", so[0], "-o", so[1]], verbose),
+                          zip(SOURCES, objs)))
+        _run([hipcc(), "--offload-arch=%s" % ARCH, "-shared", "-fPIC", "-o", tmp, *objs, *link_flags()], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

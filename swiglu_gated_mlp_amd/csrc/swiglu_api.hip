@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "fused_kernels.hpp"
+#include "host_common.hpp"
 #include "probe_kernels.hpp"
 
 // Device scratch of swiglu_fused_packed_noalloc: the split-K partial sums of
@@ -25,17 +26,13 @@
 // device address comes from hipGetSymbolAddress (scratch_device_ptr below).
 static __device__ __align__(256) unsigned char scratch[SWIGLU_NOALLOC_SCRATCH_BYTES];
 
-namespace {
-
+namespace swh {
 thread_local int g_last_hip_error = 0;
-
-swiglu_status hip_fail(hipError_t e) {
-    g_last_hip_error = (int)e;
-    return SWIGLU_ERR_HIP;
 }
 
-constexpr int64_t kMaxDim = (int64_t)1 << 30;   // every dimension fits int32 with room
-constexpr int64_t kMaxK = (int64_t)1 << 22;     // 256 rows of activations stay below 2 GiB
+using namespace swh;
+
+namespace {
 
 bool log_enabled() {
     static int on = -1;
@@ -44,34 +41,6 @@ bool log_enabled() {
         on = (s && s[0] && s[0] != '0') ? 1 : 0;
     }
     return on == 1;
-}
-
-// ---------------------------------------------------------------------------
-// argument checks (host only, no HIP calls)
-// ---------------------------------------------------------------------------
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-    uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-    return Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes};
-}
-
-bool overlap(Range a, Range b) {
-    if (a.lo == a.hi || b.lo == b.hi) return false;
-    return a.lo < b.hi && b.lo < a.hi;
-}
-
-swiglu_status check_shape(int64_t M, int64_t K, int64_t N) {
-    if (M < 0 || K <= 0 || N <= 0) return SWIGLU_ERR_BAD_SHAPE;
-    if (M > kMaxDim || K > kMaxDim || N > kMaxDim) return SWIGLU_ERR_BAD_SHAPE;
-    if (M * N > ((int64_t)1 << 40) || K * N > ((int64_t)1 << 40) || M * K > ((int64_t)1 << 40))
-        return SWIGLU_ERR_BAD_SHAPE;
-    if ((K % 8) != 0 || (N % 8) != 0) return SWIGLU_ERR_UNSUPPORTED_SHAPE;
-    if (K > kMaxK) return SWIGLU_ERR_UNSUPPORTED_SHAPE;
-    return SWIGLU_OK;
 }
 
 // The streaming kernel keeps each activation address as a 32-bit byte offset
@@ -89,8 +58,6 @@ int64_t balanced_chunk(int64_t M, int64_t limit) {
     const int64_t per = (M + n - 1) / n;
     return std::min(limit, (per + 255) / 256 * 256);
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // FP8 operands: K a multiple of 16 (16-byte activation rows), packed weights
 // in 32 KiB blocks per (128 columns, 128 k)
@@ -113,23 +80,6 @@ int64_t gemm_packed_elems(int64_t K, int64_t N) {
     return ceil_div(N, swk::PACK_ROWS) * ceil_div(K, swk::PACK_BK) * swk::PACK_ROWS * swk::PACK_BK;
 }
 int64_t gemm_tiled_cols(int64_t N) { return ceil_div(N, swk::PACK_ROWS) * swk::PACK_BN; }
-
-// ---------------------------------------------------------------------------
-// device facts
-// ---------------------------------------------------------------------------
-int cu_count_now() {
-    static std::mutex mu;
-    static int cache[64] = {0};
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess) return 0;
-        cache[dev] = n;
-    }
-    return cache[dev];
-}
 
 // Device address of `scratch` on the current device: looked up once per
 // device (with that device current) and kept; each device holds its own copy

@@ -1,0 +1,440 @@
+// Device kernels of the gated MLP's training entry points (swiglu_train_*,
+// swiglu_mlp_train_backward).
+//
+// With G = A W1, U = A W2, s = 1 / (1 + e^-G), h = G s and Y = h U, a gradient dY
+// gives
+//     dU = dY h,   dG = dY U s (1 + G (1 - s)),
+//     dA = dG W1^T + dU W2^T,   dW1 = A^T dG,   dW2 = A^T dU,
+// and for the whole block Z = Y W3:  dY = dZ W3^T,  dW3 = Y^T dZ.
+//
+// All of them are products C[i][j] = sum_k a(i, k) b(j, k) on one tile kernel
+// (tile_gemm_kernel): each operand lies in memory either with k contiguous
+// (OP_KC: element (i, k) at i * ld + k) or with k strided (OP_KS: at k * ld + i),
+// and no operand is transposed through memory: a k-contiguous tile is read from
+// LDS as it is, a k-strided one with the transposing LDS read.
+//
+//   product          i (rows)   j (columns)     k          a    b
+//   G, U             token      W1 | W2 column  K          KC   KS, dual
+//   dA               token      K               N, then N  KC   KC, two segments
+//   dW1 | dW2        K          [dG | dU] col.  token      KS   KS
+//   dY -> dG, dU     token      N               K          KC   KC
+//   dW3              N          K               token      KS   KS
+//
+// D = [dG | dU] ([M][2N]) is the one intermediate in memory.  It is rounded to
+// bf16 because the matrix cores take bf16: each element is then off by at most
+// 2^-8 of itself, independently, and the sums over N or M terms that consume it
+// are formed in fp32, so dA and the weight gradients move by less than their own
+// rounding to bf16 does.  dY (block) and the recomputed G and U stay in fp32
+// from their sums to dG and dU.
+#pragma once
+
+#include "device_common.hpp"
+
+#include <type_traits>
+
+namespace swt {
+
+using namespace swk;
+
+// 16 zero bytes that lanes past the end of a contraction read
+__device__ __attribute__((aligned(16))) uint16_t g_zeros[8];
+
+enum Operand : int { OP_KC = 0, OP_KS = 1 };
+
+// What becomes of the sums of 8 adjacent columns (x; dual products: x the G
+// sums and y the U sums of the same columns).
+enum Epilogue : int {
+    EP_STORE = 0,   // C0 (columns < n0_cols) or C1, bf16
+    EP_KEEP = 1,    // dual: Y = SiLU(x) y, G = x, U = y
+    EP_DUAL_D = 2,  // dual: D from dY and the recomputed G = x, U = y
+    EP_DY_D = 3     // x = dY: D from it and the kept G and U
+};
+
+struct GemmArgs {
+    const uint16_t* A0;    // operand a; segment 1 from A1
+    const uint16_t* A1;
+    const uint16_t* B0;    // operand b; segment 1, or the dual product's second half, from B1
+    const uint16_t* B1;
+    long long lda, ldb;    // leading dimensions (elements)
+    int rows, cols;        // output rows and columns (dual: columns of each half)
+    int kseg;              // contraction length of one segment
+    int segs;              // 1 or 2
+    int kb_seg;            // ceil(kseg / 64)
+    int tiles_m, tiles_n;
+    int splits, kb_per_split;   // contraction blocks (over both segments) per split
+    float* part;           // split sums [split][rows][part_cols]
+    int part_cols;         // cols, or 2 cols for a dual product
+    // epilogue operands
+    uint16_t* C0;          // STORE: columns below n0_cols (row length ldc); KEEP: Y; D kinds: D
+    uint16_t* C1;          // STORE: the other columns; KEEP: G
+    uint16_t* C2;          // KEEP: U
+    const uint16_t* E0;    // DUAL_D: dY; DY_D: G
+    const uint16_t* E1;    // DY_D: U
+    int n0_cols, ldc;
+};
+
+// dG and dU of one element.  s (1 + g (1 - s)) is SiLU's derivative; at large
+// negative g, s is 0 and g (1 - s) finite, so the product is 0 as it should be.
+__device__ __forceinline__ void silu_grad(float dy, float g, float u, float& dg, float& du) {
+    const float e = __builtin_amdgcn_exp2f(-g * LOG2E);
+    const float s = __builtin_amdgcn_rcpf(1.0f + e);
+    du = dy * (g * s);
+    dg = dy * u * (s * (1.0f + g * (1.0f - s)));
+}
+
+__device__ __forceinline__ void unpack8(u32x4 v, float (&f)[8]) {
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        f[2 * d] = __builtin_bit_cast(float, v[d] << 16);
+        f[2 * d + 1] = __builtin_bit_cast(float, v[d] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
+    return u32x4{pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7])};
+}
+
+__device__ __forceinline__ void st16(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4*>(p) = v; }
+
+// The epilogue of columns n .. n + 7 of row m (both in range; n a multiple of 8,
+// and every width too, so 8 columns never straddle a matrix's edge).
+template <int EPI>
+__device__ __forceinline__ void finish8(const GemmArgs& p, int m, int n, const float (&x)[8], const float (&y)[8]) {
+    if constexpr (EPI == EP_STORE) {
+        uint16_t* c = n < p.n0_cols ? p.C0 + (size_t)m * p.ldc + n : p.C1 + (size_t)m * p.ldc + (n - p.n0_cols);
+        st16(c, pack8(x));
+    } else if constexpr (EPI == EP_KEEP) {
+        const size_t at = (size_t)m * p.cols + n;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = silu_f(x[e]) * y[e];
+        st16(p.C0 + at, pack8(v));
+        st16(p.C1 + at, pack8(x));
+        st16(p.C2 + at, pack8(y));
+    } else {
+        const size_t at = (size_t)m * p.cols + n;
+        float e0[8], dg[8], du[8];
+        unpack8(ld16(p.E0 + at), e0);
+        if constexpr (EPI == EP_DUAL_D) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) silu_grad(e0[e], x[e], y[e], dg[e], du[e]);
+        } else {
+            float e1[8];
+            unpack8(ld16(p.E1 + at), e1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) silu_grad(x[e], e0[e], e1[e], dg[e], du[e]);
+        }
+        uint16_t* d = p.C0 + (size_t)m * 2 * p.cols + n;
+        st16(d, pack8(dg));
+        st16(d + p.cols, pack8(du));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One BM x BN tile of sums per workgroup of WM x WN waves (DUAL: BN / 2 columns
+// of each half).  Each wave owns BM/WM x BN/WN of it as 32 x 32 MFMA blocks.
+//   Stages of 64 k, both operands direct to LDS, two stages: the next stage's
+//   loads go out at the start of a stage and have three of its four 16-deep
+//   sub-steps to land; the one barrier per stage sits before the last sub-step,
+//   whose fragments are in registers by then.
+//   Rows or columns past the edge repeat the last ones (their sums are not
+//   stored); k past the end reads the zero chunk in both operands, so nothing
+//   behind a row's end is ever multiplied (RAGGED; only compiled in when the
+//   contraction is not a multiple of 64).
+//   The sums leave through LDS in fp32, so the epilogue works on 8 adjacent
+//   columns a lane: its reads (dY, G, U) and its stores are 16 bytes a lane over
+//   whole row segments.
+// ---------------------------------------------------------------------------
+template <int BM, int BN, int WM, int WN>
+constexpr int tile_smem_bytes() {
+    constexpr int stages = 2 * (BM + BN) * BK * 2;
+    constexpr int rpp = BM / WM >= 64 ? 64 : BM / WM;
+    constexpr int stage_f = WM * WN * rpp * (BN / WN + 4) * 4;
+    return stages > stage_f ? stages : stage_f;
+}
+
+template <int BM, int BN, int WM, int WN, int AOP, int BOP, bool DUAL, int EPI, bool RAGGED>
+__global__ __launch_bounds__(64 * WM * WN) void tile_gemm_kernel(GemmArgs p) {
+    constexpr int NW = WM * WN;
+    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+    constexpr int A_INS = BM / 8 / NW, B_INS = BN / 8 / NW;   // 1 KiB direct loads per wave per stage
+    constexpr int STAGE = (BM + BN) * BK;
+    constexpr int GROUP_M = 8;
+    static_assert(TM >= 1 && TN >= 1 && (!DUAL || TN % 2 == 0), "wave tile");
+    static_assert(AOP == OP_KC || BM >= 128, "a k-strided tile has rows of at least 128 elements");
+    static_assert(BOP == OP_KC || BN >= 128, "a k-strided tile has rows of at least 128 elements");
+    __shared__ __attribute__((aligned(16))) unsigned char smem_raw[tile_smem_bytes<BM, BN, WM, WN>()];
+    uint16_t* const smem = reinterpret_cast<uint16_t*>(smem_raw);
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+
+    // logical id -> (tile, split); a tile's splits are consecutive, so they stay
+    // on one XCD, and tiles go down GROUP_M row tiles before the next column
+    const int logical = xcd_remap(blockIdx.x, gridDim.x);
+    const int tile = logical / p.splits;
+    const int split = logical - tile * p.splits;
+    int tm, tn;
+    {
+        const int per_group = GROUP_M * p.tiles_n;
+        const int group = tile / per_group;
+        const int first_m = group * GROUP_M;
+        const int gsize = min(p.tiles_m - first_m, GROUP_M);
+        const int in_group = tile - group * per_group;
+        tm = first_m + in_group % gsize;
+        tn = in_group / gsize;
+    }
+    const int m0 = tm * BM;
+    const int n0 = tn * (DUAL ? BN / 2 : BN);
+    const int s_first = split * p.kb_per_split;
+    const int s_end = min(p.segs * p.kb_seg, s_first + p.kb_per_split);   // the host makes no empty split
+
+    // per-lane byte offsets from the stage's base, constant over the stages:
+    // k-contiguous operand: 8 rows x 128 bytes a load, chunks swizzled by row;
+    // k-strided: whole k rows of the tile's columns, chunks swizzled by k
+    uint32_t a_off[A_INS], b_off[B_INS];
+    int a_k[A_INS], b_k[B_INS];   // RAGGED: the load's (first) k within the stage
+#pragma unroll
+    for (int i = 0; i < A_INS; ++i) {
+        const int q = wave * A_INS + i;
+        if constexpr (AOP == OP_KC) {
+            const int r = q * 8 + (lane >> 3), c = (lane & 7) ^ swz(r);
+            a_off[i] = (uint32_t)((min(m0 + r, p.rows - 1) - m0) * p.lda + 8 * c) * 2;
+            a_k[i] = 8 * c;
+        } else {
+            constexpr int CPR = BM / 8, RPI = 64 / CPR;
+            const int r = q * RPI + lane / CPR, c = 8 * ((lane % CPR) ^ ((r & 3) << 2));
+            a_off[i] = (uint32_t)(r * p.lda + min(m0 + c, p.rows - 8) - m0) * 2;
+            a_k[i] = r;
+        }
+    }
+    const uint16_t* b_half[B_INS];   // dual: which half's matrix a load reads
+#pragma unroll
+    for (int i = 0; i < B_INS; ++i) {
+        const int q = wave * B_INS + i;
+        b_half[i] = p.B0;
+        if constexpr (BOP == OP_KC) {
+            const int r = q * 8 + (lane >> 3), c = (lane & 7) ^ swz(r);
+            b_off[i] = (uint32_t)((min(n0 + r, p.cols - 1) - n0) * p.ldb + 8 * c) * 2;
+            b_k[i] = 8 * c;
+        } else {
+            constexpr int CPR = BN / 8, RPI = 64 / CPR;
+            const int r = q * RPI + lane / CPR, c = 8 * ((lane % CPR) ^ ((r & 3) << 2));
+            const bool up = DUAL && c >= BN / 2;
+            const int cc = up ? c - BN / 2 : c;
+            b_off[i] = (uint32_t)(r * p.ldb + min(n0 + cc, p.cols - 8) - n0) * 2;
+            b_k[i] = r;
+            if (up) b_half[i] = p.B1;
+        }
+    }
+
+    auto issue = [&](int s, int buf) {
+        uint16_t* sA = smem + buf * STAGE;
+        uint16_t* sB = sA + BM * BK;
+        const int seg = s >= p.kb_seg ? 1 : 0;
+        const int k0 = (s - seg * p.kb_seg) * BK;
+        const int left = p.kseg - k0;   // k left in the segment, > 0
+        const char* a_base = reinterpret_cast<const char*>(
+            (seg ? p.A1 : p.A0) + (AOP == OP_KC ? (size_t)m0 * p.lda + k0 : (size_t)k0 * p.lda + m0));
+        const size_t b_at = BOP == OP_KC ? (size_t)n0 * p.ldb + k0 : (size_t)k0 * p.ldb + n0;
+#pragma unroll
+        for (int i = 0; i < A_INS; ++i) {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(a_base + a_off[i]);
+            if constexpr (RAGGED) {
+                if (a_k[i] >= left) src = g_zeros;
+            }
+            dma16(src, sA + (wave * A_INS + i) * 512);
+        }
+#pragma unroll
+        for (int i = 0; i < B_INS; ++i) {
+            const uint16_t* base = DUAL ? b_half[i] : (seg ? p.B1 : p.B0);
+            const uint16_t* src =
+                reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base + b_at) + b_off[i]);
+            if constexpr (RAGGED) {
+                if (b_k[i] >= left) src = g_zeros;
+            }
+            dma16(src, sB + (wave * B_INS + i) * 512);
+        }
+    };
+
+    f32x16 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    // fragments: lane l holds row (l & 31) of the block and the 8 k from
+    // 16kk + 8(l >> 5); the transposing read takes two reads of 4 k each
+    bf16x8 fa[2][TM], fb[2][TN];
+    const int tr_k = 8 * (lane >> 5) + ((lane & 15) >> 2);
+    const int tr_c = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    auto frag = [&](auto opc, auto widthc, const uint16_t* s, int row, int kk) -> bf16x8 {
+        constexpr int OP = decltype(opc)::value;
+        constexpr int W = decltype(widthc)::value;
+        if constexpr (OP == OP_KC) {
+            return *reinterpret_cast<const bf16x8*>(s + lds_off(row + (lane & 31), 2 * kk + (lane >> 5)));
+        } else {
+            const s16x4 both[2] = {ds_read_tr16(s + rm_off<W>(16 * kk + tr_k, row + tr_c)),
+                                   ds_read_tr16(s + rm_off<W>(16 * kk + tr_k + 4, row + tr_c))};
+            return __builtin_bit_cast(bf16x8, both);
+        }
+    };
+    auto read_frags = [&](int buf, int kk, int set) {
+        const uint16_t* sA = smem + buf * STAGE;
+        const uint16_t* sB = sA + BM * BK;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            fa[set][i] = frag(std::integral_constant<int, AOP>{}, std::integral_constant<int, BM>{}, sA,
+                              wm * (BM / WM) + i * 32, kk);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int col = DUAL ? (j >= TN / 2 ? BN / 2 : 0) + wn * (BN / WN / 2) + (j % (TN / 2 > 0 ? TN / 2 : 1)) * 32
+                                 : wn * (BN / WN) + j * 32;
+            fb[set][j] =
+                frag(std::integral_constant<int, BOP>{}, std::integral_constant<int, BN>{}, sB, col, kk);
+        }
+    };
+    auto mfmas = [&](int set) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+    };
+
+    issue(s_first, 0);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    read_frags(0, 0, 0);
+    for (int s = s_first; s < s_end; ++s) {
+        const int buf = (s - s_first) & 1;
+        const bool more = s + 1 < s_end;
+        if (more) issue(s + 1, buf ^ 1);
+        read_frags(buf, 1, 1);
+        mfmas(0);
+        read_frags(buf, 2, 0);
+        mfmas(1);
+        read_frags(buf, 3, 1);
+        mfmas(0);
+        // the next stage has landed and every wave has read this one
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (more) read_frags(buf ^ 1, 0, 0);
+        mfmas(1);
+    }
+
+    // ---- the sums through LDS (fp32), 8 adjacent columns a lane ------------------
+    constexpr int CW = BN / WN;                         // staged columns per wave (dual: G half, then U half)
+    constexpr int PW = CW + 4;                          // pitch: 16 bytes of padding per row
+    constexpr int RPP = BM / WM >= 64 ? 64 : BM / WM;   // rows per pass
+    constexpr int OW = DUAL ? CW / 2 : CW;              // output columns per wave
+    constexpr int LPR = OW / 8;                         // lanes per row
+    constexpr int RPI = 64 / LPR;                       // rows per wave step
+    float* const st = reinterpret_cast<float*>(smem_raw) + wave * RPP * PW;
+    const int row_base = m0 + wm * (BM / WM);
+    const int col_base = n0 + wn * OW;
+#pragma unroll
+    for (int ps = 0; ps < BM / WM / RPP; ++ps) {
+        __syncthreads();
+#pragma unroll
+        for (int ii = 0; ii < RPP / 32; ++ii)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16& a = acc[ps * (RPP / 32) + ii][j];
+                    *reinterpret_cast<f32x4*>(st + (ii * 32 + (lane & 31)) * PW + j * 32 + 8 * q + 4 * (lane >> 5)) =
+                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+                }
+        __syncthreads();
+        for (int t = 0; t < RPP / RPI; ++t) {
+            const int r = t * RPI + lane / LPR, c = 8 * (lane % LPR);
+            const int m = row_base + ps * RPP + r, n = col_base + c;
+            float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(st + r * PW + c + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+                if constexpr (DUAL) {
+                    const f32x4 w = *reinterpret_cast<const f32x4*>(st + r * PW + OW + c + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[4 * h + e] = w[e];
+                }
+            }
+            if (m < p.rows && n < p.cols) {
+                if (p.splits > 1) {
+                    float* d = p.part + ((size_t)split * p.rows + m) * p.part_cols + n;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        *reinterpret_cast<f32x4*>(d + 4 * h) = f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+                        if constexpr (DUAL)
+                            *reinterpret_cast<f32x4*>(d + p.cols + 4 * h) =
+                                f32x4{y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]};
+                    }
+                } else {
+                    finish8<EPI>(p, m, n, x, y);
+                }
+            }
+        }
+    }
+}
+
+// The splits' sums of 8 adjacent columns, added in split order 0 .. splits - 1
+// (the same result whatever workgroup finished first), then the epilogue.
+template <bool DUAL, int EPI>
+__global__ __launch_bounds__(256) void tile_reduce_kernel(GemmArgs p) {
+    const long long groups = (long long)p.rows * (p.cols / 8);
+    const size_t stride = (size_t)p.rows * p.part_cols;
+    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < groups; t += (long long)gridDim.x * 256) {
+        const int m = (int)(t / (p.cols / 8)), n = (int)(t % (p.cols / 8)) * 8;
+        const float* src = p.part + (size_t)m * p.part_cols + n;
+        float x[8] = {}, y[8] = {};
+        for (int s = 0; s < p.splits; ++s, src += stride) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4 * h);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[4 * h + e] += v[e];
+                if constexpr (DUAL) {
+                    const f32x4 w = *reinterpret_cast<const f32x4*>(src + p.cols + 4 * h);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[4 * h + e] += w[e];
+                }
+            }
+        }
+        finish8<EPI>(p, m, n, x, y);
+    }
+}
+
+// D = [dG | dU] from dY and the kept G and U, 8 elements a thread.
+__global__ __launch_bounds__(256) void dgate_kernel(const uint16_t* __restrict__ dY, const uint16_t* __restrict__ G,
+                                                    const uint16_t* __restrict__ U, uint16_t* __restrict__ D, int N,
+                                                    long long groups) {
+    const int per_row = N / 8;
+    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < groups; t += (long long)gridDim.x * 256) {
+        const long long m = t / per_row;
+        const int n = (int)(t - m * per_row) * 8;
+        float dy[8], g[8], u[8], dg[8], du[8];
+        unpack8(ld16(dY + t * 8), dy);
+        unpack8(ld16(G + t * 8), g);
+        unpack8(ld16(U + t * 8), u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) silu_grad(dy[e], g[e], u[e], dg[e], du[e]);
+        uint16_t* d = D + (size_t)m * 2 * N + n;
+        st16(d, pack8(dg));
+        st16(d + N, pack8(du));
+    }
+}
+
+// Zeros (weight gradients of an empty batch); count in 16-byte pieces.
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t* __restrict__ p, long long count) {
+    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < count; t += (long long)gridDim.x * 256)
+        st16(p + t * 8, u32x4{0u, 0u, 0u, 0u});
+}
+
+}  // namespace swt
