@@ -484,6 +484,70 @@ swiglu_status swiglu_mlp_train_backward(
     swiglu_bf16 *dW1, swiglu_bf16 *dW2, swiglu_bf16 *dW3, int64_t M, int64_t K,
     int64_t N, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside the packed products.  Row m of a
+ * batch has adapter i = ids[m]; ids outside 0 .. adapters - 1 (-1 by
+ * convention) have none.  An adapter adds a rank-`rank` product to a projection:
+ *     A W  becomes  A W + scales[i] (A La_i) Lb_i,
+ * for the gated product in both projections, before SiLU:
+ *     G = A W1 + scales[i] (A La1_i) Lb1_i,  U = A W2 + scales[i] (A La2_i) Lb2_i,
+ *     Y = SiLU(G) U.
+ * La [adapters,K,rank] and Lb [adapters,rank,N] bf16; adapters of smaller rank
+ * are padded with zeros by the caller.  The sums stay in fp32 to the one
+ * rounding of the output; the factor A La_i is held to 2^-17.  Rows' adapters
+ * may come in any order; rows of one request next to each other are fastest.
+ * A row's result depends on its own row of A and its own adapter alone:
+ * infinities and NaN in another request's rows or adapter do not reach it.
+ *
+ * swiglu_lora_packed_bytes / swiglu_gemm_lora_packed_bytes: size of the packed
+ *   adapters Lp of the gated product / of one projection (0 if invalid).
+ * swiglu_lora_pack / swiglu_gemm_lora_pack: the adapters into Lp, once, when
+ *   they are loaded (K and N are those of the projection's weight).
+ * swiglu_lora_workspace_bytes / swiglu_gemm_lora_workspace_bytes: workspace of
+ *   a call (the factors, and fp32 sums where the schedule splits K); never 0
+ *   for a valid shape with M > 0.
+ * swiglu_fused_packed_lora: Y [M,N] from A [M,K], the packed weights Wp of
+ *   swiglu_pack_weights and Lp, on the schedule that swiglu_fused_packed's AUTO
+ *   picks.
+ * swiglu_gemm_packed_lora: C [M,N] = A W + adapters, W [K,N] in the single-weight
+ *   pack of swiglu_gemm_pack_weight, on the schedule of swiglu_gemm_packed with
+ *   a workspace.
+ * All: K and N multiples of 8, adapters >= 1, 1 <= rank <= 256 (above:
+ * ERR_UNSUPPORTED_SHAPE), adapters * (K + N) at most 2^31; ids int32 and scales
+ * fp32 (device, 4-byte aligned; read when the call's kernels run), other
+ * pointers 16-byte aligned; the output and the workspace overlap nothing;
+ * calls that may run concurrently must not share a workspace.  M == 0 returns
+ * SWIGLU_OK without a launch.
+ * ---------------------------------------------------------------------- */
+size_t swiglu_lora_packed_bytes(int64_t K, int64_t N, int64_t adapters,
+                                int64_t rank);
+size_t swiglu_gemm_lora_packed_bytes(int64_t K, int64_t N, int64_t adapters,
+                                     int64_t rank);
+swiglu_status swiglu_lora_pack(const swiglu_bf16 *La1, const swiglu_bf16 *Lb1,
+                               const swiglu_bf16 *La2, const swiglu_bf16 *Lb2,
+                               swiglu_bf16 *Lp, int64_t K, int64_t N,
+                               int64_t adapters, int64_t rank, void *stream);
+swiglu_status swiglu_gemm_lora_pack(const swiglu_bf16 *La, const swiglu_bf16 *Lb,
+                                    swiglu_bf16 *Lp, int64_t K, int64_t N,
+                                    int64_t adapters, int64_t rank, void *stream);
+size_t swiglu_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank);
+size_t swiglu_gemm_lora_workspace_bytes(int64_t M, int64_t K, int64_t N,
+                                        int64_t rank);
+swiglu_status swiglu_fused_packed_lora(const swiglu_bf16 *A, const swiglu_bf16 *Wp,
+                                       const swiglu_bf16 *Lp, const int32_t *ids,
+                                       const float *scales, swiglu_bf16 *Y,
+                                       int64_t M, int64_t K, int64_t N,
+                                       int64_t adapters, int64_t rank,
+                                       void *workspace, size_t workspace_bytes,
+                                       void *stream);
+swiglu_status swiglu_gemm_packed_lora(const swiglu_bf16 *A, const swiglu_bf16 *Wg,
+                                      const swiglu_bf16 *Lp, const int32_t *ids,
+                                      const float *scales, swiglu_bf16 *C,
+                                      int64_t M, int64_t K, int64_t N,
+                                      int64_t adapters, int64_t rank,
+                                      void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
 #ifdef __cplusplus
 }
 #endif

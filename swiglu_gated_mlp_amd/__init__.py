@@ -72,6 +72,14 @@ SIGNATURES = {
     "swiglu_train_forward": ([_P] * 6 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "swiglu_train_backward": ([_P] * 9 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "swiglu_mlp_train_backward": ([_P] * 12 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_lora_packed_bytes": ([_I64] * 4, ctypes.c_size_t),
+    "swiglu_gemm_lora_packed_bytes": ([_I64] * 4, ctypes.c_size_t),
+    "swiglu_lora_pack": ([_P] * 5 + [_I64] * 4 + [_P], ctypes.c_int),
+    "swiglu_gemm_lora_pack": ([_P] * 3 + [_I64] * 4 + [_P], ctypes.c_int),
+    "swiglu_lora_workspace_bytes": ([_I64] * 4, ctypes.c_size_t),
+    "swiglu_gemm_lora_workspace_bytes": ([_I64] * 4, ctypes.c_size_t),
+    "swiglu_fused_packed_lora": ([_P] * 6 + [_I64] * 5 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_gemm_packed_lora": ([_P] * 6 + [_I64] * 5 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
     # include/swiglu_probe.h (diagnostic ceilings)
     "swiglu_probe_mfma": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_read": ([_P, ctypes.c_size_t, _P, ctypes.c_int, _P], ctypes.c_int),
@@ -380,6 +388,24 @@ def _resolve_workspace(workspace, need: int, device: torch.device, s: int):
     return ws, (0 if ws is None else ws.numel() * ws.element_size())
 
 
+def _new(shape, device, s: int) -> torch.Tensor:
+    """An uninitialised bf16 output, allocated on the stream that writes it."""
+    if s == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=device)):
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+
+
+def _scratch(workspace, need: int, device, s: int):
+    """As _resolve_workspace; a call under graph capture without a workspace of
+    its own gets a buffer of the graph's pool, so that no buffer that a graph
+    writes on replay is handed to another call."""
+    if workspace is None and need and torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws, need
+    return _resolve_workspace(workspace, need, device, s)
+
+
 def swiglu_choose_variant(M: int, K: int, N: int) -> int:
     return int(lib().swiglu_choose_variant(M, K, N))
 
@@ -665,3 +691,8 @@ def swiglu_probe_read(src: torch.Tensor, sink: torch.Tensor, blocks: int, stream
 # training (gradients and differentiable forms of the product and the block)
 from .train import (swiglu, swiglu_mlp, swiglu_mlp_train_backward, swiglu_train_backward,  # noqa: E402,F401
                     swiglu_train_forward, swiglu_train_forward_workspace_bytes, swiglu_train_workspace_bytes)
+
+# low-rank adapters of many requests beside the packed products
+from .lora import (swiglu_fused_packed_lora, swiglu_gemm_lora_pack, swiglu_gemm_lora_packed_bytes,  # noqa: E402,F401
+                   swiglu_gemm_lora_workspace_bytes, swiglu_gemm_packed_lora, swiglu_lora_pack,
+                   swiglu_lora_packed_bytes, swiglu_lora_workspace_bytes)

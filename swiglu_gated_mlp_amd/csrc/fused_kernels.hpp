@@ -32,6 +32,7 @@
 #pragma once
 
 #include "device_common.hpp"
+#include "lora_device.hpp"
 
 #include <type_traits>
 
@@ -861,10 +862,13 @@ constexpr int stream_smem_elems() {
 // half, one accumulator set -- so the units are twice the fused product's
 // panels and the CUs share them as evenly (p.panels counts half-panels; the
 // single Y-tile pass maps each wave's 32 columns to its half).
+// LORA: each row's low-rank adapter (la) is added to the sums in the epilogue
+// (lora_block).
 template <int BM, bool SPLIT, bool RAGGED, bool PANELS = false, bool IL = false, bool F8 = false,
-          bool SEQ = false, bool GEMM = false>
+          bool SEQ = false, bool GEMM = false, bool LORA = false>
 __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_t* smem, int first, int stride,
-                                                     int total) {
+                                                     int total, const LoraArgs* la = nullptr) {
+    static_assert(!(LORA && (SPLIT || IL || F8 || SEQ)), "adapters: bf16 per-tile or single-weight pack, whole K");
     static_assert(!(GEMM && (IL || F8 || SEQ)), "plain GEMM: bf16 single-weight pack");
     static_assert(!(IL && SPLIT), "the interleaved layout has no split-K schedule");
     static_assert(!(F8 && (IL || SPLIT)), "FP8 operands: per-tile layout, data-parallel only");
@@ -1328,11 +1332,30 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
         int el = lane;
         asm volatile("" : "+v"(el));
         __builtin_amdgcn_sched_barrier(0);
+        // LORA: row i*32 + (l & 31)'s adapter (-1: none, or no row), and the
+        // output's 32-column tile of accumulator half h (waves without a panel
+        // have none: their rows count as without adapter)
+        auto lora_row = [&](int i) {
+            const int m = cur.m0 + i * 32 + (el & 31);
+            return m < M && (!PANELS || wave < cur.np) ? lora_id(*la, m) : -1;
+        };
+        auto lora_tile = [&](int h) {
+            const int u = cur.n0 / 32 + wave;
+            if constexpr (!GEMM) return u;
+            const int tc = GH ? (u >> 1) * 32 : u * 32;   // tiled column
+            return ((tc >> 7) * PACK_ROWS + PACK_BN * (GH ? (u & 1) : h) + (tc & (PACK_BN - 1))) / 32;
+        };
         // GEMM pass gh: bf16 of accumulator set gh (no SiLU) into the Y tile
         auto fill_gemm = [&](int gh) {
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int r = i * 32 + (el & 31);
+                if constexpr (LORA) {
+                    f32x16 d[1];
+                    const int nt[1] = {lora_tile(gh)};
+                    lora_block<1, 1>(d, *la, lora_row(i), cur.m0 + r, nt, el);
+                    acc[gh][i][0] += d[0];
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     u32x2 out;
@@ -1366,12 +1389,21 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
                                                      4 * ((q & 1) ^ ((r >> 4) & 1)) + 2 * (el >> 5)) = out;
                     }
             } else {
+                f32x16 d[2];
+                if constexpr (LORA) {
+                    const int nt[2] = {lora_tile(0), lora_tile(1)};
+                    lora_block<2, 2>(d, *la, lora_row(i), cur.m0 + r, nt, el);
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float gv = acc[0][i][0][4 * q + e], uv = acc[1][i][0][4 * q + e];
+                        if constexpr (LORA) {
+                            gv += d[0][4 * q + e];
+                            uv += d[1][4 * q + e];
+                        }
                         if constexpr (F8) {
                             gv *= p.sg;
                             uv *= p.su;
@@ -1528,8 +1560,10 @@ struct DecodeArgs {
 // instruction; the 16-byte chunks of row r XOR-ed with r & 7) and reads the
 // MFMA fragments from there, instead of loading each fragment (16 rows x 64
 // bytes, half lines) from global memory.
-template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false>
-__global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p) {
+// Lora: LoraArgs, or nothing.  With it, each row's low-rank adapter is added to
+// the summed Gate and Up (or plain) values before the epilogue.
+template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false, class... Lora>
+__global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora) {
     static_assert(GEMM || !HALF, "HALF splits the single-weight product only");
     constexpr int WAVES = 4;
     constexpr int NH = HALF ? 1 : 2;    // weight halves per workgroup
@@ -1684,6 +1718,22 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p) {
         }
         const int m = t * 16 + r16;
         const int n = n0 + 16 * c + 4 * kq;
+        if constexpr (sizeof...(Lora) > 0) {
+            const LoraArgs& la = (lora, ...);
+            const int id = m < M ? lora_id(la, m) : -1;
+            if (id >= 0) {
+                if constexpr (GEMM) {
+                    const int col = (n / PACK_BN) * PACK_ROWS + n % PACK_BN + (HALF ? PACK_BN * half : 0);
+                    if (col < N) g += lora_delta4<1>(la, m, id, 0, col);
+                    if constexpr (!HALF) {
+                        if (col + PACK_BN < N) u += lora_delta4<1>(la, m, id, 0, col + PACK_BN);
+                    }
+                } else if (n < N) {
+                    g += lora_delta4<2>(la, m, id, 0, n);
+                    u += lora_delta4<2>(la, m, id, 1, n);
+                }
+            }
+        }
         if constexpr (HALF) {
             const int col = (n / PACK_BN) * PACK_ROWS + n % PACK_BN + PACK_BN * half;
             if (m < M && col < N) {

@@ -17,6 +17,7 @@
 
 #include "fused_kernels.hpp"
 #include "host_common.hpp"
+#include "lora_kernels.hpp"
 #include "probe_kernels.hpp"
 
 // Device scratch of swiglu_fused_packed_noalloc: the split-K partial sums of
@@ -246,11 +247,15 @@ hipError_t launch_tile(const swk::FusedArgs& a, int grid, hipStream_t s) {
 // n_tiled: the packed weights' output columns (N for the fused product; 128
 // per packed tile for the single-weight GEMM).  HALF: one workgroup per
 // (column groups, weight half), twice the grid.
+// la: low-rank adapters (NULL: none).
 template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false>
-hipError_t launch_decode(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA>);
+hipError_t launch_decode(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t s, const swk::LoraArgs* la) {
+    void (*plain)(swk::DecodeArgs) = &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA>;
+    void (*adapted)(swk::DecodeArgs, swk::LoraArgs) = &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA, swk::LoraArgs>;
+    const void* fn = la ? reinterpret_cast<const void*>(adapted) : reinterpret_cast<const void*>(plain);
     swk::DecodeArgs args = a;
-    void* kargs[] = {&args};
+    swk::LoraArgs lora = la ? *la : swk::LoraArgs{};
+    void* kargs[] = {&args, &lora};
     return hipLaunchKernel(fn, dim3((unsigned)(ceil_div(n_tiled, 16 * CG) * (HALF ? 2 : 1))), dim3(256), kargs, 0,
                            s);
 }
@@ -267,8 +272,19 @@ hipError_t launch_prefill(const swk::FusedArgs& a, int grid, hipStream_t s) {
 // each workgroup takes items b, b + grid, ...
 template <int BM, bool SPLIT, bool PANELS = false, bool IL = false, bool F8 = false, bool SEQ = false,
           bool GEMM = false>
-hipError_t launch_stream(const swk::FusedArgs& a, int total, int grid, hipStream_t s) {
+hipError_t launch_stream(const swk::FusedArgs& a, int total, int grid, hipStream_t s,
+                         const swk::LoraArgs* la = nullptr) {
     const bool ragged = (a.K % (F8 ? 128 : swk::BK)) != 0;
+    if constexpr (!SPLIT && !IL && !F8 && !SEQ) {
+        if (la) {
+            const void* fn = ragged ? reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, true, PANELS, GEMM>)
+                                    : reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, false, PANELS, GEMM>);
+            swk::FusedArgs args = a;
+            swk::LoraArgs lora = *la;
+            void* kargs[] = {&args, &lora, &total};
+            return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, 0, s);
+        }
+    }
     const void* fn =
         ragged ? reinterpret_cast<const void*>(&swk::stream_prefill_kernel<BM, SPLIT, true, PANELS, IL, F8, SEQ, GEMM>)
                : reinterpret_cast<const void*>(&swk::stream_prefill_kernel<BM, SPLIT, false, PANELS, IL, F8, SEQ, GEMM>);
@@ -281,7 +297,8 @@ hipError_t launch_stream(const swk::FusedArgs& a, int total, int grid, hipStream
 // schedule, the mixed 256/128-row launch) on either weight layout; SEQ: the
 // sequential Gate-then-Up order (per-tile layout, no panel schedule).
 template <bool IL, bool F8 = false, bool SEQ = false, bool GEMM = false>
-hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t s) {
+hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t s,
+                            const swk::LoraArgs* la = nullptr) {
     const int grid = p.tiles;
     if (p.t.BM == 128) {
         if constexpr (SEQ) return launch_stream<128, false, false, false, false, true>(a, grid, grid, s);
@@ -298,7 +315,7 @@ hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t 
                 pa.tiles_m = 1;
                 pa.panels = 4 * p.tiles_n;
                 const int g = std::min(pa.panels, p.cus);
-                return launch_stream<256, false, true, IL, F8, false, false>(pa, g, g, s);
+                return launch_stream<256, false, true, IL, F8, false, false>(pa, g, g, s, la);
             }
         }
         if (p.panels > 0) {
@@ -308,14 +325,14 @@ hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t 
             pa.panels = GEMM ? 2 * p.panels : p.panels;
             if (pa.panels <= 4 * p.cus) {
                 const int g = std::min(pa.panels, p.cus);
-                return launch_stream<128, false, true, IL, F8, false, GEMM>(pa, g, g, s);
+                return launch_stream<128, false, true, IL, F8, false, GEMM>(pa, g, g, s, la);
             }
         }
-        return launch_stream<128, false, false, IL, F8, false, GEMM>(a, grid, grid, s);
+        return launch_stream<128, false, false, IL, F8, false, GEMM>(a, grid, grid, s, la);
     }
     // one workgroup per CU works through the 256-row tiles
     if (p.tail_ntiles == 0)
-        return launch_stream<256, false, false, IL, F8, SEQ, GEMM>(a, grid, std::min(grid, p.cus), s);
+        return launch_stream<256, false, false, IL, F8, SEQ, GEMM>(a, grid, std::min(grid, p.cus), s, la);
     // one launch: the 256-row tiles of the first column tiles, then
     // the last tail_ntiles column tiles as 128-row tiles
     swk::FusedArgs big = a, tail = a;
@@ -327,6 +344,15 @@ hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t 
     int n_pers = std::min(n_big, p.cus);
     const int grid_all = n_pers + tail.tiles_m * tail.tiles_n;
     const bool ragged = (a.K % (F8 ? 128 : swk::BK)) != 0;
+    if constexpr (!IL && !F8 && !SEQ) {
+        if (la) {
+            const void* lfn = ragged ? reinterpret_cast<const void*>(&swk::stream_lora_mixed_kernel<true, GEMM>)
+                                     : reinterpret_cast<const void*>(&swk::stream_lora_mixed_kernel<false, GEMM>);
+            swk::LoraArgs lora = *la;
+            void* largs[] = {&big, &tail, &lora, &n_pers, &n_big};
+            return hipLaunchKernel(lfn, dim3(grid_all), dim3(256), largs, 0, s);
+        }
+    }
     const void* fn = ragged
                          ? reinterpret_cast<const void*>(&swk::stream_prefill_mixed_kernel<true, IL, F8, SEQ, GEMM>)
                          : reinterpret_cast<const void*>(&swk::stream_prefill_mixed_kernel<false, IL, F8, SEQ, GEMM>);
@@ -382,21 +408,22 @@ hipError_t launch_decode_fp8(const swk::FusedArgs& a, int cus, hipStream_t s) {
 //   K=3584 N=18944 M=16: <1,1,8,L> 44.1-44.4 against 45.9-46.3; M=1 / 4 / 8: no gain
 //   K=896 N=4864 M=64: <4,2,1,L> 9.33-9.38 against 9.82-9.90; M=32 with 8 groups: 55.6 against 52.0
 // n_tiled: the packed weights' output columns.
-hipError_t launch_decode_cfg(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s) {
+hipError_t launch_decode_cfg(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s,
+                             const swk::LoraArgs* la = nullptr) {
     const bool long_k = p.KB >= 96;
     const int64_t wg64 = ceil_div(n_tiled, 64), wg128 = ceil_div(n_tiled, 128);
     switch (p.decode_mt) {
         case 1:
-            if (long_k && 4 * wg128 >= 3 * p.cus) return launch_decode<1, 8, 2>(d, n_tiled, s);
-            return d.M > 8 ? launch_decode<1, 1, 8, false, false, true>(d, n_tiled, s)
-                           : launch_decode<1, 1, 8>(d, n_tiled, s);
+            if (long_k && 4 * wg128 >= 3 * p.cus) return launch_decode<1, 8, 2>(d, n_tiled, s, la);
+            return d.M > 8 ? launch_decode<1, 1, 8, false, false, true>(d, n_tiled, s, la)
+                           : launch_decode<1, 1, 8>(d, n_tiled, s, la);
         case 2:
-            if (2 * wg128 >= p.cus) return launch_decode<2, 8, 1>(d, n_tiled, s);
-            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<2, 4, 1>(d, n_tiled, s)
-                                                    : launch_decode<2, 2, 2>(d, n_tiled, s);
+            if (2 * wg128 >= p.cus) return launch_decode<2, 8, 1>(d, n_tiled, s, la);
+            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<2, 4, 1>(d, n_tiled, s, la)
+                                                    : launch_decode<2, 2, 2>(d, n_tiled, s, la);
         default:
-            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<4, 4, 1>(d, n_tiled, s)
-                                                    : launch_decode<4, 2, 1, false, false, true>(d, n_tiled, s);
+            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<4, 4, 1>(d, n_tiled, s, la)
+                                                    : launch_decode<4, 2, 1, false, false, true>(d, n_tiled, s, la);
     }
 }
 
@@ -421,24 +448,25 @@ hipError_t launch_decode_cfg(const swk::DecodeArgs& d, int64_t n_tiled, const Pl
 // i.e. halves whenever the whole-pair grid leaves CUs short of work, the
 // deepest per-wave prefetch the registers allow at one or two tokens' rows,
 // and staged activations for narrow groups from 9 rows on.
-hipError_t launch_decode_gemm(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s) {
+hipError_t launch_decode_gemm(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s,
+                             const swk::LoraArgs* la = nullptr) {
     const bool long_k = p.KB >= 96;
     const int64_t wg64 = ceil_div(n_tiled, 64);
     switch (p.decode_mt) {
         case 1:
-            if (long_k && 2 * wg64 >= p.cus) return launch_decode<1, 4, 4, true, true>(d, n_tiled, s);
-            if (d.M <= 8) return launch_decode<1, 1, 14, true, true>(d, n_tiled, s);
-            return launch_decode<1, 1, 8, true, true, true>(d, n_tiled, s);
+            if (long_k && 2 * wg64 >= p.cus) return launch_decode<1, 4, 4, true, true>(d, n_tiled, s, la);
+            if (d.M <= 8) return launch_decode<1, 1, 14, true, true>(d, n_tiled, s, la);
+            return launch_decode<1, 1, 8, true, true, true>(d, n_tiled, s, la);
         case 2:
             if (long_k) {
-                return 4 * wg64 >= 3 * p.cus ? launch_decode<2, 8, 1, true, true>(d, n_tiled, s)
-                                             : launch_decode<2, 2, 2, true, true>(d, n_tiled, s);
+                return 4 * wg64 >= 3 * p.cus ? launch_decode<2, 8, 1, true, true>(d, n_tiled, s, la)
+                                             : launch_decode<2, 2, 2, true, true>(d, n_tiled, s, la);
             }
-            return 2 * ceil_div(n_tiled, 128) >= p.cus ? launch_decode<2, 8, 1, true>(d, n_tiled, s)
-                                                       : launch_decode<2, 2, 2, true>(d, n_tiled, s);
+            return 2 * ceil_div(n_tiled, 128) >= p.cus ? launch_decode<2, 8, 1, true>(d, n_tiled, s, la)
+                                                       : launch_decode<2, 2, 2, true>(d, n_tiled, s, la);
         default:
-            if (long_k && 4 * wg64 >= 3 * p.cus) return launch_decode<4, 4, 1, true>(d, n_tiled, s);
-            return launch_decode<4, 1, 1, true, true, true>(d, n_tiled, s);
+            if (long_k && 4 * wg64 >= 3 * p.cus) return launch_decode<4, 4, 1, true>(d, n_tiled, s, la);
+            return launch_decode<4, 1, 1, true, true, true>(d, n_tiled, s, la);
     }
 }
 
@@ -1111,6 +1139,246 @@ swiglu_status swiglu_mlp_unfused(const swiglu_bf16* A, const swiglu_bf16* W1g, c
     st = swiglu_unfused_packed(A, W1g, W2g, G_scratch, U_scratch, Y, M, K, N, stream);
     if (st != SWIGLU_OK) return st;
     return swiglu_gemm_packed(Y, W3g, Z, M, N, K, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Low-rank adapters beside the packed products
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+constexpr int64_t kMaxRank = 256;
+
+swiglu_status check_lora(int64_t M, int64_t K, int64_t N, int64_t adapters, int64_t rank) {
+    const swiglu_status st = check_shape(M, K, N);
+    if (st != SWIGLU_OK) return st;
+    if (adapters <= 0 || rank <= 0 || adapters > kMaxDim) return SWIGLU_ERR_BAD_SHAPE;
+    if (rank > kMaxRank) return SWIGLU_ERR_UNSUPPORTED_SHAPE;
+    if (adapters * (K + N) > ((int64_t)1 << 31)) return SWIGLU_ERR_BAD_SHAPE;
+    return SWIGLU_OK;
+}
+
+// the pack's sizes (lora_device.hpp, lora_kernels.hpp); groups: 2 for the gated
+// product, 1 for a plain projection
+struct LoraPack {
+    int groups, chunks, KB, ntiles;
+    int64_t a_elems, b_elems;   // parts A and B
+};
+
+LoraPack lora_pack_of(int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups) {
+    LoraPack l{};
+    l.groups = groups;
+    l.chunks = (int)ceil_div(rank, 16);
+    l.KB = (int)ceil_div(K, 64);
+    // the packed weights' tiles: 128 columns (gated) or 256
+    l.ntiles = (int)(groups == 2 ? ceil_div(N, 128) * 4 : ceil_div(N, 256) * 8);
+    l.a_elems = adapters * groups * l.chunks * l.KB * 1024;
+    l.b_elems = adapters * groups * l.chunks * l.ntiles * 512;
+    return l;
+}
+
+size_t lora_packed_bytes(int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups) {
+    if (check_lora(0, K, N, adapters, rank) != SWIGLU_OK) return 0;
+    const LoraPack l = lora_pack_of(K, N, adapters, rank, groups);
+    return (size_t)(l.a_elems + l.b_elems) * 2;
+}
+
+swiglu_status lora_pack_impl(const uint16_t* La1, const uint16_t* Lb1, const uint16_t* La2, const uint16_t* Lb2,
+                             uint16_t* Lp, int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups,
+                             void* stream) {
+    const swiglu_status st = check_lora(0, K, N, adapters, rank);
+    if (st != SWIGLU_OK) return st;
+    const LoraPack l = lora_pack_of(K, N, adapters, rank, groups);
+    const uint16_t* ins[4] = {La1, Lb1, La2, Lb2};
+    if (!Lp) return SWIGLU_ERR_NULL_POINTER;
+    for (int i = 0; i < 2 * groups; ++i)
+        if (!ins[i]) return SWIGLU_ERR_NULL_POINTER;
+    if (!aligned16(Lp)) return SWIGLU_ERR_MISALIGNED;
+    for (int i = 0; i < 2 * groups; ++i)
+        if (!aligned16(ins[i])) return SWIGLU_ERR_MISALIGNED;
+    const Range out = range_of(Lp, (l.a_elems + l.b_elems) * 2);
+    for (int i = 0; i < 2 * groups; ++i)
+        if (overlap(out, range_of(ins[i], adapters * rank * (i & 1 ? N : K) * 2))) return SWIGLU_ERR_ALIASING;
+    int Ki = (int)K, Ni = (int)N, r = (int)rank, g = groups, chunks = l.chunks, KB = l.KB, nt = l.ntiles;
+    long long pa = l.a_elems / 8, pieces = (l.a_elems + l.b_elems) / 8;
+    void* args[] = {&La1, &La2, &Lb1, &Lb2, &Lp, &g, &Ki, &Ni, &r, &chunks, &KB, &nt, &pa, &pieces};
+    const hipError_t e =
+        hipLaunchKernel(reinterpret_cast<const void*>(&swk::lora_pack_kernel),
+                        dim3((unsigned)std::min<int64_t>(ceil_div(pieces, 256), 1 << 20)), dim3(256), args, 0,
+                        (hipStream_t)stream);
+    return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+int64_t lora_t_bytes(int64_t M, int64_t rank, int groups) {
+    return (M * ceil_div(rank, 16) * groups * 64 + 255) / 256 * 256;
+}
+
+// The product's schedule: AUTO's, or data-parallel for a chunk of rows.
+Plan lora_plan(int64_t M, int64_t K, int64_t N, int groups, bool chunked) {
+    if (groups == 1)
+        return chunked ? make_plan(M, K, gemm_tiled_cols(N), SWIGLU_VARIANT_DATA_PARALLEL, cu_count_now())
+                       : gemm_plan(M, K, N);
+    return make_plan(M, K, N, chunked ? SWIGLU_VARIANT_DATA_PARALLEL : SWIGLU_VARIANT_AUTO, cu_count_now());
+}
+
+size_t lora_workspace(int64_t M, int64_t K, int64_t N, int64_t rank, int groups) {
+    if (check_lora(M, K, N, 1, rank) != SWIGLU_OK || M == 0) return 0;
+    const int64_t limit = stream_rows_limit(K, 2);
+    if (M > limit) return (size_t)lora_t_bytes(balanced_chunk(M, limit), rank, groups);
+    const Plan p = lora_plan(M, K, N, groups, false);
+    return (size_t)lora_t_bytes(M, rank, groups) +
+           split_workspace_bytes(p, M, groups == 2 ? N : gemm_tiled_cols(N));
+}
+
+template <int WAVES, int TT>
+hipError_t launch_shrink(swk::LoraShrinkArgs a, hipStream_t s) {
+    const int64_t blocks = ceil_div(a.M, 16), ty = ceil_div(a.groups * a.chunks, TT);
+    // workgroups that share a row block's distinct adapters, while the grid is small
+    const int64_t z = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / (blocks * ty)));
+    void* kargs[] = {&a};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swk::lora_shrink_kernel<WAVES, TT>),
+                           dim3((unsigned)blocks, (unsigned)ty, (unsigned)std::min<int64_t>(z, a.M)),
+                           dim3(64 * WAVES), kargs, 0, s);
+}
+
+// A few row blocks: 16 waves on each (block, tile), where the latency of the
+// loads counts; many: 4 waves and up to 4 tiles, so that A is read once.
+hipError_t run_shrink(const swk::LoraShrinkArgs& a, hipStream_t s) {
+    const int64_t blocks = ceil_div(a.M, 16), tiles = a.groups * a.chunks;
+    if (blocks * tiles <= 512) return launch_shrink<16, 1>(a, s);
+    if (tiles >= 4) return launch_shrink<4, 4>(a, s);
+    return tiles >= 2 ? launch_shrink<4, 2>(a, s) : launch_shrink<4, 1>(a, s);
+}
+
+// One chunk of rows, arguments checked.
+hipError_t run_lora(const uint16_t* A, const uint16_t* W, const uint16_t* Lp, const int* ids, const float* scales,
+                    uint16_t* Y, int64_t M, int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups,
+                    bool chunked, void* workspace, hipStream_t s) {
+    const LoraPack l = lora_pack_of(K, N, adapters, rank, groups);
+    swk::LoraShrinkArgs sh{};
+    sh.A = A; sh.P = Lp; sh.ids = ids; sh.scales = scales;
+    sh.T = (uint16_t*)workspace;
+    sh.M = (int)M; sh.K = (int)K; sh.KB = l.KB;
+    sh.adapters = (int)adapters; sh.groups = groups; sh.chunks = l.chunks; sh.rank = (int)rank;
+    hipError_t e = run_shrink(sh, s);
+    if (e != hipSuccess) return e;
+
+    swk::LoraArgs la{};
+    la.T = sh.T; la.B = Lp + l.a_elems; la.ids = ids;
+    la.adapters = (int)adapters; la.chunks = l.chunks; la.ntiles = l.ntiles;
+    const int64_t nt = groups == 2 ? N : gemm_tiled_cols(N);
+    const Plan p = lora_plan(M, K, N, groups, chunked);
+    if (p.variant == SWIGLU_VARIANT_DECODE) {
+        swk::DecodeArgs d{};
+        d.A = A; d.Wp = W; d.Y = Y;
+        d.M = (int)M; d.K = (int)K; d.N = (int)N; d.KB = p.KB;
+        return groups == 2 ? launch_decode_cfg(d, N, p, s, &la) : launch_decode_gemm(d, nt, p, s, &la);
+    }
+    swk::FusedArgs a{};
+    a.A = A; a.W1 = W; a.Y = Y;
+    a.M = (int)M; a.K = (int)K; a.N = (int)N;
+    a.tiles_m = p.tiles_m; a.tiles_n = p.tiles_n;
+    a.splits = p.splits; a.kb_per_split = p.kb_per_split; a.KB = p.KB;
+    if (p.splits == 1)
+        return groups == 2 ? launch_stream_dp<false>(a, p, s, &la)
+                           : launch_stream_dp<false, false, false, true>(a, p, s, &la);
+    // splits: the plain kernels' partial sums, reduced with the adapters
+    a.part = reinterpret_cast<float*>((char*)workspace + lora_t_bytes(M, rank, groups));
+    const int grid = p.tiles * p.splits;
+    if (groups == 2)
+        e = p.t.BM == 128 ? launch_stream<128, true>(a, grid, grid, s) : launch_stream<256, true>(a, grid, grid, s);
+    else
+        e = p.t.BM == 128 ? launch_stream<128, true, false, false, false, false, true>(a, grid, grid, s)
+                          : launch_stream<256, true, false, false, false, false, true>(a, grid, grid, s);
+    if (e != hipSuccess) return e;
+    const int64_t rgrid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(M * (nt / 4), 256), (int64_t)p.cus * 8));
+    int Mi = (int)M, Ni = (int)N, NTi = (int)nt, Si = p.splits;
+    const float* part = a.part;
+    void* args[] = {(void*)&part, (void*)&Y, &la, &Mi, &Ni, &NTi, &Si};
+    return hipLaunchKernel(groups == 2 ? reinterpret_cast<const void*>(&swk::lora_reduce_kernel<false>)
+                                       : reinterpret_cast<const void*>(&swk::lora_reduce_kernel<true>),
+                           dim3((unsigned)rgrid), dim3(256), args, 0, s);
+}
+
+swiglu_status lora_impl(const uint16_t* A, const uint16_t* W, const uint16_t* Lp, const int* ids, const float* scales,
+                        uint16_t* Y, int64_t M, int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+    swiglu_status st = check_lora(M, K, N, adapters, rank);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return SWIGLU_OK;
+    if (!A || !W || !Lp || !ids || !scales || !Y) return SWIGLU_ERR_NULL_POINTER;
+    if (!aligned16(A) || !aligned16(W) || !aligned16(Lp) || !aligned16(Y) || ((uintptr_t)ids & 3) ||
+        ((uintptr_t)scales & 3))
+        return SWIGLU_ERR_MISALIGNED;
+    const int64_t wbytes = (groups == 2 ? packed_elems(K, N) : gemm_packed_elems(K, N)) * 2;
+    const Range ins[5] = {range_of(A, M * K * 2), range_of(W, wbytes),
+                          range_of(Lp, (int64_t)lora_packed_bytes(K, N, adapters, rank, groups)),
+                          range_of(ids, M * 4), range_of(scales, adapters * 4)};
+    const Range y = range_of(Y, M * N * 2);
+    for (const Range& r : ins)
+        if (overlap(y, r)) return SWIGLU_ERR_ALIASING;
+    const size_t need = lora_workspace(M, K, N, rank, groups);
+    if (!workspace || workspace_bytes < need) return SWIGLU_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return SWIGLU_ERR_MISALIGNED;
+    const Range w = range_of(workspace, (int64_t)need);
+    for (const Range& r : ins)
+        if (overlap(w, r)) return SWIGLU_ERR_ALIASING;
+    if (overlap(w, y)) return SWIGLU_ERR_ALIASING;
+    const int64_t limit = stream_rows_limit(K, 2);
+    const bool chunked = M > limit;
+    const int64_t rows = chunked ? balanced_chunk(M, limit) : M;
+    for (int64_t m0 = 0; m0 < M; m0 += rows) {
+        const hipError_t e = run_lora(A + m0 * K, W, Lp, ids + m0, scales, Y + m0 * N, std::min(rows, M - m0), K, N,
+                                      adapters, rank, groups, chunked, workspace, (hipStream_t)stream);
+        if (e != hipSuccess) return hip_fail(e);
+    }
+    return SWIGLU_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t swiglu_lora_packed_bytes(int64_t K, int64_t N, int64_t adapters, int64_t rank) {
+    return lora_packed_bytes(K, N, adapters, rank, 2);
+}
+
+size_t swiglu_gemm_lora_packed_bytes(int64_t K, int64_t N, int64_t adapters, int64_t rank) {
+    return lora_packed_bytes(K, N, adapters, rank, 1);
+}
+
+swiglu_status swiglu_lora_pack(const swiglu_bf16* La1, const swiglu_bf16* Lb1, const swiglu_bf16* La2,
+                               const swiglu_bf16* Lb2, swiglu_bf16* Lp, int64_t K, int64_t N, int64_t adapters,
+                               int64_t rank, void* stream) {
+    return lora_pack_impl(La1, Lb1, La2, Lb2, Lp, K, N, adapters, rank, 2, stream);
+}
+
+swiglu_status swiglu_gemm_lora_pack(const swiglu_bf16* La, const swiglu_bf16* Lb, swiglu_bf16* Lp, int64_t K, int64_t N,
+                                    int64_t adapters, int64_t rank, void* stream) {
+    return lora_pack_impl(La, Lb, nullptr, nullptr, Lp, K, N, adapters, rank, 1, stream);
+}
+
+size_t swiglu_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank) {
+    return lora_workspace(M, K, N, rank, 2);
+}
+
+size_t swiglu_gemm_lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t rank) {
+    return lora_workspace(M, K, N, rank, 1);
+}
+
+swiglu_status swiglu_fused_packed_lora(const swiglu_bf16* A, const swiglu_bf16* Wp, const swiglu_bf16* Lp,
+                                       const int32_t* ids, const float* scales, swiglu_bf16* Y, int64_t M, int64_t K,
+                                       int64_t N, int64_t adapters, int64_t rank, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+    return lora_impl(A, Wp, Lp, ids, scales, Y, M, K, N, adapters, rank, 2, workspace, workspace_bytes, stream);
+}
+
+swiglu_status swiglu_gemm_packed_lora(const swiglu_bf16* A, const swiglu_bf16* Wg, const swiglu_bf16* Lp,
+                                      const int32_t* ids, const float* scales, swiglu_bf16* C, int64_t M, int64_t K,
+                                      int64_t N, int64_t adapters, int64_t rank, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    return lora_impl(A, Wg, Lp, ids, scales, C, M, K, N, adapters, rank, 1, workspace, workspace_bytes, stream);
 }
 
 swiglu_status swiglu_probe_mfma(float* sink, int blocks, int iters, void* stream) {

@@ -10,27 +10,10 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _dev_bf16, _ptr, _resolve_workspace, _shape, _stream, lib, swiglu_fused, swiglu_gemm_bf16
+from . import (_check, _dev_bf16, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
+               swiglu_gemm_bf16)
 
 _need: dict = {}
-
-
-def _new(shape, device, s: int) -> torch.Tensor:
-    """An uninitialised bf16 output, allocated on the stream that writes it."""
-    if s == torch.cuda.current_stream(device).cuda_stream:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=device)):
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-
-
-def _scratch(workspace, need: int, device, s: int):
-    """As _resolve_workspace; a call under graph capture without a workspace of
-    its own gets a buffer of the graph's pool, so that no buffer that a graph
-    writes on replay is handed to another call."""
-    if workspace is None and need and torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        return ws, need
-    return _resolve_workspace(workspace, need, device, s)
 
 
 def swiglu_train_workspace_bytes(M: int, K: int, N: int) -> int:
