@@ -137,6 +137,15 @@ hipError_t launch_gemm_tile(const swt::GemmArgs& a, hipStream_t s) {
 }
 
 template <int AOP, int BOP, bool DUAL, int EPI>
+hipError_t launch_wide(const swt::GemmArgs& a, hipStream_t s) {
+    const void* fn = a.kseg % 64 ? reinterpret_cast<const void*>(&swt::wide_gemm_kernel<AOP, BOP, DUAL, EPI, true>)
+                                 : reinterpret_cast<const void*>(&swt::wide_gemm_kernel<AOP, BOP, DUAL, EPI, false>);
+    swt::GemmArgs args = a;
+    void* kargs[] = {&args};
+    return hipLaunchKernel(fn, dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits)), dim3(256), kargs, 0, s);
+}
+
+template <int AOP, int BOP, bool DUAL, int EPI>
 hipError_t launch_product(swt::GemmArgs a, const TilePlan& t, hipStream_t s) {
     a.tiles_m = t.tiles_m;
     a.tiles_n = t.tiles_n;
@@ -145,7 +154,7 @@ hipError_t launch_product(swt::GemmArgs a, const TilePlan& t, hipStream_t s) {
     a.part_cols = a.cols * (DUAL ? 2 : 1);
     a.kb_seg = (int)ceil_div(a.kseg, 64);
     hipError_t e;
-    if (t.bm == 256) e = launch_gemm_tile<256, 256, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
+    if (t.bm == 256) e = launch_wide<AOP, BOP, DUAL, EPI>(a, s);
     else if (t.bm == 128) e = launch_gemm_tile<128, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
     else if constexpr (AOP == swt::OP_KC) e = launch_gemm_tile<64, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
     else e = hipErrorInvalidValue;

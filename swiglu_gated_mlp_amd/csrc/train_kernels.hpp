@@ -130,6 +130,34 @@ __device__ __forceinline__ void finish8(const GemmArgs& p, int m, int n, const f
     }
 }
 
+__device__ __forceinline__ void load8(const float* s, float (&x)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(s + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+    }
+}
+
+__device__ __forceinline__ void store8(float* d, const float (&x)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<f32x4*>(d + 4 * h) = f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+}
+
+// 8 columns of a finished tile: to the split's sums, or through the epilogue.
+template <bool DUAL, int EPI>
+__device__ __forceinline__ void finish_or_part(const GemmArgs& p, int split, int m, int n, const float (&x)[8],
+                                               const float (&y)[8]) {
+    if (p.splits > 1) {
+        float* d = p.part + ((size_t)split * p.rows + m) * p.part_cols + n;
+        store8(d, x);
+        if constexpr (DUAL) store8(d + p.cols, y);
+    } else {
+        finish8<EPI>(p, m, n, x, y);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // One BM x BN tile of sums per workgroup of WM x WN waves (DUAL: BN / 2 columns
 // of each half).  Each wave owns BM/WM x BN/WN of it as 32 x 32 MFMA blocks.
@@ -355,31 +383,274 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_gemm_kernel(GemmArgs p) {
             const int r = t * RPI + lane / LPR, c = 8 * (lane % LPR);
             const int m = row_base + ps * RPP + r, n = col_base + c;
             float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            load8(st + r * PW + c, x);
+            if constexpr (DUAL) load8(st + r * PW + OW + c, y);
+            if (m < p.rows && n < p.cols) finish_or_part<DUAL, EPI>(p, split, m, n, x, y);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The same product on 256 x 256 tiles (dual: 128 columns of each half), for
+// outputs large enough to fill the CUs with them.  4 waves, 2 x 2, own 128 x 128
+// sums each, all 256 accumulation registers of a wave.
+//   A tile moves 64 KiB into a CU per 64-deep stage for 2048 matrix-core cycles;
+//   what bounds it is having those loads in flight early enough.  Two whole
+//   stages are 128 of the 160 KiB of LDS, so the ring is made of five 32 KiB half
+//   stages (one operand's 256 x 64 each): stage s's b goes out as soon as stage
+//   s - 2 has been read, a whole stage before it is needed, and its a another
+//   three sub-steps earlier, into the fifth slot.
+//   Each 16-deep sub-step is a fixed sequence (fenced, four matrix instructions
+//   at a time) with the next sub-step's fragment reads and a share of the loads
+//   between them; the waits are explicit: fragments at the start of the sub-step
+//   that uses them, loads before the stage's one barrier, where only the a loads
+//   of the stage after next may still be in flight.  Stages past the end load
+//   the zero chunk, so every stage issues the same loads and the counts hold.
+// ---------------------------------------------------------------------------
+constexpr int WIDE_SLOT = 256 * BK;   // elements of a half stage
+
+// Direct global -> LDS load of 16 bytes a lane that the compiler does not track:
+// LDS byte address lds (uniform) + 16 * lane receives the lane's bytes.  With the
+// tracked builtin, every transposing LDS read waits for all loads in flight
+// (vmcnt(0)): it cannot know that they fill other slots.  There is no register to
+// write early; the kernel waits with explicit counts, and the compiler's own
+// waits for loads it does track only wait for more than they must.
+__device__ __forceinline__ void dma16_uniform(const uint16_t* base, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void dma16_lane(const uint16_t* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src)
+                 : "memory", "m0");
+}
+
+template <int AOP, int BOP, bool DUAL, int EPI, bool RAGGED>
+__global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p) {
+    constexpr int INS = 8;   // 1 KiB direct loads per wave and half stage
+    constexpr int GROUP_M = 8;
+    __shared__ __attribute__((aligned(16))) uint16_t smem[5 * WIDE_SLOT];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+
+    const int logical = xcd_remap(blockIdx.x, gridDim.x);
+    const int tile = logical / p.splits;
+    const int split = logical - tile * p.splits;
+    int tm, tn;
+    {
+        const int per_group = GROUP_M * p.tiles_n;
+        const int group = tile / per_group;
+        const int first_m = group * GROUP_M;
+        const int gsize = min(p.tiles_m - first_m, GROUP_M);
+        const int in_group = tile - group * per_group;
+        tm = first_m + in_group % gsize;
+        tn = in_group / gsize;
+    }
+    const int m0 = tm * 256;
+    const int n0 = tn * (DUAL ? 128 : 256);
+    const int s_first = split * p.kb_per_split;
+    const int s_end = min(p.segs * p.kb_seg, s_first + p.kb_per_split);   // the host makes no empty split
+
+    // Byte offsets of a lane's 16 bytes in load i from the stage's base.
+    // k-contiguous: load q = 8 wave + i brings rows 8q .. 8q + 7, lane l's chunk
+    // is (l & 7) ^ (l >> 3) ^ (q & 7) (lds_off's swizzle); k-strided: k rows 2q
+    // and 2q + 1, columns 8 ((l & 31) ^ 4 (k & 3)) (rm_off's).
+    uint32_t a_off[INS], b_off[INS];
+    const int hi5 = lane >> 5;
+    auto ks_chunk = [&](int i) { return (lane & 31) ^ ((2 * (i & 1) + hi5) << 2); };
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(st + r * PW + c + 4 * h);
+    for (int i = 0; i < INS; ++i) {
+        const int q = wave * INS + i;
+        const int kc = 8 * ((lane & 7) ^ (lane >> 3) ^ i);
+        if constexpr (AOP == OP_KC)
+            a_off[i] = (uint32_t)((min(m0 + q * 8 + (lane >> 3), p.rows - 1) - m0) * p.lda + kc) * 2;
+        else
+            a_off[i] = (uint32_t)((2 * q + hi5) * p.lda + min(m0 + 8 * ks_chunk(i), p.rows - 8) - m0) * 2;
+        if constexpr (BOP == OP_KC)
+            b_off[i] = (uint32_t)((min(n0 + q * 8 + (lane >> 3), p.cols - 1) - n0) * p.ldb + kc) * 2;
+        else
+            b_off[i] = (uint32_t)((2 * q + hi5) * p.ldb +
+                                  min(n0 + 8 * (ks_chunk(i) & (DUAL ? 15 : 31)), p.cols - 8) - n0) * 2;
+    }
+    // dual: the lanes of a load's second half read the other matrix
+    const uint16_t* const b_lane = (DUAL && (lane & 16)) ? p.B1 : p.B0;
+    // the first k of a lane's chunk within the stage (RAGGED)
+    const int kc_x = 8 * ((lane & 7) ^ (lane >> 3));
+    auto lane_k = [&](int op, int i) { return op == OP_KC ? kc_x ^ (8 * i) : 2 * (wave * INS + i) + hi5; };
+
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_ptr)smem;
+    // load i of operand a (or b) of stage s into ring slot `slot`
+    auto issue = [&](auto bc, int s, int slot, int i) {
+        constexpr bool ISB = decltype(bc)::value;
+        constexpr int OP = ISB ? BOP : AOP;
+        const bool valid = s < s_end;
+        const int seg = s >= p.kb_seg ? 1 : 0;
+        const int k0 = (s - seg * p.kb_seg) * BK;
+        const long long ld = ISB ? p.ldb : p.lda;
+        const int r0 = ISB ? n0 : m0;
+        const uint32_t off = ISB ? b_off[i] : a_off[i];
+        const size_t at = OP == OP_KC ? (size_t)r0 * ld + k0 : (size_t)k0 * ld + r0;
+        const uint32_t dst = lds0 + (uint32_t)(slot * WIDE_SLOT + (wave * INS + i) * 512) * 2;
+        if constexpr (!RAGGED && !(ISB && DUAL)) {
+            const uint16_t* m = ISB ? (seg ? p.B1 : p.B0) : (seg ? p.A1 : p.A0);
+            dma16_uniform(valid ? m + at : g_zeros, off & (valid ? 0xffffffffu : 0u), dst);
+        } else {
+            const uint16_t* m = ISB ? (DUAL ? b_lane : (seg ? p.B1 : p.B0)) : (seg ? p.A1 : p.A0);
+            const uint16_t* src =
+                reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(m + at) + off);
+            if (!valid || (RAGGED && k0 + lane_k(OP, i) >= p.kseg)) src = g_zeros;
+            dma16_lane(src, dst);
+        }
+    };
+    using A_ = std::false_type;
+    using B_ = std::true_type;
+
+    // Fragment addresses: a few lane offsets and constants.  k-contiguous: rows
+    // w*128 + 32i + (l & 31), chunk (2kk + (l >> 5)) ^ swz(row), and
+    // swz(32i + r) = swz(r) ^ 4 (i & 1): four bases x = kk ^ 2 (i & 1).
+    // k-strided: k row 16kk + 8 (l >> 5) + (l & 15) / 4, whose low bits fix the
+    // swizzle for the lane, columns w*128 + 32i + ...: four bases, one per i.
+    auto frag_bases = [&](int op, int w, bool dual, uint32_t (&base)[4]) {
+        if (op == OP_KC) {
+            const int r = lane & 31, hs = hi5 ^ swz(r);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
-                if constexpr (DUAL) {
-                    const f32x4 w = *reinterpret_cast<const f32x4*>(st + r * PW + OW + c + 4 * h);
+            for (int x = 0; x < 4; ++x) base[x] = (uint32_t)(w * 128 * 128 + r * 128 + ((hs ^ (2 * x)) << 4));
+        } else {
+            const int k = 8 * hi5 + ((lane & 15) >> 2);
+            const int c = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[4 * h + e] = w[e];
+            for (int i = 0; i < 4; ++i) {
+                const int col = dual ? (i >> 1) * 128 + w * 64 + (i & 1) * 32 : w * 128 + i * 32;
+                base[i] = (uint32_t)rm_off<256>(k, col + c) * 2;
+            }
+        }
+    };
+    uint32_t a_base[4], b_base[4];
+    frag_bases(AOP, wm, false, a_base);
+    frag_bases(BOP, wn, DUAL, b_base);
+    bf16x8 fa[2][4], fb[2][4];
+    auto read_one = [&](int op, const uint32_t (&base)[4], uint32_t so, int kk, int i) -> bf16x8 {
+        const char* sm = reinterpret_cast<const char*>(smem) + so;
+        if (op == OP_KC)
+            return *reinterpret_cast<const bf16x8*>(sm + i * 4096 + base[kk ^ (2 * (i & 1))]);
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(sm + kk * 8192 + base[i]);
+        const s16x4 both[2] = {ds_read_tr16(q), ds_read_tr16(q + 1024)};
+        return __builtin_bit_cast(bf16x8, both);
+    };
+    // byte offset of a ring slot, opaque so that addresses are formed from the
+    // lane bases instead of being kept for every slot
+    auto slot_off = [&](int slot) {
+        uint32_t so = (uint32_t)slot * (WIDE_SLOT * 2);
+        asm volatile("" : "+s"(so));
+        return so;
+    };
+
+    f32x16 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    // one 16-deep sub-step on fragment set CUR: 16 matrix instructions, the next
+    // sub-step's reads (sub-step rkk of the slots at aso, bso) in its first half,
+    // and NLD loads per quarter of operand LB from load l0 on
+    auto substep = [&](auto curc, uint32_t aso, uint32_t bso, int rkk, auto bc, auto nldc, int ls, int lslot, int l0) {
+        constexpr int CUR = decltype(curc)::value;
+        constexpr int NLD = decltype(nldc)::value;
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[CUR][j], fa[CUR][i], acc[i][j], 0, 0, 0);
+            if (i < 2) {
+#pragma unroll
+                for (int t = 2 * i; t < 2 * i + 2; ++t) {
+                    fa[CUR ^ 1][t] = read_one(AOP, a_base, aso, rkk, t);
+                    fb[CUR ^ 1][t] = read_one(BOP, b_base, bso, rkk, t);
                 }
             }
-            if (m < p.rows && n < p.cols) {
-                if (p.splits > 1) {
-                    float* d = p.part + ((size_t)split * p.rows + m) * p.part_cols + n;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        *reinterpret_cast<f32x4*>(d + 4 * h) = f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
-                        if constexpr (DUAL)
-                            *reinterpret_cast<f32x4*>(d + p.cols + 4 * h) =
-                                f32x4{y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]};
-                    }
-                } else {
-                    finish8<EPI>(p, m, n, x, y);
+            for (int t = 0; t < NLD; ++t) issue(bc, ls, lslot, l0 + i * NLD + t);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    using C0 = std::integral_constant<int, 0>;
+    using C1 = std::integral_constant<int, 1>;
+    using C2 = std::integral_constant<int, 2>;
+
+    // stage s in slots sa (a) and sa + 1 (b), modulo 5
+    auto wrap = [](int x) { return x >= 5 ? x - 5 : x; };
+#pragma unroll
+    for (int i = 0; i < INS; ++i) issue(A_{}, s_first, 0, i);
+#pragma unroll
+    for (int i = 0; i < INS; ++i) issue(B_{}, s_first, 1, i);
+#pragma unroll
+    for (int i = 0; i < INS; ++i) issue(A_{}, s_first + 1, 2, i);
+#pragma unroll
+    for (int i = 0; i < INS; ++i) issue(B_{}, s_first + 1, 3, i);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * INS, 0));
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        fa[0][t] = read_one(AOP, a_base, 0u, 0, t);
+        fb[0][t] = read_one(BOP, b_base, WIDE_SLOT * 2, 0, t);
+    }
+    int sa = 0;
+    for (int s = s_first; s < s_end; ++s) {
+        const uint32_t ao = slot_off(sa), bo = slot_off(wrap(sa + 1));
+        __builtin_amdgcn_sched_barrier(0);
+        substep(C0{}, ao, bo, 1, A_{}, C1{}, s + 2, wrap(sa + 4), 0);
+        substep(C1{}, ao, bo, 2, A_{}, C1{}, s + 2, wrap(sa + 4), 4);
+        substep(C0{}, ao, bo, 3, A_{}, C0{}, 0, 0, 0);
+        // stage s + 1 has landed (only stage s + 2's a loads may be in flight),
+        // and this wave has read stage s (its last reads too: they fill the
+        // next sub-step's fragments)
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(INS, 0));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        const int sn = wrap(sa + 2);
+        substep(C1{}, slot_off(sn), slot_off(wrap(sn + 1)), 0, B_{}, C2{}, s + 2, sa, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        sa = sn;
+    }
+    // the zero-chunk loads past the end
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __builtin_amdgcn_s_barrier();
+
+    // the sums through LDS (fp32, 64 rows of the wave at a time), as in
+    // tile_gemm_kernel
+    constexpr int PW = 128 + 4;
+    constexpr int OW = DUAL ? 64 : 128;
+    constexpr int LPR = OW / 8, RPI = 64 / LPR;
+    static_assert(4 * 64 * PW * 4 <= 5 * WIDE_SLOT * 2, "staging fits");
+    float* const st = reinterpret_cast<float*>(smem) + wave * 64 * PW;
+    const int row_base = m0 + wm * 128, col_base = n0 + wn * OW;
+#pragma unroll
+    for (int ps = 0; ps < 2; ++ps) {
+        if (ps) __syncthreads();
+#pragma unroll
+        for (int ii = 0; ii < 2; ++ii)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x16& a = acc[2 * ps + ii][j];
+                    *reinterpret_cast<f32x4*>(st + (ii * 32 + (lane & 31)) * PW + j * 32 + 8 * q + 4 * hi5) =
+                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
                 }
-            }
+        __syncthreads();
+        for (int t = 0; t < 64 / RPI; ++t) {
+            const int r = t * RPI + lane / LPR, c = 8 * (lane % LPR);
+            const int m = row_base + ps * 64 + r, n = col_base + c;
+            float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            load8(st + r * PW + c, x);
+            if constexpr (DUAL) load8(st + r * PW + OW + c, y);
+            if (m < p.rows && n < p.cols) finish_or_part<DUAL, EPI>(p, split, m, n, x, y);
         }
     }
 }
