@@ -53,7 +53,10 @@ struct TilePlan {
     int bm, bn;            // tile (dual: bn / 2 columns of each half)
     int tiles_m, tiles_n;
     int splits, kb_per_split;
+    int workers, full;     // 256 x 256 tiles: workgroups, and tiles computed whole
 };
+
+constexpr int64_t kPieceBytes = 256 * 256 * 4;   // the sums of a piece of a 256 x 256 tile
 
 // rows x cols sums (dual: cols of each half) over kb blocks of 64.  small_ok:
 // operand a is k-contiguous, so 64-row tiles exist.
@@ -62,17 +65,25 @@ TilePlan plan_tiles(int64_t rows, int64_t cols, bool dual, int64_t kb, bool smal
     TilePlan t{};
     const int half = dual ? 2 : 1;
     const int64_t big = ceil_div(rows, 256) * ceil_div(cols, 256 / half);
-    if (rows > 128 && 4 * big >= 3 * cus) {
+    if (rows > 128 && big * kb >= 12 * cus) {
         t.bm = t.bn = 256;
-    } else {
-        t.bm = (rows <= 64 && small_ok) ? 64 : 128;
-        t.bn = 128;
+        t.tiles_m = (int)ceil_div(rows, 256);
+        t.tiles_n = (int)ceil_div(cols, 256 / half);
+        t.splits = 1;
+        t.kb_per_split = (int)kb;
+        t.workers = cus;
+        t.full = (int)(big / cus * cus);
+        // a last round that is nearly full costs less than its pieces' sums
+        if (10 * (big - t.full) >= 9 * cus) t.full = (int)big;
+        return t;
     }
+    t.bm = (rows <= 64 && small_ok) ? 64 : 128;
+    t.bn = 128;
     t.tiles_m = (int)ceil_div(rows, t.bm);
     t.tiles_n = (int)ceil_div(cols, t.bn / half);
     const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
     int64_t s = 1;
-    if (2 * tiles < 3 * cus && t.bm < 256) s = std::min<int64_t>(ceil_div(3 * cus, 2 * tiles), kb / 8);
+    if (2 * tiles < 3 * cus) s = std::min<int64_t>(ceil_div(3 * cus, 2 * tiles), kb / 8);
     s = std::max<int64_t>(s, 1);
     t.kb_per_split = (int)ceil_div(kb, s);
     t.splits = (int)ceil_div(kb, t.kb_per_split);
@@ -80,6 +91,7 @@ TilePlan plan_tiles(int64_t rows, int64_t cols, bool dual, int64_t kb, bool smal
 }
 
 int64_t part_bytes(const TilePlan& t, int64_t rows, int64_t cols, bool dual) {
+    if (t.bm == 256) return t.full < t.tiles_m * t.tiles_n ? 2 * t.workers * kPieceBytes : 0;
     return t.splits > 1 ? (int64_t)t.splits * rows * cols * (dual ? 2 : 1) * 4 : 0;
 }
 
@@ -137,12 +149,18 @@ hipError_t launch_gemm_tile(const swt::GemmArgs& a, hipStream_t s) {
 }
 
 template <int AOP, int BOP, bool DUAL, int EPI>
-hipError_t launch_wide(const swt::GemmArgs& a, hipStream_t s) {
+hipError_t launch_wide(const swt::GemmArgs& a, int workers, hipStream_t s) {
     const void* fn = a.kseg % 64 ? reinterpret_cast<const void*>(&swt::wide_gemm_kernel<AOP, BOP, DUAL, EPI, true>)
                                  : reinterpret_cast<const void*>(&swt::wide_gemm_kernel<AOP, BOP, DUAL, EPI, false>);
     swt::GemmArgs args = a;
-    void* kargs[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits)), dim3(256), kargs, 0, s);
+    const int rest = a.tiles_m * a.tiles_n - a.full;
+    int whole = std::min(a.full, workers);
+    void* kargs[] = {&args, &whole, &workers};
+    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(whole + (rest ? workers : 0))), dim3(256), kargs, 0, s);
+    if (e != hipSuccess || rest == 0) return e;
+    void* rargs[] = {&args, &workers};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::wide_reduce_kernel<DUAL, EPI>),
+                           dim3((unsigned)(rest * (DUAL ? 8 : 16))), dim3(256), rargs, 0, s);
 }
 
 template <int AOP, int BOP, bool DUAL, int EPI>
@@ -154,8 +172,9 @@ hipError_t launch_product(swt::GemmArgs a, const TilePlan& t, hipStream_t s) {
     a.part_cols = a.cols * (DUAL ? 2 : 1);
     a.kb_seg = (int)ceil_div(a.kseg, 64);
     hipError_t e;
-    if (t.bm == 256) e = launch_wide<AOP, BOP, DUAL, EPI>(a, s);
-    else if (t.bm == 128) e = launch_gemm_tile<128, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
+    a.full = t.full;
+    if (t.bm == 256) return launch_wide<AOP, BOP, DUAL, EPI>(a, t.workers, s);
+    if (t.bm == 128) e = launch_gemm_tile<128, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
     else if constexpr (AOP == swt::OP_KC) e = launch_gemm_tile<64, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
     else e = hipErrorInvalidValue;
     if (e != hipSuccess || t.splits == 1) return e;

@@ -62,7 +62,8 @@ struct GemmArgs {
     int kb_seg;            // ceil(kseg / 64)
     int tiles_m, tiles_n;
     int splits, kb_per_split;   // contraction blocks (over both segments) per split
-    float* part;           // split sums [split][rows][part_cols]
+    int full;              // 256-row tiles computed whole (wide_gemm_kernel)
+    float* part;           // split sums [split][rows][part_cols], or pieces' sums
     int part_cols;         // cols, or 2 cols for a dual product
     // epilogue operands
     uint16_t* C0;          // STORE: columns below n0_cols (row length ldc); KEEP: Y; D kinds: D
@@ -155,6 +156,158 @@ __device__ __forceinline__ void finish_or_part(const GemmArgs& p, int split, int
         if constexpr (DUAL) store8(d + p.cols, y);
     } else {
         finish8<EPI>(p, m, n, x, y);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The epilogue of one 32 x 32 MFMA block without LDS.  A lane holds 16 sums of
+// row l & 31: v[4q + e] is column 8q + 4 (l >> 5) + e.  Two exchanges between
+// lanes (v_permlane32_swap, v_permlane16_swap) turn the block, packed to bf16,
+// into 16 bytes a lane with four lanes on 64 adjacent bytes of a row:
+//   out[h]: row 16h + (l & 15), columns 8c .. 8c + 7, c = 2 ((l >> 4) & 1) + (l >> 5).
+// They are their own inverse, so operands of the epilogue (dY, G, U) are loaded
+// that way too and brought into the lanes that hold the matching sums.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(unsigned& a, unsigned& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// d[q][w]: packed columns 8q + 4 (l >> 5) + 2w, + 1
+__device__ __forceinline__ void block_to_rows(unsigned (&d)[4][2], u32x4 (&out)[2]) {
+#pragma unroll
+    for (int q = 0; q < 4; q += 2)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) swap32(d[q][w], d[q + 1][w]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) swap16(d[q][w], d[q + 2][w]);
+    out[0] = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
+    out[1] = u32x4{d[2][0], d[2][1], d[3][0], d[3][1]};
+}
+__device__ __forceinline__ void rows_to_block(const u32x4 (&in)[2], float (&v)[16]) {
+    unsigned d[4][2] = {{in[0][0], in[0][1]}, {in[0][2], in[0][3]}, {in[1][0], in[1][1]}, {in[1][2], in[1][3]}};
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) swap16(d[q][w], d[q + 2][w]);
+#pragma unroll
+    for (int q = 0; q < 4; q += 2)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) swap32(d[q][w], d[q + 1][w]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            v[4 * q + 2 * w] = __builtin_bit_cast(float, d[q][w] << 16);
+            v[4 * q + 2 * w + 1] = __builtin_bit_cast(float, d[q][w] & 0xFFFF0000u);
+        }
+}
+
+// A matrix seen from a tile's corner, for the block epilogue: accesses of lanes
+// past its rows or columns have offsets past the descriptor's end, where loads
+// give 0 and stores are dropped, so the epilogue has no branches (with branches
+// the compiler moved all sums of a wave out of the accumulation registers at
+// once and spilled).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr int RSRC_END = 0x7FFFFFF0;
+__device__ __forceinline__ Rsrc corner(const uint16_t* c, long long ld, int m0, int n0) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(c + (size_t)m0 * ld + n0), 0, RSRC_END, 0x00020000);
+}
+// The lane's two 16-byte pieces of a block: rows r, r + 16 and column n of the
+// tile at (m0, n0); inside: whether they lie in the matrix.
+struct BlockAt {
+    int r, n;
+    bool ok[2];
+    __device__ __forceinline__ uint32_t at(int h, long long ld) const {
+        return ok[h] ? (uint32_t)((r + 16 * h) * (int)ld + n) * 2 : 0xFFFFFFF0u;
+    }
+};
+__device__ __forceinline__ BlockAt block_at(const GemmArgs& p, int m0, int n0, int r0, int c0, int lane) {
+    BlockAt b;
+    b.r = r0 + (lane & 15);
+    b.n = c0 + 8 * (2 * ((lane >> 4) & 1) + (lane >> 5));
+    const bool in = n0 + b.n < p.cols;
+    b.ok[0] = in && m0 + b.r < p.rows;
+    b.ok[1] = in && m0 + b.r + 16 < p.rows;
+    return b;
+}
+__device__ __forceinline__ void block_store(const BlockAt& b, Rsrc c, long long ld, const float (&v)[16]) {
+    unsigned d[4][2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) d[q][w] = pack2(v[4 * q + 2 * w], v[4 * q + 2 * w + 1]);
+    u32x4 out[2];
+    block_to_rows(d, out);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) __builtin_amdgcn_raw_buffer_store_b128(out[h], c, b.at(h, ld), 0, 0);
+}
+__device__ __forceinline__ void block_load(const BlockAt& b, Rsrc c, long long ld, float (&v)[16]) {
+    u32x4 in[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) in[h] = __builtin_amdgcn_raw_buffer_load_b128(c, b.at(h, ld), 0, 0);
+    rows_to_block(in, v);
+}
+
+// The epilogue of the block at row r0, column c0 of the tile at (m0, n0) (x;
+// dual: and y).
+template <int EPI>
+__device__ __forceinline__ void finish_block(const GemmArgs& p, int m0, int n0, int r0, int c0, int lane,
+                                             const f32x16& x, const f32x16& y) {
+    const BlockAt b = block_at(p, m0, n0, r0, c0, lane);
+    float v[16], w[16];
+    if constexpr (EPI == EP_STORE) {
+        // columns from n0_cols on belong to C1 (a 16-byte piece never straddles)
+        BlockAt b0 = b, b1 = b;
+        const bool second = n0 + b.n >= p.n0_cols;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            b0.ok[h] = b.ok[h] && !second;
+            b1.ok[h] = b.ok[h] && second;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = x[r];
+        // the tile's corner within C1 may lie before its first column: the
+        // descriptor starts at the row, the column offset is not negative then
+        if (n0 < p.n0_cols) block_store(b0, corner(p.C0, p.ldc, m0, n0), p.ldc, v);
+        if (n0 + 256 > p.n0_cols) {
+            b1.n += n0 - p.n0_cols;
+            block_store(b1, corner(p.C1, p.ldc, m0, 0), p.ldc, v);
+        }
+    } else if constexpr (EPI == EP_KEEP) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = silu_f(x[r]) * y[r];
+        block_store(b, corner(p.C0, p.cols, m0, n0), p.cols, v);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = x[r];
+        block_store(b, corner(p.C1, p.cols, m0, n0), p.cols, v);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = y[r];
+        block_store(b, corner(p.C2, p.cols, m0, n0), p.cols, v);
+    } else {
+        float dg[16], du[16];
+        block_load(b, corner(p.E0, p.cols, m0, n0), p.cols, v);
+        if constexpr (EPI == EP_DUAL_D) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) silu_grad(v[r], x[r], y[r], dg[r], du[r]);
+        } else {
+            block_load(b, corner(p.E1, p.cols, m0, n0), p.cols, w);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) silu_grad(x[r], v[r], w[r], dg[r], du[r]);
+        }
+        const Rsrc d = corner(p.C0, 2 * (long long)p.cols, m0, n0);
+        block_store(b, d, 2 * (long long)p.cols, dg);
+        BlockAt bu = b;
+        bu.n += p.cols;
+        block_store(bu, d, 2 * (long long)p.cols, du);
     }
 }
 
@@ -414,52 +567,97 @@ constexpr int WIDE_SLOT = 256 * BK;   // elements of a half stage
 // tracked builtin, every transposing LDS read waits for all loads in flight
 // (vmcnt(0)): it cannot know that they fill other slots.  There is no register to
 // write early; the kernel waits with explicit counts, and the compiler's own
-// waits for loads it does track only wait for more than they must.
+// waits for loads it does track only wait for more than they must.  (m0, which
+// holds the LDS address, has no other use in the kernel.)
 __device__ __forceinline__ void dma16_uniform(const uint16_t* base, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory", "m0");
+                 : "memory");
 }
 __device__ __forceinline__ void dma16_lane(const uint16_t* src, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src)
-                 : "memory", "m0");
+                 : "memory");
 }
 
-template <int AOP, int BOP, bool DUAL, int EPI, bool RAGGED>
-__global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p) {
+// Work of one launch: the first workgroups, one per CU, compute tiles 0 .. full - 1
+// whole, tile after tile, and start the next tile's loads before the epilogue of
+// the last.  The R stages of the remaining tiles, fewer than there are CUs, are
+// dealt out evenly to W further workgroups, which start as CUs fall free: worker w
+// takes stages [w R / W, (w + 1) R / W) in order, at most two pieces, each the sums
+// of part of one tile, which go to memory and are added by wide_reduce_kernel.  So
+// no CU idles through a last round of whole tiles (448 tiles on 256 CUs), and
+// outputs of a few tiles fill the CUs too.
+struct WideRest {
+    int pieces, tile, s0, s_first, s_second, slot;
+};
+__device__ __forceinline__ WideRest wide_rest(const GemmArgs& p, int KB, int W, int w) {
+    const long long R = (long long)(p.tiles_m * p.tiles_n - p.full) * KB;
+    const long long r0 = R * w / W, r1 = R * (w + 1) / W;
+    WideRest r;
+    r.tile = (int)(r0 / KB);
+    r.s0 = (int)(r0 - (long long)r.tile * KB);
+    const int len = (int)(r1 - r0);   // <= KB
+    r.s_first = min(KB, r.s0 + len);
+    r.s_second = r.s0 + len - KB;
+    r.pieces = len == 0 ? 0 : (r.s_second > 0 ? 2 : 1);
+    r.slot = 2 * w;
+    return r;
+}
+
+// Whole tiles first, first + stride, ... < total (PIECES: the pieces of worker
+// first of stride workers), one after another in one workgroup.
+template <int AOP, int BOP, bool DUAL, int EPI, bool RAGGED, bool PIECES>
+__device__ __forceinline__ void wide_tiles(const GemmArgs& p, uint16_t* smem, int first, int stride, int total) {
     constexpr int INS = 8;   // 1 KiB direct loads per wave and half stage
     constexpr int GROUP_M = 8;
-    __shared__ __attribute__((aligned(16))) uint16_t smem[5 * WIDE_SLOT];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
 
-    const int logical = xcd_remap(blockIdx.x, gridDim.x);
-    const int tile = logical / p.splits;
-    const int split = logical - tile * p.splits;
-    int tm, tn;
-    {
+    const int KB = p.segs * p.kb_seg;
+    WideRest rest{};
+    if constexpr (PIECES) rest = wide_rest(p, KB, stride, xcd_remap(first, stride));
+    const int nitems = PIECES ? rest.pieces : (total - first + stride - 1) / stride;
+    if (nitems <= 0) return;
+    struct Item {
+        int m0, n0, s0, s1;   // stages [s0, s1)
+    };
+    auto item_of = [&](int k) __attribute__((always_inline)) {
+        Item it;
+        int tile;
+        if constexpr (PIECES) {
+            tile = p.full + rest.tile + k;
+            it.s0 = k ? 0 : rest.s0;
+            it.s1 = k ? rest.s_second : rest.s_first;
+        } else {
+            tile = xcd_remap(first + k * stride, total);
+            it.s0 = 0;
+            it.s1 = KB;
+        }
         const int per_group = GROUP_M * p.tiles_n;
         const int group = tile / per_group;
         const int first_m = group * GROUP_M;
         const int gsize = min(p.tiles_m - first_m, GROUP_M);
         const int in_group = tile - group * per_group;
-        tm = first_m + in_group % gsize;
-        tn = in_group / gsize;
-    }
-    const int m0 = tm * 256;
-    const int n0 = tn * (DUAL ? 128 : 256);
-    const int s_first = split * p.kb_per_split;
-    const int s_end = min(p.segs * p.kb_seg, s_first + p.kb_per_split);   // the host makes no empty split
+        it.m0 = (first_m + in_group % gsize) * 256;
+        it.n0 = (in_group / gsize) * (DUAL ? 128 : 256);
+        return it;
+    };
 
     // Byte offsets of a lane's 16 bytes in load i from the stage's base.
     // k-contiguous: load q = 8 wave + i brings rows 8q .. 8q + 7, lane l's chunk
     // is (l & 7) ^ (l >> 3) ^ (q & 7) (lds_off's swizzle); k-strided: k rows 2q
     // and 2q + 1, columns 8 ((l & 31) ^ 4 (k & 3)) (rm_off's).
     uint32_t a_off[INS], b_off[INS];
+    int m0 = 0, n0 = 0, s_end = 0;   // of the item that the loads fetch
     const int hi5 = lane >> 5;
     auto ks_chunk = [&](int i) { return (lane & 31) ^ ((2 * (i & 1) + hi5) << 2); };
+    // valid: false past the last item, whose loads then all read the zero chunk
+    auto load_item = [&](const Item& it, bool valid) __attribute__((always_inline)) {
+        m0 = it.m0;
+        n0 = it.n0;
+        s_end = valid ? it.s1 : 0;
 #pragma unroll
     for (int i = 0; i < INS; ++i) {
         const int q = wave * INS + i;
@@ -474,6 +672,7 @@ __global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p) {
             b_off[i] = (uint32_t)((2 * q + hi5) * p.ldb +
                                   min(n0 + 8 * (ks_chunk(i) & (DUAL ? 15 : 31)), p.cols - 8) - n0) * 2;
     }
+    };
     // dual: the lanes of a load's second half read the other matrix
     const uint16_t* const b_lane = (DUAL && (lane & 16)) ? p.B1 : p.B0;
     // the first k of a lane's chunk within the stage (RAGGED)
@@ -482,7 +681,7 @@ __global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p) {
 
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_ptr)smem;
     // load i of operand a (or b) of stage s into ring slot `slot`
-    auto issue = [&](auto bc, int s, int slot, int i) {
+    auto issue = [&](auto bc, int s, int slot, int i) __attribute__((always_inline)) {
         constexpr bool ISB = decltype(bc)::value;
         constexpr int OP = ISB ? BOP : AOP;
         const bool valid = s < s_end;
@@ -548,12 +747,14 @@ __global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p) {
     };
 
     f32x16 acc[4][4];
+    auto zero_acc = [&]() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    };
 
     // one 16-deep sub-step on fragment set CUR: 16 matrix instructions, the next
     // sub-step's reads (sub-step rkk of the slots at aso, bso) in its first half,
@@ -585,74 +786,151 @@ __global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p) {
 
     // stage s in slots sa (a) and sa + 1 (b), modulo 5
     auto wrap = [](int x) { return x >= 5 ? x - 5 : x; };
+    auto issue_first = [&](int s0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < INS; ++i) issue(A_{}, s_first, 0, i);
+        for (int i = 0; i < INS; ++i) issue(A_{}, s0, 0, i);
 #pragma unroll
-    for (int i = 0; i < INS; ++i) issue(B_{}, s_first, 1, i);
+        for (int i = 0; i < INS; ++i) issue(B_{}, s0, 1, i);
 #pragma unroll
-    for (int i = 0; i < INS; ++i) issue(A_{}, s_first + 1, 2, i);
+        for (int i = 0; i < INS; ++i) issue(A_{}, s0 + 1, 2, i);
 #pragma unroll
-    for (int i = 0; i < INS; ++i) issue(B_{}, s_first + 1, 3, i);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * INS, 0));
-    __builtin_amdgcn_s_barrier();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        fa[0][t] = read_one(AOP, a_base, 0u, 0, t);
-        fb[0][t] = read_one(BOP, b_base, WIDE_SLOT * 2, 0, t);
-    }
-    int sa = 0;
-    for (int s = s_first; s < s_end; ++s) {
-        const uint32_t ao = slot_off(sa), bo = slot_off(wrap(sa + 1));
-        __builtin_amdgcn_sched_barrier(0);
-        substep(C0{}, ao, bo, 1, A_{}, C1{}, s + 2, wrap(sa + 4), 0);
-        substep(C1{}, ao, bo, 2, A_{}, C1{}, s + 2, wrap(sa + 4), 4);
-        substep(C0{}, ao, bo, 3, A_{}, C0{}, 0, 0, 0);
-        // stage s + 1 has landed (only stage s + 2's a loads may be in flight),
-        // and this wave has read stage s (its last reads too: they fill the
-        // next sub-step's fragments)
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(INS, 0));
+        for (int i = 0; i < INS; ++i) issue(B_{}, s0 + 1, 3, i);
+    };
+    Item cur = item_of(0);
+    load_item(cur, true);
+    issue_first(cur.s0);
+    for (int k = 0;;) {
+        zero_acc();
+        // stage s0 has landed once at most stage s0 + 1's loads are in flight
+        // (the last item's stores are in the count too; loads complete in order
+        // among themselves)
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * INS, 0));
         __builtin_amdgcn_s_barrier();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            fa[0][t] = read_one(AOP, a_base, 0u, 0, t);
+            fb[0][t] = read_one(BOP, b_base, WIDE_SLOT * 2, 0, t);
+        }
+        int sa = 0;
+        for (int s = cur.s0; s < cur.s1; ++s) {
+            const uint32_t ao = slot_off(sa), bo = slot_off(wrap(sa + 1));
+            __builtin_amdgcn_sched_barrier(0);
+            substep(C0{}, ao, bo, 1, A_{}, C1{}, s + 2, wrap(sa + 4), 0);
+            substep(C1{}, ao, bo, 2, A_{}, C1{}, s + 2, wrap(sa + 4), 4);
+            substep(C0{}, ao, bo, 3, A_{}, C0{}, 0, 0, 0);
+            // stage s + 1 has landed (only stage s + 2's a loads may be in
+            // flight), and this wave has read stage s (its last reads fill the
+            // next sub-step's fragments)
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(INS, 0));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            const int sn = wrap(sa + 2);
+            substep(C1{}, slot_off(sn), slot_off(wrap(sn + 1)), 0, B_{}, C2{}, s + 2, sa, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            sa = sn;
+        }
+        // the sums stay in accumulation registers here (left to itself the
+        // compiler copies all of them out at the loop's end, and spills)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
+        // the zero-chunk loads past the end; then no wave reads the ring any more
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+        __builtin_amdgcn_s_barrier();
+        // the next item's first stages stream in during this one's epilogue
+        const bool more = k + 1 < nitems;
+        const Item nxt = item_of(more ? k + 1 : k);
+        load_item(nxt, more);
+        issue_first(nxt.s0);
         __builtin_amdgcn_sched_barrier(0);
-        const int sn = wrap(sa + 2);
-        substep(C1{}, slot_off(sn), slot_off(wrap(sn + 1)), 0, B_{}, C2{}, s + 2, sa, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        sa = sn;
-    }
-    // the zero-chunk loads past the end
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
-    __builtin_amdgcn_s_barrier();
-
-    // the sums through LDS (fp32, 64 rows of the wave at a time), as in
-    // tile_gemm_kernel
-    constexpr int PW = 128 + 4;
-    constexpr int OW = DUAL ? 64 : 128;
-    constexpr int LPR = OW / 8, RPI = 64 / LPR;
-    static_assert(4 * 64 * PW * 4 <= 5 * WIDE_SLOT * 2, "staging fits");
-    float* const st = reinterpret_cast<float*>(smem) + wave * 64 * PW;
-    const int row_base = m0 + wm * 128, col_base = n0 + wn * OW;
+        if constexpr (PIECES) {
+            // a piece's sums as they lie in the lanes: [wave][i][j][q][lane][4]
+            float* d = p.part + (size_t)(rest.slot + k) * 65536 + wave * 16384 + lane * 4;
 #pragma unroll
-    for (int ps = 0; ps < 2; ++ps) {
-        if (ps) __syncthreads();
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int ii = 0; ii < 2; ++ii)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<f32x4*>(d + ((i * 4 + j) * 4 + q) * 256) =
+                            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x16& a = acc[2 * ps + ii][j];
-                    *reinterpret_cast<f32x4*>(st + (ii * 32 + (lane & 31)) * PW + j * 32 + 8 * q + 4 * hi5) =
-                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < (DUAL ? 2 : 4); ++j) {
+                    // an opaque copy of the lane index: the block's addresses
+                    // are formed here, not kept in registers across the item
+                    int el = lane;
+                    if constexpr (DUAL) asm volatile("" : "+v"(el), "+a"(acc[i][j]), "+a"(acc[i][j + 2]));
+                    else asm volatile("" : "+v"(el), "+a"(acc[i][j]));
+                    finish_block<EPI>(p, cur.m0, cur.n0, wm * 128 + i * 32, wn * (DUAL ? 64 : 128) + j * 32, el,
+                                      acc[i][j], acc[i][DUAL ? j + 2 : j]);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-        __syncthreads();
-        for (int t = 0; t < 64 / RPI; ++t) {
-            const int r = t * RPI + lane / LPR, c = 8 * (lane % LPR);
-            const int m = row_base + ps * 64 + r, n = col_base + c;
-            float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            load8(st + r * PW + c, x);
-            if constexpr (DUAL) load8(st + r * PW + OW + c, y);
-            if (m < p.rows && n < p.cols) finish_or_part<DUAL, EPI>(p, split, m, n, x, y);
+        }
+        if (!more) break;
+        cur = nxt;
+        ++k;
+    }
+    // the loads past the last item
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+}
+
+template <int AOP, int BOP, bool DUAL, int EPI, bool RAGGED>
+__global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p, int whole, int workers) {
+    __shared__ __attribute__((aligned(16))) uint16_t smem[5 * WIDE_SLOT];
+    const int b = blockIdx.x;
+    if (b < whole) wide_tiles<AOP, BOP, DUAL, EPI, RAGGED, false>(p, smem, b, whole, p.full);
+    else wide_tiles<AOP, BOP, DUAL, EPI, RAGGED, true>(p, smem, b - whole, workers, workers);
+}
+
+// The pieces of the tiles past p.full, added in the order of the contraction
+// (whatever workgroup finished first), then the epilogue: one wave per 32 x 32
+// block (dual: pair of blocks), 4 to a workgroup.  workers: the product kernel's
+// workgroups.
+template <bool DUAL, int EPI>
+__global__ __launch_bounds__(256) void wide_reduce_kernel(GemmArgs p, int workers) {
+    constexpr int GROUP_M = 8;
+    constexpr int BLOCKS = DUAL ? 32 : 64;   // per tile
+    const int lane = threadIdx.x & 63;
+    const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rtile = id / BLOCKS, blk = id % BLOCKS;
+    const int wv = blk / (BLOCKS / 4), i = blk / (BLOCKS / 16) % 4, j = blk % (BLOCKS / 16);
+    const int KB = p.segs * p.kb_seg;
+    const long long total = (long long)(p.tiles_m * p.tiles_n - p.full) * KB;
+    // workers [w0, w1] hold the tile's stages
+    const long long first = (long long)rtile * KB;
+    int w = (int)(first * workers / total);
+    while (total * (w + 1) / workers <= first) ++w;
+    f32x16 x, y;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
+    for (; w < workers && total * w / workers < first + KB; ++w) {
+        if (total * w / workers == total * (w + 1) / workers) continue;
+        const WideRest rest = wide_rest(p, KB, workers, w);
+        const float* src = p.part + (size_t)(rest.slot + (rest.tile == rtile ? 0 : 1)) * 65536 + wv * 16384 + lane * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(src + ((i * 4 + j) * 4 + q) * 256);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[4 * q + e] += a[e];
+            if constexpr (DUAL) {
+                const f32x4 b = *reinterpret_cast<const f32x4*>(src + ((i * 4 + j + 2) * 4 + q) * 256);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[4 * q + e] += b[e];
+            }
         }
     }
+    const int tile = p.full + rtile;
+    const int per_group = GROUP_M * p.tiles_n;
+    const int group = tile / per_group;
+    const int first_m = group * GROUP_M;
+    const int gsize = min(p.tiles_m - first_m, GROUP_M);
+    const int in_group = tile - group * per_group;
+    finish_block<EPI>(p, (first_m + in_group % gsize) * 256, (in_group / gsize) * (DUAL ? 128 : 256),
+                      (wv & 1) * 128 + i * 32, (wv >> 1) * (DUAL ? 64 : 128) + j * 32, lane, x, y);
 }
 
 // The splits' sums of 8 adjacent columns, added in split order 0 .. splits - 1
