@@ -7,6 +7,9 @@
 #include "host_common.hpp"
 #include "train_kernels.hpp"
 
+#include <array>
+#include <map>
+
 using namespace swh;
 
 namespace {
@@ -47,185 +50,349 @@ struct Buffers {
 };
 
 // ---------------------------------------------------------------------------
-// tiles and splits of one product
+// Products, and their tiles and parts in a launch
 // ---------------------------------------------------------------------------
-struct TilePlan {
-    int bm, bn;            // tile (dual: bn / 2 columns of each half)
-    int tiles_m, tiles_n;
-    int splits, kb_per_split;
-    int workers, full;     // 256 x 256 tiles: workgroups, and tiles computed whole
+// F_: the forward product; then the products of a backward pass in its two phases,
+// D (recomputed, or from dZ; with dW3 beside it), then dA and dW1 | dW2.
+enum Kind { F_KEEP, D_DUAL, D_DY, G_DA, G_DW, G_DW3 };
+
+struct Shape {
+    int64_t rows, cols, kb;   // output (dual: columns of each half), contraction blocks
+    bool dual, strided;       // strided: both operands k-strided (no 64-row tiles)
 };
 
-constexpr int64_t kPieceBytes = 256 * 256 * 4;   // the sums of a piece of a 256 x 256 tile
-
-// rows x cols sums (dual: cols of each half) over kb blocks of 64.  small_ok:
-// operand a is k-contiguous, so 64-row tiles exist.
-TilePlan plan_tiles(int64_t rows, int64_t cols, bool dual, int64_t kb, bool small_ok, int cus) {
-    if (cus <= 0) cus = 256;
-    TilePlan t{};
-    const int half = dual ? 2 : 1;
-    const int64_t big = ceil_div(rows, 256) * ceil_div(cols, 256 / half);
-    if (rows > 128 && big * kb >= 12 * cus) {
-        t.bm = t.bn = 256;
-        t.tiles_m = (int)ceil_div(rows, 256);
-        t.tiles_n = (int)ceil_div(cols, 256 / half);
-        t.splits = 1;
-        t.kb_per_split = (int)kb;
-        t.workers = cus;
-        t.full = (int)(big / cus * cus);
-        // a last round that is nearly full costs less than its pieces' sums
-        if (10 * (big - t.full) >= 9 * cus) t.full = (int)big;
-        return t;
+Shape shape_of(Kind p, int64_t M, int64_t K, int64_t N) {
+    switch (p) {
+        case G_DA: return {M, K, 2 * ceil_div(N, 64), false, false};
+        case G_DW: return {K, 2 * N, ceil_div(M, 64), false, true};
+        case D_DY: return {M, N, ceil_div(K, 64), false, false};
+        case G_DW3: return {N, K, ceil_div(M, 64), false, true};
+        default: return {M, N, ceil_div(K, 64), true, false};   // F_KEEP, D_DUAL
     }
-    t.bm = (rows <= 64 && small_ok) ? 64 : 128;
-    t.bn = 128;
-    t.tiles_m = (int)ceil_div(rows, t.bm);
-    t.tiles_n = (int)ceil_div(cols, t.bn / half);
-    const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
-    int64_t s = 1;
-    if (2 * tiles < 3 * cus) s = std::min<int64_t>(ceil_div(3 * cus, 2 * tiles), kb / 8);
-    s = std::max<int64_t>(s, 1);
-    t.kb_per_split = (int)ceil_div(kb, s);
-    t.splits = (int)ceil_div(kb, t.kb_per_split);
+}
+
+// One product's items: tiles of bm x bn, the first `whole` as they are, the rest
+// in `splits` parts of kb_per_split blocks.
+struct Tiles {
+    int bm, bn;
+    int tiles_m, tiles_n;
+    int whole, rest, splits, kb_per_split;
+    int items() const { return whole + rest * splits; }
+    int64_t part_bytes() const { return (int64_t)rest * splits * bm * bn * 4; }
+};
+
+Tiles make_tiles(const Shape& s, int bm) {
+    Tiles t{};
+    t.bm = bm;
+    t.bn = bm == 256 ? 256 : 128;
+    t.tiles_m = (int)ceil_div(s.rows, t.bm);
+    t.tiles_n = (int)ceil_div(s.cols, t.bn / (s.dual ? 2 : 1));
+    t.whole = t.tiles_m * t.tiles_n;
+    t.splits = 1;
+    t.kb_per_split = (int)s.kb;
     return t;
 }
 
-int64_t part_bytes(const TilePlan& t, int64_t rows, int64_t cols, bool dual) {
-    if (t.bm == 256) return t.full < t.tiles_m * t.tiles_n ? 2 * t.workers * kPieceBytes : 0;
-    return t.splits > 1 ? (int64_t)t.splits * rows * cols * (dual ? 2 : 1) * 4 : 0;
+// The same with the tiles past `whole` in about `splits` parts.
+Tiles split_tiles(Tiles t, int64_t kb, int whole, int splits) {
+    t.kb_per_split = (int)ceil_div(kb, splits);
+    t.splits = (int)ceil_div(kb, t.kb_per_split);
+    t.rest = t.splits > 1 ? t.tiles_m * t.tiles_n - whole : 0;
+    t.whole = t.tiles_m * t.tiles_n - t.rest;
+    if (t.rest == 0) {
+        t.splits = 1;
+        t.kb_per_split = (int)kb;
+    }
+    return t;
+}
+
+// Microseconds of an item of `kb` contraction blocks, to choose by: measured on
+// this chip for a 64-deep stage and around it (first loads, epilogue).  256 x 256:
+// 15.0 / 18.2 / 25.8 / 38.1 / 64.1 us for a launch of 256 items of 1 / 3 / 8 / 16 /
+// 32 stages.
+double item_us(int bm, int64_t kb) { return bm == 256 ? 10.0 + 1.55 * kb : (bm == 128 ? 7.0 + 0.6 * kb : 6.0 + 0.5 * kb); }
+// parts' sums: a launch, and 4 bytes a sum written and read
+constexpr double kReduceUs = 6.0, kPartUs = 2.0 / 5.0e6;
+
+// When the last of a launch's items ends, each handed to the CU that falls free
+// first: CUs are kept in groups that fall free at the same time.
+struct Dispatch {
+    double at[64];
+    int cus[64];
+    int n = 1;
+    explicit Dispatch(int total) { at[0] = 0.0; cus[0] = total; }
+    void run(int count, double us) {
+        while (count > 0) {
+            int g = 0;
+            for (int i = 1; i < n; ++i)
+                if (at[i] < at[g]) g = i;
+            // whole rounds of a single group at once
+            int m = std::min(count, cus[g]);
+            const double end = at[g] + us * (n == 1 && count > cus[g] ? count / cus[g] : 1);
+            if (n == 1 && count > cus[g]) {
+                count -= count / cus[g] * cus[g];
+                at[g] = end;
+                continue;
+            }
+            count -= m;
+            int h = 0;
+            while (h < n && !(h != g && at[h] > end - 0.5 && at[h] < end + 0.5)) ++h;
+            if (m == cus[g]) {
+                at[g] = end;
+            } else if (h < n || n == 64) {
+                cus[h < n ? h : g] += h < n ? m : 0;
+                cus[g] -= h < n ? m : 0;
+            } else {
+                at[n] = end;
+                cus[n++] = m;
+                cus[g] -= m;
+            }
+        }
+    }
+    double end() const { return *std::max_element(at, at + n); }
+};
+
+// A launch of one product, or of two at once.
+struct Launch {
+    int jobs;
+    Kind kind[2];
+    Tiles t[2];
+    bool second_first;   // the second product's items have the longer run
+    int64_t part_bytes() const { return t[0].part_bytes() + (jobs == 2 ? t[1].part_bytes() : 0); }
+};
+
+double launch_us(Launch& l, const Shape* s, int cus) {
+    const bool b_first = l.jobs == 2 && item_us(l.t[1].bm, l.t[1].kb_per_split) > item_us(l.t[0].bm, l.t[0].kb_per_split);
+    l.second_first = b_first;
+    Dispatch d(cus);
+    for (int q = 0; q < l.jobs; ++q) {
+        const int i = b_first ? 1 - q : q;
+        d.run(l.t[i].whole, item_us(l.t[i].bm, s[i].kb));
+        d.run(l.t[i].rest * l.t[i].splits, item_us(l.t[i].bm, l.t[i].kb_per_split));
+    }
+    return d.end() + (l.part_bytes() ? kReduceUs + l.part_bytes() * kPartUs : 0.0);
+}
+
+// The fastest of the candidate tiles and splits.
+Launch search_launch(int jobs, const Kind* kind, int64_t M, int64_t K, int64_t N, int cus) {
+    if (cus <= 0) cus = 256;
+    static const int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
+    Shape s[2];
+    Tiles cand[2][40];
+    int n[2] = {0, 0};
+    for (int i = 0; i < jobs; ++i) {
+        s[i] = shape_of(kind[i], M, K, N);
+        const int sizes[2] = {256, s[i].rows <= 64 && !s[i].strided ? 64 : 128};
+        for (int bm : sizes) {
+            const Tiles t = make_tiles(s[i], bm);
+            const int64_t all = (int64_t)t.tiles_m * t.tiles_n;
+            for (int p : kSplits) {
+                if (p > 1 && (p > s[i].kb / 3 || all * p > 4 * (int64_t)cus)) break;
+                cand[i][n[i]++] = split_tiles(t, s[i].kb, 0, p);
+            }
+            // whole rounds, and the rest of the tiles split to fill one
+            const int64_t rest = all % cus;
+            if (bm == 256 && all > cus && rest > 0 && s[i].kb >= 6)
+                cand[i][n[i]++] = split_tiles(t, s[i].kb, (int)(all - rest),
+                                              (int)std::max<int64_t>(2, std::min<int64_t>(cus / rest, s[i].kb / 3)));
+        }
+    }
+    Launch best{}, l{};
+    double best_us = 1e30;
+    l.jobs = jobs;
+    for (int i = 0; i < n[0]; ++i)
+        for (int j = 0; j < (jobs == 2 ? n[1] : 1); ++j) {
+            l.kind[0] = kind[0];
+            l.t[0] = cand[0][i];
+            if (jobs == 2) {
+                l.kind[1] = kind[1];
+                l.t[1] = cand[1][j];
+                if (l.t[0].bm == 256 && l.t[1].bm != 256) continue;   // no kernel for it
+            }
+            const double us = launch_us(l, s, cus);
+            if (us < best_us) {
+                best_us = us;
+                best = l;
+            }
+        }
+    return best;
+}
+
+// search_launch, remembered by shape (the choice depends on nothing else).
+Launch plan_launch(int jobs, const Kind* kind, int64_t M, int64_t K, int64_t N, int cus) {
+    static std::mutex mu;
+    static std::map<std::array<int64_t, 5>, Launch> seen;
+    const std::array<int64_t, 5> key = {jobs == 2 ? 16 * (kind[1] + 1) + kind[0] : kind[0], M, K, N, cus};
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        const auto it = seen.find(key);
+        if (it != seen.end()) return it->second;
+    }
+    const Launch l = search_launch(jobs, kind, M, K, N, cus);
+    std::lock_guard<std::mutex> lock(mu);
+    if (seen.size() >= 4096) seen.clear();
+    seen[key] = l;
+    return l;
 }
 
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
-
-// The products of the training entry points, their sizes and tiles.
-enum Product { P_FORWARD, P_DUAL_D, P_DA, P_DW, P_DY, P_DW3 };
-
-struct ProductShape {
-    int64_t rows, cols, kb;
-    bool dual, small_ok;
-};
-
-ProductShape shape_of(Product p, int64_t M, int64_t K, int64_t N) {
-    switch (p) {
-        case P_DA: return {M, K, 2 * ceil_div(N, 64), false, true};
-        case P_DW: return {K, 2 * N, ceil_div(M, 64), false, false};
-        case P_DY: return {M, N, ceil_div(K, 64), false, true};
-        case P_DW3: return {N, K, ceil_div(M, 64), false, false};
-        default: return {M, N, ceil_div(K, 64), true, true};   // P_FORWARD, P_DUAL_D
-    }
-}
-
-TilePlan plan_of(Product p, int64_t M, int64_t K, int64_t N, int cus) {
-    const ProductShape s = shape_of(p, M, K, N);
-    return plan_tiles(s.rows, s.cols, s.dual, s.kb, s.small_ok, cus);
-}
-
-int64_t product_part_bytes(Product p, int64_t M, int64_t K, int64_t N, int cus) {
-    const ProductShape s = shape_of(p, M, K, N);
-    return part_bytes(plan_of(p, M, K, N, cus), s.rows, s.cols, s.dual);
-}
-
 int64_t d_bytes(int64_t M, int64_t N) { return align256(M * 2 * N * 2); }
+
+// The launches of a backward pass: D, then the gradients.
+struct Passes {
+    int n = 0;
+    Launch l[3];
+    int64_t part_bytes() const {
+        int64_t b = 0;
+        for (int i = 0; i < n; ++i) b = std::max(b, l[i].part_bytes());
+        return b;
+    }
+};
+// d: D_DUAL, D_DY, or -1 (kept Gate and Up: an element-wise kernel)
+Passes plan_backward(int d, bool da, bool dw, int64_t M, int64_t K, int64_t N, int cus) {
+    Passes p;
+    if (d == D_DY && dw) {
+        const Kind k[2] = {D_DY, G_DW3};
+        p.l[p.n++] = plan_launch(2, k, M, K, N, cus);
+    } else if (d >= 0) {
+        const Kind k[1] = {(Kind)d};
+        p.l[p.n++] = plan_launch(1, k, M, K, N, cus);
+    }
+    const Kind k[2] = {da ? G_DA : G_DW, G_DW};
+    if (da || dw) p.l[p.n++] = plan_launch(da && dw ? 2 : 1, k, M, K, N, cus);
+    return p;
+}
 
 int64_t train_workspace(int64_t M, int64_t K, int64_t N, int cus) {
     int64_t part = 0;
-    for (Product p : {P_FORWARD, P_DUAL_D, P_DA, P_DW, P_DY, P_DW3})
-        part = std::max(part, product_part_bytes(p, M, K, N, cus));
-    return d_bytes(M, N) + part;
+    for (int d : {(int)D_DUAL, (int)D_DY})
+        for (int g = 1; g < 4; ++g) part = std::max(part, plan_backward(d, g & 1, g & 2, M, K, N, cus).part_bytes());
+    const Kind f[1] = {F_KEEP};
+    return d_bytes(M, N) + std::max(part, plan_launch(1, f, M, K, N, cus).part_bytes());
 }
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN, int AOP, int BOP, bool DUAL, int EPI>
-hipError_t launch_gemm_tile(const swt::GemmArgs& a, hipStream_t s) {
-    const void* fn =
-        a.kseg % 64 ? reinterpret_cast<const void*>(&swt::tile_gemm_kernel<BM, BN, WM, WN, AOP, BOP, DUAL, EPI, true>)
-                    : reinterpret_cast<const void*>(&swt::tile_gemm_kernel<BM, BN, WM, WN, AOP, BOP, DUAL, EPI, false>);
-    swt::GemmArgs args = a;
-    void* kargs[] = {&args};
-    const unsigned grid = (unsigned)((int64_t)a.tiles_m * a.tiles_n * a.splits);
-    return hipLaunchKernel(fn, dim3(grid), dim3(64 * WM * WN), kargs, 0, s);
+using swt::OP_KC;
+using swt::OP_KS;
+template <int BM, int EPI>
+using PDual = swt::Product<BM, BM == 256 ? 256 : 128, OP_KC, OP_KS, true, EPI>;
+template <int BM, int EPI>
+using PRows = swt::Product<BM, BM == 256 ? 256 : 128, OP_KC, OP_KC, false, EPI>;    // dA, dY
+template <int BM>
+using PGrad = swt::Product<BM, BM == 256 ? 256 : 128, OP_KS, OP_KS, false, swt::EP_STORE>;   // weight gradients
+
+template <class A, class B>
+hipError_t launch_pair(const Launch& l, swt::GemmArgs a, swt::GemmArgs b, hipStream_t s) {
+    int items[2] = {l.t[0].items(), l.jobs == 2 ? l.t[1].items() : 0};
+    int b_first = l.second_first;
+    void* kargs[] = {&a, &b, &items[0], &items[1], &b_first};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&swt::gemm_kernel<A, B>),
+                                         dim3((unsigned)(items[0] + items[1])), dim3(256), kargs, 0, s);
+    if (e != hipSuccess || l.part_bytes() == 0) return e;
+    auto blocks = [](const Tiles& t, bool dual) {   // four waves a workgroup, one a block (pair)
+        return t.rest * (t.bm / 32) * (t.bn / 32) / (dual ? 2 : 1) / 4;
+    };
+    int na = blocks(l.t[0], A::DUAL);
+    const int nb = l.jobs == 2 ? blocks(l.t[1], false) : 0;
+    void* rargs[] = {&a, &b, &na};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::gemm_reduce_kernel<A, B>), dim3((unsigned)(na + nb)),
+                           dim3(256), rargs, 0, s);
 }
 
-template <int AOP, int BOP, bool DUAL, int EPI>
-hipError_t launch_wide(const swt::GemmArgs& a, int workers, hipStream_t s) {
-    const void* fn = a.kseg % 64 ? reinterpret_cast<const void*>(&swt::wide_gemm_kernel<AOP, BOP, DUAL, EPI, true>)
-                                 : reinterpret_cast<const void*>(&swt::wide_gemm_kernel<AOP, BOP, DUAL, EPI, false>);
-    swt::GemmArgs args = a;
-    const int rest = a.tiles_m * a.tiles_n - a.full;
-    int whole = std::min(a.full, workers);
-    void* kargs[] = {&args, &whole, &workers};
-    hipError_t e = hipLaunchKernel(fn, dim3((unsigned)(whole + (rest ? workers : 0))), dim3(256), kargs, 0, s);
-    if (e != hipSuccess || rest == 0) return e;
-    void* rargs[] = {&args, &workers};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::wide_reduce_kernel<DUAL, EPI>),
-                           dim3((unsigned)(rest * (DUAL ? 8 : 16))), dim3(256), rargs, 0, s);
+template <class A>
+hipError_t launch_with(const Launch& l, const swt::GemmArgs& a, const swt::GemmArgs& b, hipStream_t s) {
+    if (l.jobs == 1) return launch_pair<A, swt::NoProduct>(l, a, b, s);
+    if constexpr (A::EPI == swt::EP_STORE || A::EPI == swt::EP_DY_D) {
+        if constexpr (A::BM == 256) return launch_pair<A, PGrad<256>>(l, a, b, s);
+        else return l.t[1].bm == 256 ? launch_pair<A, PGrad<256>>(l, a, b, s) : launch_pair<A, PGrad<128>>(l, a, b, s);
+    }
+    return hipErrorInvalidValue;
 }
 
-template <int AOP, int BOP, bool DUAL, int EPI>
-hipError_t launch_product(swt::GemmArgs a, const TilePlan& t, hipStream_t s) {
-    a.tiles_m = t.tiles_m;
-    a.tiles_n = t.tiles_n;
-    a.splits = t.splits;
-    a.kb_per_split = t.kb_per_split;
-    a.part_cols = a.cols * (DUAL ? 2 : 1);
-    a.kb_seg = (int)ceil_div(a.kseg, 64);
-    hipError_t e;
-    a.full = t.full;
-    if (t.bm == 256) return launch_wide<AOP, BOP, DUAL, EPI>(a, t.workers, s);
-    if (t.bm == 128) e = launch_gemm_tile<128, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
-    else if constexpr (AOP == swt::OP_KC) e = launch_gemm_tile<64, 128, 2, 2, AOP, BOP, DUAL, EPI>(a, s);
-    else e = hipErrorInvalidValue;
-    if (e != hipSuccess || t.splits == 1) return e;
-    void* kargs[] = {&a};
-    const int64_t groups = (int64_t)a.rows * (a.cols / 8);
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::tile_reduce_kernel<DUAL, EPI>),
-                           dim3((unsigned)std::min<int64_t>(ceil_div(groups, 256), 8192)), dim3(256), kargs, 0, s);
+template <template <int, int> class P, int EPI>
+hipError_t launch_rows(const Launch& l, const swt::GemmArgs& a, const swt::GemmArgs& b, hipStream_t s) {
+    switch (l.t[0].bm) {
+        case 256: return launch_with<P<256, EPI>>(l, a, b, s);
+        case 128: return launch_with<P<128, EPI>>(l, a, b, s);
+        default: return launch_with<P<64, EPI>>(l, a, b, s);
+    }
+}
+
+hipError_t run_launch(const Launch& l, swt::GemmArgs a, swt::GemmArgs b, float* part, hipStream_t s) {
+    swt::GemmArgs* args[2] = {&a, &b};
+    for (int i = 0; i < l.jobs; ++i) {
+        const Tiles& t = l.t[i];
+        args[i]->tiles_m = t.tiles_m;
+        args[i]->tiles_n = t.tiles_n;
+        args[i]->whole = t.whole;
+        args[i]->rest = t.rest;
+        args[i]->splits = t.splits;
+        args[i]->kb_per_split = t.kb_per_split;
+        args[i]->kb_seg = (int)ceil_div(args[i]->kseg, 64);
+        args[i]->part = part;
+        part += t.part_bytes() / 4;
+    }
+    switch (l.kind[0]) {
+        case F_KEEP: return launch_rows<PDual, swt::EP_KEEP>(l, a, b, s);
+        case D_DUAL: return launch_rows<PDual, swt::EP_DUAL_D>(l, a, b, s);
+        case D_DY: return launch_rows<PRows, swt::EP_DY_D>(l, a, b, s);
+        case G_DA: return launch_rows<PRows, swt::EP_STORE>(l, a, b, s);
+        default:
+            return l.t[0].bm == 256 ? launch_pair<PGrad<256>, swt::NoProduct>(l, a, b, s)
+                                    : launch_pair<PGrad<128>, swt::NoProduct>(l, a, b, s);
+    }
 }
 
 struct Call {
     int64_t M, K, N;
-    int cus;
     hipStream_t s;
+    uint16_t* D;
     float* part;
 };
 
-// G, U (dual product) of A and the weights; EPI: EP_KEEP or EP_DUAL_D
+// G, U (dual product) of A and the weights
 swt::GemmArgs dual_args(const Call& c, const uint16_t* A, const uint16_t* W1, const uint16_t* W2) {
     swt::GemmArgs a{};
     a.A0 = A; a.lda = c.K;
     a.B0 = W1; a.B1 = W2; a.ldb = c.N;
     a.rows = (int)c.M; a.cols = (int)c.N;
     a.kseg = (int)c.K; a.segs = 1;
-    a.part = c.part;
     return a;
 }
 
 // dA = dG W1^T + dU W2^T
-hipError_t run_da(const Call& c, const uint16_t* D, const uint16_t* W1, const uint16_t* W2, uint16_t* dA) {
+swt::GemmArgs da_args(const Call& c, const uint16_t* W1, const uint16_t* W2, uint16_t* dA) {
     swt::GemmArgs a{};
-    a.A0 = D; a.A1 = D + c.N; a.lda = 2 * c.N;
+    a.A0 = c.D; a.A1 = c.D + c.N; a.lda = 2 * c.N;
     a.B0 = W1; a.B1 = W2; a.ldb = c.N;
     a.rows = (int)c.M; a.cols = (int)c.K;
     a.kseg = (int)c.N; a.segs = 2;
-    a.part = c.part;
     a.C0 = dA; a.n0_cols = a.ldc = (int)c.K;
-    return launch_product<swt::OP_KC, swt::OP_KC, false, swt::EP_STORE>(a, plan_of(P_DA, c.M, c.K, c.N, c.cus), c.s);
+    return a;
 }
 
-// X^T Z of two token-major matrices: dW1 | dW2 = A^T D, dW3 = Y^T dZ
-hipError_t run_dw(const Call& c, Product p, const uint16_t* X, const uint16_t* Z, uint16_t* C0, uint16_t* C1) {
-    const ProductShape sh = shape_of(p, c.M, c.K, c.N);
+// X^T Z of two token-major matrices of `rows` and `cols` columns: dW1 | dW2 = A^T D
+// (columns from n0_cols on to C1), dW3 = Y^T dZ
+swt::GemmArgs dw_args(const Call& c, const uint16_t* X, int64_t rows, const uint16_t* Z, int64_t cols, int64_t n0_cols,
+                      uint16_t* C0, uint16_t* C1) {
     swt::GemmArgs a{};
-    a.A0 = X; a.lda = sh.rows;
-    a.B0 = Z; a.ldb = sh.cols;
-    a.rows = (int)sh.rows; a.cols = (int)sh.cols;
+    a.A0 = X; a.lda = rows;
+    a.B0 = Z; a.ldb = cols;
+    a.rows = (int)rows; a.cols = (int)cols;
     a.kseg = (int)c.M; a.segs = 1;
-    a.part = c.part;
     a.C0 = C0; a.C1 = C1;
-    a.n0_cols = a.ldc = (int)(p == P_DW ? c.N : c.K);
-    return launch_product<swt::OP_KS, swt::OP_KS, false, swt::EP_STORE>(a, plan_of(p, c.M, c.K, c.N, c.cus), c.s);
+    a.n0_cols = a.ldc = (int)n0_cols;
+    return a;
+}
+
+// dA and dW1, dW2 from D (the last launch of a plan)
+hipError_t run_gradients(const Call& c, const Launch& l, const uint16_t* A, const uint16_t* W1, const uint16_t* W2,
+                         uint16_t* dA, uint16_t* dW1, uint16_t* dW2) {
+    const swt::GemmArgs da = da_args(c, W1, W2, dA);
+    const swt::GemmArgs dw = dw_args(c, A, c.K, c.D, 2 * c.N, c.N, dW1, dW2);
+    return run_launch(l, dA ? da : dw, dw, c.part, c.s);
 }
 
 hipError_t run_zero(uint16_t* p, int64_t elems, hipStream_t s) {
@@ -268,7 +435,8 @@ size_t swiglu_train_workspace_bytes(int64_t M, int64_t K, int64_t N) {
 
 size_t swiglu_train_forward_workspace_bytes(int64_t M, int64_t K, int64_t N) {
     if (check_train_shape(M, K, N) != SWIGLU_OK || M == 0) return 0;
-    return (size_t)product_part_bytes(P_FORWARD, M, K, N, cu_count_now());
+    const Kind f[1] = {F_KEEP};
+    return (size_t)plan_launch(1, f, M, K, N, cu_count_now()).part_bytes();
 }
 
 swiglu_status swiglu_train_forward(const swiglu_bf16* A, const swiglu_bf16* W1, const swiglu_bf16* W2, swiglu_bf16* Y,
@@ -282,14 +450,14 @@ swiglu_status swiglu_train_forward(const swiglu_bf16* A, const swiglu_bf16* W1, 
     b.out(Y, M * N); b.out(G, M * N); b.out(U, M * N);
     if (workspace) b.out(workspace, (int64_t)(workspace_bytes / 2));
     if ((st = b.check()) != SWIGLU_OK) return st;
-    const int cus = cu_count_now();
+    const Kind f[1] = {F_KEEP};
+    const Launch l = plan_launch(1, f, M, K, N, cu_count_now());
     if (!workspace) workspace_bytes = 0;
-    if (workspace_bytes < (size_t)product_part_bytes(P_FORWARD, M, K, N, cus)) return SWIGLU_ERR_WORKSPACE;
-    const Call c{M, K, N, cus, (hipStream_t)stream, (float*)workspace};
+    if (workspace_bytes < (size_t)l.part_bytes()) return SWIGLU_ERR_WORKSPACE;
+    const Call c{M, K, N, (hipStream_t)stream, nullptr, (float*)workspace};
     swt::GemmArgs a = dual_args(c, A, W1, W2);
     a.C0 = Y; a.C1 = G; a.C2 = U;
-    const hipError_t e = launch_product<swt::OP_KC, swt::OP_KS, true, swt::EP_KEEP>(a, plan_of(P_FORWARD, M, K, N, cus),
-                                                                                   c.s);
+    const hipError_t e = run_launch(l, a, a, c.part, c.s);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
 }
 
@@ -316,18 +484,17 @@ swiglu_status swiglu_train_backward(const swiglu_bf16* dY, const swiglu_bf16* A,
     if ((st = b.check()) != SWIGLU_OK) return st;
     const int cus = cu_count_now();
     if (!workspace || workspace_bytes < (size_t)train_workspace(M, K, N, cus)) return SWIGLU_ERR_WORKSPACE;
-    uint16_t* const D = (uint16_t*)workspace;
-    const Call c{M, K, N, cus, (hipStream_t)stream, (float*)((char*)workspace + d_bytes(M, N))};
+    const Call c{M, K, N, (hipStream_t)stream, (uint16_t*)workspace, (float*)((char*)workspace + d_bytes(M, N))};
+    const Passes p = plan_backward(G ? -1 : (int)D_DUAL, dA, dW1, M, K, N, cus);
     hipError_t e;
     if (G) {
-        e = run_dgate(c, dY, G, U, D);
+        e = run_dgate(c, dY, G, U, c.D);
     } else {
         swt::GemmArgs a = dual_args(c, A, W1, W2);
-        a.C0 = D; a.E0 = dY;
-        e = launch_product<swt::OP_KC, swt::OP_KS, true, swt::EP_DUAL_D>(a, plan_of(P_DUAL_D, M, K, N, cus), c.s);
+        a.C0 = c.D; a.E0 = dY;
+        e = run_launch(p.l[0], a, a, c.part, c.s);
     }
-    if (e == hipSuccess && dA) e = run_da(c, D, W1, W2, dA);
-    if (e == hipSuccess && dW1) e = run_dw(c, P_DW, A, D, dW1, dW2);
+    if (e == hipSuccess && (dA || dW1)) e = run_gradients(c, p.l[p.n - 1], A, W1, W2, dA, dW1, dW2);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
 }
 
@@ -357,19 +524,17 @@ swiglu_status swiglu_mlp_train_backward(const swiglu_bf16* dZ, const swiglu_bf16
     if ((st = b.check()) != SWIGLU_OK) return st;
     const int cus = cu_count_now();
     if (!workspace || workspace_bytes < (size_t)train_workspace(M, K, N, cus)) return SWIGLU_ERR_WORKSPACE;
-    uint16_t* const D = (uint16_t*)workspace;
-    const Call c{M, K, N, cus, (hipStream_t)stream, (float*)((char*)workspace + d_bytes(M, N))};
+    const Call c{M, K, N, (hipStream_t)stream, (uint16_t*)workspace, (float*)((char*)workspace + d_bytes(M, N))};
+    const Passes p = plan_backward(D_DY, dA, dW1, M, K, N, cus);
     swt::GemmArgs a{};
     a.A0 = dZ; a.lda = K;
     a.B0 = W3; a.ldb = K;
     a.rows = (int)M; a.cols = (int)N;
     a.kseg = (int)K; a.segs = 1;
-    a.part = c.part;
-    a.C0 = D; a.E0 = G; a.E1 = U;
-    hipError_t e = launch_product<swt::OP_KC, swt::OP_KC, false, swt::EP_DY_D>(a, plan_of(P_DY, M, K, N, cus), c.s);
-    if (e == hipSuccess && dA) e = run_da(c, D, W1, W2, dA);
-    if (e == hipSuccess && dW1) e = run_dw(c, P_DW, A, D, dW1, dW2);
-    if (e == hipSuccess && dW3) e = run_dw(c, P_DW3, Y, dZ, dW3, dW3);
+    a.C0 = c.D; a.E0 = G; a.E1 = U;
+    const swt::GemmArgs dw3 = dw_args(c, Y, N, dZ, K, K, dW3, dW3);
+    hipError_t e = run_launch(p.l[0], a, dw3, c.part, c.s);
+    if (e == hipSuccess && (dA || dW1)) e = run_gradients(c, p.l[p.n - 1], A, W1, W2, dA, dW1, dW2);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
 }
 

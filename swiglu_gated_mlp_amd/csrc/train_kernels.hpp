@@ -8,7 +8,7 @@
 // and for the whole block Z = Y W3:  dY = dZ W3^T,  dW3 = Y^T dZ.
 //
 // All of them are products C[i][j] = sum_k a(i, k) b(j, k) on one tile kernel
-// (tile_gemm_kernel): each operand lies in memory either with k contiguous
+// (gemm_item): each operand lies in memory either with k contiguous
 // (OP_KC: element (i, k) at i * ld + k) or with k strided (OP_KS: at k * ld + i),
 // and no operand is transposed through memory: a k-contiguous tile is read from
 // LDS as it is, a k-strided one with the transposing LDS read.
@@ -36,13 +36,10 @@ namespace swt {
 
 using namespace swk;
 
-// 16 zero bytes that lanes past the end of a contraction read
-__device__ __attribute__((aligned(16))) uint16_t g_zeros[8];
-
 enum Operand : int { OP_KC = 0, OP_KS = 1 };
 
-// What becomes of the sums of 8 adjacent columns (x; dual products: x the G
-// sums and y the U sums of the same columns).
+// What becomes of the sums x (dual products: x the G sums and y the U sums of
+// the same columns).
 enum Epilogue : int {
     EP_STORE = 0,   // C0 (columns < n0_cols) or C1, bf16
     EP_KEEP = 1,    // dual: Y = SiLU(x) y, G = x, U = y
@@ -61,10 +58,10 @@ struct GemmArgs {
     int segs;              // 1 or 2
     int kb_seg;            // ceil(kseg / 64)
     int tiles_m, tiles_n;
-    int splits, kb_per_split;   // contraction blocks (over both segments) per split
-    int full;              // 256-row tiles computed whole (wide_gemm_kernel)
-    float* part;           // split sums [split][rows][part_cols], or pieces' sums
-    int part_cols;         // cols, or 2 cols for a dual product
+    // work items, one workgroup each: tiles 0 .. whole - 1, then the others (rest
+    // of them) in `splits` parts of kb_per_split contraction blocks
+    int whole, rest, splits, kb_per_split;
+    float* part;           // the parts' sums, [split][rest tile]
     // epilogue operands
     uint16_t* C0;          // STORE: columns below n0_cols (row length ldc); KEEP: Y; D kinds: D
     uint16_t* C1;          // STORE: the other columns; KEEP: G
@@ -97,66 +94,30 @@ __device__ __forceinline__ u32x4 pack8(const float (&f)[8]) {
 
 __device__ __forceinline__ void st16(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4*>(p) = v; }
 
-// The epilogue of columns n .. n + 7 of row m (both in range; n a multiple of 8,
-// and every width too, so 8 columns never straddle a matrix's edge).
-template <int EPI>
-__device__ __forceinline__ void finish8(const GemmArgs& p, int m, int n, const float (&x)[8], const float (&y)[8]) {
-    if constexpr (EPI == EP_STORE) {
-        uint16_t* c = n < p.n0_cols ? p.C0 + (size_t)m * p.ldc + n : p.C1 + (size_t)m * p.ldc + (n - p.n0_cols);
-        st16(c, pack8(x));
-    } else if constexpr (EPI == EP_KEEP) {
-        const size_t at = (size_t)m * p.cols + n;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = silu_f(x[e]) * y[e];
-        st16(p.C0 + at, pack8(v));
-        st16(p.C1 + at, pack8(x));
-        st16(p.C2 + at, pack8(y));
-    } else {
-        const size_t at = (size_t)m * p.cols + n;
-        float e0[8], dg[8], du[8];
-        unpack8(ld16(p.E0 + at), e0);
-        if constexpr (EPI == EP_DUAL_D) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) silu_grad(e0[e], x[e], y[e], dg[e], du[e]);
-        } else {
-            float e1[8];
-            unpack8(ld16(p.E1 + at), e1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) silu_grad(x[e], e0[e], e1[e], dg[e], du[e]);
-        }
-        uint16_t* d = p.C0 + (size_t)m * 2 * p.cols + n;
-        st16(d, pack8(dg));
-        st16(d + p.cols, pack8(du));
-    }
+// ---------------------------------------------------------------------------
+// Direct global -> LDS loads, 16 bytes a lane: LDS byte address lds (uniform)
+// + 16 * lane receives the bytes at the descriptor's base + off.  A lane whose
+// offset lies past the descriptor's end gets zeros: that is how k past the end of
+// the contraction, and whole stages past it, become zeros in both operands, at
+// the price of one compare and select a load (addressing such lanes at a chunk of
+// zeros in memory took 64-bit addresses in every lane and 35 % more time).
+//   The load is not tracked by the compiler: with the tracked builtin every
+// transposing LDS read waits for all loads in flight (vmcnt(0)), as it cannot
+// know that they fill other slots.  There is no register to write early; the
+// kernels wait with explicit counts, and the compiler's own waits for loads it
+// does track only wait for more than they must.  (m0, which holds the LDS address,
+// has no other use in these kernels.)
+// ---------------------------------------------------------------------------
+constexpr int RSRC_END = 0x7FFFFFF0;          // every offset of a valid lane is below
+constexpr uint32_t OFF_NONE = 0xFFFFFFF0u;    // past every descriptor's end
+__device__ __forceinline__ i32x4 stage_rsrc(const uint16_t* base, bool valid) {
+    const uint64_t p = (uint64_t)base;
+    return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, valid ? RSRC_END : 0, 0x00020000};
 }
-
-__device__ __forceinline__ void load8(const float* s, float (&x)[8]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(s + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
-    }
-}
-
-__device__ __forceinline__ void store8(float* d, const float (&x)[8]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<f32x4*>(d + 4 * h) = f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
-}
-
-// 8 columns of a finished tile: to the split's sums, or through the epilogue.
-template <bool DUAL, int EPI>
-__device__ __forceinline__ void finish_or_part(const GemmArgs& p, int split, int m, int n, const float (&x)[8],
-                                               const float (&y)[8]) {
-    if (p.splits > 1) {
-        float* d = p.part + ((size_t)split * p.rows + m) * p.part_cols + n;
-        store8(d, x);
-        if constexpr (DUAL) store8(d + p.cols, y);
-    } else {
-        finish8<EPI>(p, m, n, x, y);
-    }
+__device__ __forceinline__ void dma16_buffer(i32x4 rsrc, uint32_t off, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
+                 "s"(rsrc)
+                 : "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -217,7 +178,6 @@ __device__ __forceinline__ void rows_to_block(const u32x4 (&in)[2], float (&v)[1
 // the compiler moved all sums of a wave out of the accumulation registers at
 // once and spilled).
 typedef __amdgpu_buffer_rsrc_t Rsrc;
-constexpr int RSRC_END = 0x7FFFFFF0;
 __device__ __forceinline__ Rsrc corner(const uint16_t* c, long long ld, int m0, int n0) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(c + (size_t)m0 * ld + n0), 0, RSRC_END, 0x00020000);
 }
@@ -227,7 +187,7 @@ struct BlockAt {
     int r, n;
     bool ok[2];
     __device__ __forceinline__ uint32_t at(int h, long long ld) const {
-        return ok[h] ? (uint32_t)((r + 16 * h) * (int)ld + n) * 2 : 0xFFFFFFF0u;
+        return ok[h] ? (uint32_t)((r + 16 * h) * (int)ld + n) * 2 : OFF_NONE;
     }
 };
 __device__ __forceinline__ BlockAt block_at(const GemmArgs& p, int m0, int n0, int r0, int c0, int lane) {
@@ -312,132 +272,233 @@ __device__ __forceinline__ void finish_block(const GemmArgs& p, int m0, int n0, 
 }
 
 // ---------------------------------------------------------------------------
-// One BM x BN tile of sums per workgroup of WM x WN waves (DUAL: BN / 2 columns
-// of each half).  Each wave owns BM/WM x BN/WN of it as 32 x 32 MFMA blocks.
-//   Stages of 64 k, both operands direct to LDS, two stages: the next stage's
-//   loads go out at the start of a stage and have three of its four 16-deep
-//   sub-steps to land; the one barrier per stage sits before the last sub-step,
-//   whose fragments are in registers by then.
-//   Rows or columns past the edge repeat the last ones (their sums are not
-//   stored); k past the end reads the zero chunk in both operands, so nothing
-//   behind a row's end is ever multiplied (RAGGED; only compiled in when the
-//   contraction is not a multiple of 64).
-//   The sums leave through LDS in fp32, so the epilogue works on 8 adjacent
-//   columns a lane: its reads (dY, G, U) and its stores are 16 bytes a lane over
-//   whole row segments.
+// Work items.  A launch holds the items of one product, or of two that do not
+// depend on each other (dA and the weight gradients; dY and dW3), and the
+// dispatcher hands them to CUs as these fall free (an item's LDS fills a CU), so a
+// product of few tiles runs beside the other's, and no CU idles through a last
+// round of one product's tiles (7B width, M=8192: 448 and 2072 tiles on 256 CUs).
+// Where the items would be too few, tiles are split over the contraction.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN>
-constexpr int tile_smem_bytes() {
-    constexpr int stages = 2 * (BM + BN) * BK * 2;
-    constexpr int rpp = BM / WM >= 64 ? 64 : BM / WM;
-    constexpr int stage_f = WM * WN * rpp * (BN / WN + 4) * 4;
-    return stages > stage_f ? stages : stage_f;
+struct ItemAt {
+    int m0, n0, s0, s1;   // corner of the tile, stages [s0, s1)
+    int slot;             // -1: whole tile; else the part's place in `part`
+};
+// The corner of a tile of the grid: down eight row tiles before the next column.
+template <int BM, int BN>
+__device__ __forceinline__ void tile_corner(const GemmArgs& p, int tile, int& m0, int& n0) {
+    constexpr int GROUP_M = 8;
+    const int per_group = GROUP_M * p.tiles_n;
+    const int group = tile / per_group;
+    const int first_m = group * GROUP_M;
+    const int gsize = min(p.tiles_m - first_m, GROUP_M);
+    const int in_group = tile - group * per_group;
+    m0 = (first_m + in_group % gsize) * BM;
+    n0 = in_group / gsize * BN;
+}
+// whole tiles: an XCD holds a contiguous run; parts: all tiles of a split before the next, so an XCD holds a range of
+// the contraction and fetches its piece of both operands once
+template <int BM, int BN>
+__device__ __forceinline__ ItemAt item_at(const GemmArgs& p, int b) {
+    const int KB = p.segs * p.kb_seg;
+    ItemAt it;
+    int tile;
+    if (b < p.whole) {
+        tile = xcd_remap(b, p.whole);
+        it.s0 = 0;
+        it.s1 = KB;
+        it.slot = -1;
+    } else {
+        it.slot = xcd_remap(b - p.whole, p.rest * p.splits);
+        const int split = it.slot / p.rest;
+        tile = p.whole + it.slot - split * p.rest;
+        it.s0 = split * p.kb_per_split;
+        it.s1 = min(KB, it.s0 + p.kb_per_split);   // the host makes no empty part
+    }
+    tile_corner<BM, BN>(p, tile, it.m0, it.n0);
+    // the same in every lane: kept in scalar registers
+    it.m0 = __builtin_amdgcn_readfirstlane(it.m0);
+    it.n0 = __builtin_amdgcn_readfirstlane(it.n0);
+    it.s0 = __builtin_amdgcn_readfirstlane(it.s0);
+    it.s1 = __builtin_amdgcn_readfirstlane(it.s1);
+    it.slot = __builtin_amdgcn_readfirstlane(it.slot);
+    return it;
 }
 
-template <int BM, int BN, int WM, int WN, int AOP, int BOP, bool DUAL, int EPI, bool RAGGED>
-__global__ __launch_bounds__(64 * WM * WN) void tile_gemm_kernel(GemmArgs p) {
-    constexpr int NW = WM * WN;
-    constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-    constexpr int A_INS = BM / 8 / NW, B_INS = BN / 8 / NW;   // 1 KiB direct loads per wave per stage
-    constexpr int STAGE = (BM + BN) * BK;
-    constexpr int GROUP_M = 8;
-    static_assert(TM >= 1 && TN >= 1 && (!DUAL || TN % 2 == 0), "wave tile");
-    static_assert(AOP == OP_KC || BM >= 128, "a k-strided tile has rows of at least 128 elements");
-    static_assert(BOP == OP_KC || BN >= 128, "a k-strided tile has rows of at least 128 elements");
-    __shared__ __attribute__((aligned(16))) unsigned char smem_raw[tile_smem_bytes<BM, BN, WM, WN>()];
-    uint16_t* const smem = reinterpret_cast<uint16_t*>(smem_raw);
-
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave % WM, wn = wave / WM;
-
-    // logical id -> (tile, split); a tile's splits are consecutive, so they stay
-    // on one XCD, and tiles go down GROUP_M row tiles before the next column
-    const int logical = xcd_remap(blockIdx.x, gridDim.x);
-    const int tile = logical / p.splits;
-    const int split = logical - tile * p.splits;
-    int tm, tn;
-    {
-        const int per_group = GROUP_M * p.tiles_n;
-        const int group = tile / per_group;
-        const int first_m = group * GROUP_M;
-        const int gsize = min(p.tiles_m - first_m, GROUP_M);
-        const int in_group = tile - group * per_group;
-        tm = first_m + in_group % gsize;
-        tn = in_group / gsize;
+// A 32 x 32 block of sums as it lies in the lanes: [quad][lane][4].
+__device__ __forceinline__ void store_sums(float* d, const f32x16& a) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(d + q * 256) = f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+}
+__device__ __forceinline__ void add_sums(const float* s, f32x16& a) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(s + q * 256);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[4 * q + e] += v[e];
     }
-    const int m0 = tm * BM;
-    const int n0 = tn * (DUAL ? BN / 2 : BN);
-    const int s_first = split * p.kb_per_split;
-    const int s_end = min(p.segs * p.kb_seg, s_first + p.kb_per_split);   // the host makes no empty split
+}
 
-    // per-lane byte offsets from the stage's base, constant over the stages:
-    // k-contiguous operand: 8 rows x 128 bytes a load, chunks swizzled by row;
-    // k-strided: whole k rows of the tile's columns, chunks swizzled by k
+// ---------------------------------------------------------------------------
+// A BM x BN item, four waves (2 x 2) of BM/2 x BN/2 sums each (DUAL: BN / 2
+// columns of each half, each wave BN/4 of either).
+//   256 x 256 (all 256 accumulation registers of a wave): 64 KiB go into a CU per
+// 64-deep stage of 2048 matrix-core cycles, and what bounds it is having them in
+// flight early enough.  Two whole stages are 128 of the 160 KiB of LDS, so the
+// ring is made of five 32 KiB half stages (one operand's 256 x 64 each): stage s's
+// b goes out as soon as stage s - 2 has been read, a whole stage before it is
+// needed, and its a another three sub-steps earlier, into the fifth slot.
+//   Smaller tiles, for few rows: there a product is a chain of load latencies (a
+// 128 x 128 stage has 512 matrix-core cycles, its loads take four times as long),
+// so the ring holds five or six whole stages, all but one of them in flight.
+//   In both, each 16-deep sub-step is a fixed (fenced) sequence of matrix
+// instructions with the next sub-step's fragment reads and a share of the loads
+// between them; the waits are explicit: fragments at the start of the sub-step
+// that uses them, loads before the stage's one barrier, where only those not
+// needed by the next stage may be in flight.  Every stage issues the same loads
+// (past the end they give zeros), so the counts hold.
+//   Rows or columns past the edge repeat the last ones; their sums are not stored.
+//   LDS tiles: k-contiguous [rows][64], chunks swizzled by row (lds_off);
+// k-strided [64][columns], chunks swizzled by k (rm_off; DUAL: one [64][BN / 2]
+// tile for each half).
+// ---------------------------------------------------------------------------
+template <int BM_, int BN_, int AOP_, int BOP_, bool DUAL_, int EPI_>
+struct Product {
+    static constexpr int BM = BM_, BN = BN_, AOP = AOP_, BOP = BOP_, EPI = EPI_;
+    static constexpr bool DUAL = DUAL_;
+    static constexpr int TM = BM / 64, TN = BN / 64;   // a wave's blocks
+    static constexpr int COLS = DUAL ? BN / 2 : BN;    // output columns of a tile
+    static_assert(!DUAL || TN % 2 == 0, "a wave holds both halves of its columns");
+};
+constexpr int LDS_BYTES = 163840;
+
+// element offset in a k-strided LDS tile of COLS columns (rm_off; rows of 64
+// columns are 128 bytes, where the lowest bit of k alone is free to swizzle with)
+template <int COLS>
+__device__ __forceinline__ int ks_off(int k, int col) {
+    return COLS >= 128 ? rm_off<COLS>(k, col) : k * COLS + (((col >> 3) ^ ((k & 1) << 2)) << 3) + (col & 7);
+}
+
+template <class P>
+__device__ __forceinline__ void gemm_item(const GemmArgs& p, uint16_t* smem, int b) {
+    constexpr int BM = P::BM, BN = P::BN, AOP = P::AOP, BOP = P::BOP, TM = P::TM, TN = P::TN;
+    constexpr bool DUAL = P::DUAL;
+    constexpr bool HALVES = BM == 256 && BN == 256;   // the ring of half stages
+    constexpr int A_INS = BM / 32, B_INS = BN / 32;   // 1 KiB loads per wave and stage
+    constexpr int A_ELEMS = BM * BK, B_ELEMS = BN * BK;
+    constexpr int NS = HALVES ? 2 : (LDS_BYTES / 2 / (A_ELEMS + B_ELEMS) < 6 ? LDS_BYTES / 2 / (A_ELEMS + B_ELEMS) : 6);
+    constexpr int BCOL = DUAL ? BN / 2 : BN;          // columns of a k-strided b tile in LDS
+    static_assert(AOP == OP_KC || BM >= 128, "a k-strided tile has rows of at least 128 elements");
+    static_assert(BOP == OP_KC || BCOL >= 64, "a k-strided tile has rows of at least 64 elements");
+    static_assert(HALVES || (NS - 2) * (A_INS + B_INS) <= 63, "vmcnt range");
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int hi5 = lane >> 5;
+    const ItemAt it = item_at<BM, P::COLS>(p, b);
+    const int m0 = it.m0, n0 = it.n0;
+
+    // Byte offsets of a lane's 16 bytes in load i from the stage's base, constant
+    // over the stages, and the lane's (first) k within the stage.  k-contiguous:
+    // 8 rows x 128 bytes a load; k-strided: whole k rows of the tile's columns.
     uint32_t a_off[A_INS], b_off[B_INS];
-    int a_k[A_INS], b_k[B_INS];   // RAGGED: the load's (first) k within the stage
+    auto kc_k = [&](int q) { return 8 * ((lane & 7) ^ swz(q * 8 + (lane >> 3))); };
+    auto ks_k = [&](int q, int cols) { return q * (512 / cols) + lane / (cols / 8); };
+    auto ks_c = [&](int q, int cols) {   // logical column of the lane's chunk
+        const int k = ks_k(q, cols);
+        return 8 * ((lane % (cols / 8)) ^ (cols >= 128 ? (k & 3) << 2 : (k & 1) << 2));
+    };
 #pragma unroll
     for (int i = 0; i < A_INS; ++i) {
         const int q = wave * A_INS + i;
-        if constexpr (AOP == OP_KC) {
-            const int r = q * 8 + (lane >> 3), c = (lane & 7) ^ swz(r);
-            a_off[i] = (uint32_t)((min(m0 + r, p.rows - 1) - m0) * p.lda + 8 * c) * 2;
-            a_k[i] = 8 * c;
-        } else {
-            constexpr int CPR = BM / 8, RPI = 64 / CPR;
-            const int r = q * RPI + lane / CPR, c = 8 * ((lane % CPR) ^ ((r & 3) << 2));
-            a_off[i] = (uint32_t)(r * p.lda + min(m0 + c, p.rows - 8) - m0) * 2;
-            a_k[i] = r;
-        }
+        a_off[i] = AOP == OP_KC ? (uint32_t)((min(m0 + q * 8 + (lane >> 3), p.rows - 1) - m0) * p.lda + kc_k(q)) * 2
+                                : (uint32_t)(ks_k(q, BM) * p.lda + min(m0 + ks_c(q, BM), p.rows - 8) - m0) * 2;
     }
-    const uint16_t* b_half[B_INS];   // dual: which half's matrix a load reads
+    // dual: waves 0, 1 load the first half, waves 2, 3 the second
+    auto b_q = [&](int i) { return DUAL ? (wave & 1) * B_INS + i : wave * B_INS + i; };
 #pragma unroll
     for (int i = 0; i < B_INS; ++i) {
-        const int q = wave * B_INS + i;
-        b_half[i] = p.B0;
-        if constexpr (BOP == OP_KC) {
-            const int r = q * 8 + (lane >> 3), c = (lane & 7) ^ swz(r);
-            b_off[i] = (uint32_t)((min(n0 + r, p.cols - 1) - n0) * p.ldb + 8 * c) * 2;
-            b_k[i] = 8 * c;
-        } else {
-            constexpr int CPR = BN / 8, RPI = 64 / CPR;
-            const int r = q * RPI + lane / CPR, c = 8 * ((lane % CPR) ^ ((r & 3) << 2));
-            const bool up = DUAL && c >= BN / 2;
-            const int cc = up ? c - BN / 2 : c;
-            b_off[i] = (uint32_t)(r * p.ldb + min(n0 + cc, p.cols - 8) - n0) * 2;
-            b_k[i] = r;
-            if (up) b_half[i] = p.B1;
-        }
+        const int q = b_q(i);
+        b_off[i] = BOP == OP_KC ? (uint32_t)((min(n0 + q * 8 + (lane >> 3), p.cols - 1) - n0) * p.ldb + kc_k(q)) * 2
+                                : (uint32_t)(ks_k(q, BCOL) * p.ldb + min(n0 + ks_c(q, BCOL), p.cols - 8) - n0) * 2;
     }
 
-    auto issue = [&](int s, int buf) {
-        uint16_t* sA = smem + buf * STAGE;
-        uint16_t* sB = sA + BM * BK;
+    // descriptor of an operand's stage s
+    auto rsrc_of = [&](bool isb, int s) __attribute__((always_inline)) {
         const int seg = s >= p.kb_seg ? 1 : 0;
         const int k0 = (s - seg * p.kb_seg) * BK;
-        const int left = p.kseg - k0;   // k left in the segment, > 0
-        const char* a_base = reinterpret_cast<const char*>(
-            (seg ? p.A1 : p.A0) + (AOP == OP_KC ? (size_t)m0 * p.lda + k0 : (size_t)k0 * p.lda + m0));
-        const size_t b_at = BOP == OP_KC ? (size_t)n0 * p.ldb + k0 : (size_t)k0 * p.ldb + n0;
+        const int op = isb ? BOP : AOP;
+        const long long ld = isb ? p.ldb : p.lda;
+        const int r0 = isb ? n0 : m0;
+        const uint16_t* m = isb ? ((DUAL ? wave >= 2 : seg) ? p.B1 : p.B0) : (seg ? p.A1 : p.A0);
+        return stage_rsrc(m + (op == OP_KC ? (size_t)r0 * ld + k0 : (size_t)k0 * ld + r0), s < it.s1);
+    };
+    auto left_of = [&](int s) { return p.kseg - (s >= p.kb_seg ? s - p.kb_seg : s) * BK; };
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_ptr)smem;
+    // load i of an operand's stage (its descriptor, k left in it) to LDS element dst
+    auto load_a = [&](i32x4 rsrc, int left, int i, int dst) __attribute__((always_inline)) {
+        const int q = wave * A_INS + i;
+        const int k = AOP == OP_KC ? kc_k(q) : ks_k(q, BM);
+        dma16_buffer(rsrc, k < left ? a_off[i] : OFF_NONE, lds0 + (uint32_t)(dst + q * 512) * 2);
+    };
+    auto load_b = [&](i32x4 rsrc, int left, int i, int dst) __attribute__((always_inline)) {
+        const int q = b_q(i);
+        const int k = BOP == OP_KC ? kc_k(q) : ks_k(q, BCOL);
+        dma16_buffer(rsrc, k < left ? b_off[i] : OFF_NONE,
+                     lds0 + (uint32_t)(dst + (DUAL && wave >= 2 ? B_ELEMS / 2 : 0) + q * 512) * 2);
+    };
+
+    // Fragment addresses: a few lane offsets and constants.  k-contiguous: rows
+    // w + 32i + (l & 31), chunk (2kk + (l >> 5)) ^ swz(row), and
+    // swz(32i + r) = swz(r) ^ 4 (i & 1): four bases x = kk ^ 2 (i & 1).
+    // k-strided: k row 16kk + 8 (l >> 5) + (l & 15) / 4, whose low bits fix the
+    // swizzle for the lane: one base per block.
+    uint32_t a_base[4], b_base[4];
+    const int tr_k = 8 * hi5 + ((lane & 15) >> 2), tr_c = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    auto kc_base = [&](int x, int row0) {
+        const int r = lane & 31;
+        return (uint32_t)(row0 * 128 + r * 128 + (((hi5 ^ swz(row0 + r)) ^ (2 * x)) << 4));
+    };
 #pragma unroll
-        for (int i = 0; i < A_INS; ++i) {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(a_base + a_off[i]);
-            if constexpr (RAGGED) {
-                if (a_k[i] >= left) src = g_zeros;
-            }
-            dma16(src, sA + (wave * A_INS + i) * 512);
+    for (int x = 0; x < 4; ++x) {
+        a_base[x] = AOP == OP_KC ? kc_base(x, wm * (BM / 2))
+                                 : (uint32_t)rm_off<BM>(tr_k, wm * (BM / 2) + (x < TM ? x : 0) * 32 + tr_c) * 2;
+        if constexpr (BOP == OP_KC) {
+            b_base[x] = kc_base(x, wn * (BN / 2));
+        } else {
+            const int j = x < TN ? x : 0;
+            const int half = DUAL ? j / (TN / 2 > 0 ? TN / 2 : 1) : 0;
+            const int col = DUAL ? wn * (BN / 4) + j % (TN / 2 > 0 ? TN / 2 : 1) * 32 : wn * (BN / 2) + j * 32;
+            b_base[x] = (uint32_t)(half * (B_ELEMS / 2) + ks_off<BCOL>(tr_k, col + tr_c)) * 2;
         }
-#pragma unroll
-        for (int i = 0; i < B_INS; ++i) {
-            const uint16_t* base = DUAL ? b_half[i] : (seg ? p.B1 : p.B0);
-            const uint16_t* src =
-                reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(base + b_at) + b_off[i]);
-            if constexpr (RAGGED) {
-                if (b_k[i] >= left) src = g_zeros;
-            }
-            dma16(src, sB + (wave * B_INS + i) * 512);
+    }
+    auto read_frag = [&](auto opc, auto colsc, const uint32_t (&base)[4], uint32_t so, int kk, int i) -> bf16x8 {
+        constexpr int OP = decltype(opc)::value;
+        constexpr int COLS = decltype(colsc)::value;
+        const char* sm = reinterpret_cast<const char*>(smem) + so;
+        if constexpr (OP == OP_KC) {
+            return *reinterpret_cast<const bf16x8*>(sm + i * 4096 + base[kk ^ (2 * (i & 1))]);
+        } else {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(sm + kk * (16 * COLS * 2) + base[i]);
+            const s16x4 both[2] = {ds_read_tr16(q), ds_read_tr16(q + 4 * COLS)};
+            return __builtin_bit_cast(bf16x8, both);
         }
+    };
+    bf16x8 fa[2][TM], fb[2][TN];
+    auto read_a = [&](uint32_t so, int kk, int i, int set) {
+        fa[set][i] = read_frag(std::integral_constant<int, AOP>{}, std::integral_constant<int, BM>{}, a_base, so, kk, i);
+    };
+    auto read_b = [&](uint32_t so, int kk, int j, int set) {
+        fb[set][j] =
+            read_frag(std::integral_constant<int, BOP>{}, std::integral_constant<int, BCOL>{}, b_base, so, kk, j);
+    };
+    // a byte offset in LDS, opaque so that addresses are formed from the lane bases
+    // instead of being kept for every slot
+    auto opaque = [](int elems) {
+        uint32_t so = (uint32_t)elems * 2;
+        asm volatile("" : "+s"(so));
+        return so;
     };
 
     f32x16 acc[TM][TN];
@@ -447,516 +508,223 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_gemm_kernel(GemmArgs p) {
         for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    using Set0 = std::integral_constant<int, 0>;
+    using Set1 = std::integral_constant<int, 1>;
 
-    // fragments: lane l holds row (l & 31) of the block and the 8 k from
-    // 16kk + 8(l >> 5); the transposing read takes two reads of 4 k each
-    bf16x8 fa[2][TM], fb[2][TN];
-    const int tr_k = 8 * (lane >> 5) + ((lane & 15) >> 2);
-    const int tr_c = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-    auto frag = [&](auto opc, auto widthc, const uint16_t* s, int row, int kk) -> bf16x8 {
-        constexpr int OP = decltype(opc)::value;
-        constexpr int W = decltype(widthc)::value;
-        if constexpr (OP == OP_KC) {
-            return *reinterpret_cast<const bf16x8*>(s + lds_off(row + (lane & 31), 2 * kk + (lane >> 5)));
-        } else {
-            const s16x4 both[2] = {ds_read_tr16(s + rm_off<W>(16 * kk + tr_k, row + tr_c)),
-                                   ds_read_tr16(s + rm_off<W>(16 * kk + tr_k + 4, row + tr_c))};
-            return __builtin_bit_cast(bf16x8, both);
-        }
-    };
-    auto read_frags = [&](int buf, int kk, int set) {
-        const uint16_t* sA = smem + buf * STAGE;
-        const uint16_t* sB = sA + BM * BK;
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            fa[set][i] = frag(std::integral_constant<int, AOP>{}, std::integral_constant<int, BM>{}, sA,
-                              wm * (BM / WM) + i * 32, kk);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int col = DUAL ? (j >= TN / 2 ? BN / 2 : 0) + wn * (BN / WN / 2) + (j % (TN / 2 > 0 ? TN / 2 : 1)) * 32
-                                 : wn * (BN / WN) + j * 32;
-            fb[set][j] =
-                frag(std::integral_constant<int, BOP>{}, std::integral_constant<int, BN>{}, sB, col, kk);
-        }
-    };
-    auto mfmas = [&](int set) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
-    };
-
-    issue(s_first, 0);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    read_frags(0, 0, 0);
-    for (int s = s_first; s < s_end; ++s) {
-        const int buf = (s - s_first) & 1;
-        const bool more = s + 1 < s_end;
-        if (more) issue(s + 1, buf ^ 1);
-        read_frags(buf, 1, 1);
-        mfmas(0);
-        read_frags(buf, 2, 0);
-        mfmas(1);
-        read_frags(buf, 3, 1);
-        mfmas(0);
-        // the next stage has landed and every wave has read this one
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        if (more) read_frags(buf ^ 1, 0, 0);
-        mfmas(1);
-    }
-
-    // ---- the sums through LDS (fp32), 8 adjacent columns a lane ------------------
-    constexpr int CW = BN / WN;                         // staged columns per wave (dual: G half, then U half)
-    constexpr int PW = CW + 4;                          // pitch: 16 bytes of padding per row
-    constexpr int RPP = BM / WM >= 64 ? 64 : BM / WM;   // rows per pass
-    constexpr int OW = DUAL ? CW / 2 : CW;              // output columns per wave
-    constexpr int LPR = OW / 8;                         // lanes per row
-    constexpr int RPI = 64 / LPR;                       // rows per wave step
-    float* const st = reinterpret_cast<float*>(smem_raw) + wave * RPP * PW;
-    const int row_base = m0 + wm * (BM / WM);
-    const int col_base = n0 + wn * OW;
-#pragma unroll
-    for (int ps = 0; ps < BM / WM / RPP; ++ps) {
-        __syncthreads();
-#pragma unroll
-        for (int ii = 0; ii < RPP / 32; ++ii)
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x16& a = acc[ps * (RPP / 32) + ii][j];
-                    *reinterpret_cast<f32x4*>(st + (ii * 32 + (lane & 31)) * PW + j * 32 + 8 * q + 4 * (lane >> 5)) =
-                        f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
-                }
-        __syncthreads();
-        for (int t = 0; t < RPP / RPI; ++t) {
-            const int r = t * RPI + lane / LPR, c = 8 * (lane % LPR);
-            const int m = row_base + ps * RPP + r, n = col_base + c;
-            float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            load8(st + r * PW + c, x);
-            if constexpr (DUAL) load8(st + r * PW + OW + c, y);
-            if (m < p.rows && n < p.cols) finish_or_part<DUAL, EPI>(p, split, m, n, x, y);
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// The same product on 256 x 256 tiles (dual: 128 columns of each half), for
-// outputs large enough to fill the CUs with them.  4 waves, 2 x 2, own 128 x 128
-// sums each, all 256 accumulation registers of a wave.
-//   A tile moves 64 KiB into a CU per 64-deep stage for 2048 matrix-core cycles;
-//   what bounds it is having those loads in flight early enough.  Two whole
-//   stages are 128 of the 160 KiB of LDS, so the ring is made of five 32 KiB half
-//   stages (one operand's 256 x 64 each): stage s's b goes out as soon as stage
-//   s - 2 has been read, a whole stage before it is needed, and its a another
-//   three sub-steps earlier, into the fifth slot.
-//   Each 16-deep sub-step is a fixed sequence (fenced, four matrix instructions
-//   at a time) with the next sub-step's fragment reads and a share of the loads
-//   between them; the waits are explicit: fragments at the start of the sub-step
-//   that uses them, loads before the stage's one barrier, where only the a loads
-//   of the stage after next may still be in flight.  Stages past the end load
-//   the zero chunk, so every stage issues the same loads and the counts hold.
-// ---------------------------------------------------------------------------
-constexpr int WIDE_SLOT = 256 * BK;   // elements of a half stage
-
-// Direct global -> LDS load of 16 bytes a lane that the compiler does not track:
-// LDS byte address lds (uniform) + 16 * lane receives the lane's bytes.  With the
-// tracked builtin, every transposing LDS read waits for all loads in flight
-// (vmcnt(0)): it cannot know that they fill other slots.  There is no register to
-// write early; the kernel waits with explicit counts, and the compiler's own
-// waits for loads it does track only wait for more than they must.  (m0, which
-// holds the LDS address, has no other use in the kernel.)
-__device__ __forceinline__ void dma16_uniform(const uint16_t* base, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory");
-}
-__device__ __forceinline__ void dma16_lane(const uint16_t* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(src)
-                 : "memory");
-}
-
-// Work of one launch: the first workgroups, one per CU, compute tiles 0 .. full - 1
-// whole, tile after tile, and start the next tile's loads before the epilogue of
-// the last.  The R stages of the remaining tiles, fewer than there are CUs, are
-// dealt out evenly to W further workgroups, which start as CUs fall free: worker w
-// takes stages [w R / W, (w + 1) R / W) in order, at most two pieces, each the sums
-// of part of one tile, which go to memory and are added by wide_reduce_kernel.  So
-// no CU idles through a last round of whole tiles (448 tiles on 256 CUs), and
-// outputs of a few tiles fill the CUs too.
-struct WideRest {
-    int pieces, tile, s0, s_first, s_second, slot;
-};
-__device__ __forceinline__ WideRest wide_rest(const GemmArgs& p, int KB, int W, int w) {
-    const long long R = (long long)(p.tiles_m * p.tiles_n - p.full) * KB;
-    const long long r0 = R * w / W, r1 = R * (w + 1) / W;
-    WideRest r;
-    r.tile = (int)(r0 / KB);
-    r.s0 = (int)(r0 - (long long)r.tile * KB);
-    const int len = (int)(r1 - r0);   // <= KB
-    r.s_first = min(KB, r.s0 + len);
-    r.s_second = r.s0 + len - KB;
-    r.pieces = len == 0 ? 0 : (r.s_second > 0 ? 2 : 1);
-    r.slot = 2 * w;
-    return r;
-}
-
-// Whole tiles first, first + stride, ... < total (PIECES: the pieces of worker
-// first of stride workers), one after another in one workgroup.
-template <int AOP, int BOP, bool DUAL, int EPI, bool RAGGED, bool PIECES>
-__device__ __forceinline__ void wide_tiles(const GemmArgs& p, uint16_t* smem, int first, int stride, int total) {
-    constexpr int INS = 8;   // 1 KiB direct loads per wave and half stage
-    constexpr int GROUP_M = 8;
-
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave & 1, wn = wave >> 1;
-
-    const int KB = p.segs * p.kb_seg;
-    WideRest rest{};
-    if constexpr (PIECES) rest = wide_rest(p, KB, stride, xcd_remap(first, stride));
-    const int nitems = PIECES ? rest.pieces : (total - first + stride - 1) / stride;
-    if (nitems <= 0) return;
-    struct Item {
-        int m0, n0, s0, s1;   // stages [s0, s1)
-    };
-    auto item_of = [&](int k) __attribute__((always_inline)) {
-        Item it;
-        int tile;
-        if constexpr (PIECES) {
-            tile = p.full + rest.tile + k;
-            it.s0 = k ? 0 : rest.s0;
-            it.s1 = k ? rest.s_second : rest.s_first;
-        } else {
-            tile = xcd_remap(first + k * stride, total);
-            it.s0 = 0;
-            it.s1 = KB;
-        }
-        const int per_group = GROUP_M * p.tiles_n;
-        const int group = tile / per_group;
-        const int first_m = group * GROUP_M;
-        const int gsize = min(p.tiles_m - first_m, GROUP_M);
-        const int in_group = tile - group * per_group;
-        it.m0 = (first_m + in_group % gsize) * 256;
-        it.n0 = (in_group / gsize) * (DUAL ? 128 : 256);
-        return it;
-    };
-
-    // Byte offsets of a lane's 16 bytes in load i from the stage's base.
-    // k-contiguous: load q = 8 wave + i brings rows 8q .. 8q + 7, lane l's chunk
-    // is (l & 7) ^ (l >> 3) ^ (q & 7) (lds_off's swizzle); k-strided: k rows 2q
-    // and 2q + 1, columns 8 ((l & 31) ^ 4 (k & 3)) (rm_off's).
-    uint32_t a_off[INS], b_off[INS];
-    int m0 = 0, n0 = 0, s_end = 0;   // of the item that the loads fetch
-    const int hi5 = lane >> 5;
-    auto ks_chunk = [&](int i) { return (lane & 31) ^ ((2 * (i & 1) + hi5) << 2); };
-    // valid: false past the last item, whose loads then all read the zero chunk
-    auto load_item = [&](const Item& it, bool valid) __attribute__((always_inline)) {
-        m0 = it.m0;
-        n0 = it.n0;
-        s_end = valid ? it.s1 : 0;
-#pragma unroll
-    for (int i = 0; i < INS; ++i) {
-        const int q = wave * INS + i;
-        const int kc = 8 * ((lane & 7) ^ (lane >> 3) ^ i);
-        if constexpr (AOP == OP_KC)
-            a_off[i] = (uint32_t)((min(m0 + q * 8 + (lane >> 3), p.rows - 1) - m0) * p.lda + kc) * 2;
-        else
-            a_off[i] = (uint32_t)((2 * q + hi5) * p.lda + min(m0 + 8 * ks_chunk(i), p.rows - 8) - m0) * 2;
-        if constexpr (BOP == OP_KC)
-            b_off[i] = (uint32_t)((min(n0 + q * 8 + (lane >> 3), p.cols - 1) - n0) * p.ldb + kc) * 2;
-        else
-            b_off[i] = (uint32_t)((2 * q + hi5) * p.ldb +
-                                  min(n0 + 8 * (ks_chunk(i) & (DUAL ? 15 : 31)), p.cols - 8) - n0) * 2;
-    }
-    };
-    // dual: the lanes of a load's second half read the other matrix
-    const uint16_t* const b_lane = (DUAL && (lane & 16)) ? p.B1 : p.B0;
-    // the first k of a lane's chunk within the stage (RAGGED)
-    const int kc_x = 8 * ((lane & 7) ^ (lane >> 3));
-    auto lane_k = [&](int op, int i) { return op == OP_KC ? kc_x ^ (8 * i) : 2 * (wave * INS + i) + hi5; };
-
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void_ptr)smem;
-    // load i of operand a (or b) of stage s into ring slot `slot`
-    auto issue = [&](auto bc, int s, int slot, int i) __attribute__((always_inline)) {
-        constexpr bool ISB = decltype(bc)::value;
-        constexpr int OP = ISB ? BOP : AOP;
-        const bool valid = s < s_end;
-        const int seg = s >= p.kb_seg ? 1 : 0;
-        const int k0 = (s - seg * p.kb_seg) * BK;
-        const long long ld = ISB ? p.ldb : p.lda;
-        const int r0 = ISB ? n0 : m0;
-        const uint32_t off = ISB ? b_off[i] : a_off[i];
-        const size_t at = OP == OP_KC ? (size_t)r0 * ld + k0 : (size_t)k0 * ld + r0;
-        const uint32_t dst = lds0 + (uint32_t)(slot * WIDE_SLOT + (wave * INS + i) * 512) * 2;
-        if constexpr (!RAGGED && !(ISB && DUAL)) {
-            const uint16_t* m = ISB ? (seg ? p.B1 : p.B0) : (seg ? p.A1 : p.A0);
-            dma16_uniform(valid ? m + at : g_zeros, off & (valid ? 0xffffffffu : 0u), dst);
-        } else {
-            const uint16_t* m = ISB ? (DUAL ? b_lane : (seg ? p.B1 : p.B0)) : (seg ? p.A1 : p.A0);
-            const uint16_t* src =
-                reinterpret_cast<const uint16_t*>(reinterpret_cast<const char*>(m + at) + off);
-            if (!valid || (RAGGED && k0 + lane_k(OP, i) >= p.kseg)) src = g_zeros;
-            dma16_lane(src, dst);
-        }
-    };
-    using A_ = std::false_type;
-    using B_ = std::true_type;
-
-    // Fragment addresses: a few lane offsets and constants.  k-contiguous: rows
-    // w*128 + 32i + (l & 31), chunk (2kk + (l >> 5)) ^ swz(row), and
-    // swz(32i + r) = swz(r) ^ 4 (i & 1): four bases x = kk ^ 2 (i & 1).
-    // k-strided: k row 16kk + 8 (l >> 5) + (l & 15) / 4, whose low bits fix the
-    // swizzle for the lane, columns w*128 + 32i + ...: four bases, one per i.
-    auto frag_bases = [&](int op, int w, bool dual, uint32_t (&base)[4]) {
-        if (op == OP_KC) {
-            const int r = lane & 31, hs = hi5 ^ swz(r);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) base[x] = (uint32_t)(w * 128 * 128 + r * 128 + ((hs ^ (2 * x)) << 4));
-        } else {
-            const int k = 8 * hi5 + ((lane & 15) >> 2);
-            const int c = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    if constexpr (HALVES) {
+        constexpr int SLOT = 256 * BK;   // elements of a half stage
+        // one 16-deep sub-step on fragment set CUR: 16 matrix instructions, the
+        // next sub-step's reads (rkk of the slots at aso, bso) in its first half,
+        // and NLD loads a quarter from load l0 on
+        auto substep = [&](auto curc, uint32_t aso, uint32_t bso, int rkk, auto ldbc, auto nldc, i32x4 rsrc, int left,
+                           int dst, int l0) __attribute__((always_inline)) {
+            constexpr int CUR = decltype(curc)::value;
+            constexpr bool LDB = decltype(ldbc)::value;
+            constexpr int NLD = decltype(nldc)::value;
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int col = dual ? (i >> 1) * 128 + w * 64 + (i & 1) * 32 : w * 128 + i * 32;
-                base[i] = (uint32_t)rm_off<256>(k, col + c) * 2;
-            }
-        }
-    };
-    uint32_t a_base[4], b_base[4];
-    frag_bases(AOP, wm, false, a_base);
-    frag_bases(BOP, wn, DUAL, b_base);
-    bf16x8 fa[2][4], fb[2][4];
-    auto read_one = [&](int op, const uint32_t (&base)[4], uint32_t so, int kk, int i) -> bf16x8 {
-        const char* sm = reinterpret_cast<const char*>(smem) + so;
-        if (op == OP_KC)
-            return *reinterpret_cast<const bf16x8*>(sm + i * 4096 + base[kk ^ (2 * (i & 1))]);
-        const uint16_t* q = reinterpret_cast<const uint16_t*>(sm + kk * 8192 + base[i]);
-        const s16x4 both[2] = {ds_read_tr16(q), ds_read_tr16(q + 1024)};
-        return __builtin_bit_cast(bf16x8, both);
-    };
-    // byte offset of a ring slot, opaque so that addresses are formed from the
-    // lane bases instead of being kept for every slot
-    auto slot_off = [&](int slot) {
-        uint32_t so = (uint32_t)slot * (WIDE_SLOT * 2);
-        asm volatile("" : "+s"(so));
-        return so;
-    };
-
-    f32x16 acc[4][4];
-    auto zero_acc = [&]() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[CUR][j], fa[CUR][i], acc[i][j], 0, 0, 0);
+                if (i < 2) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-    };
-
-    // one 16-deep sub-step on fragment set CUR: 16 matrix instructions, the next
-    // sub-step's reads (sub-step rkk of the slots at aso, bso) in its first half,
-    // and NLD loads per quarter of operand LB from load l0 on
-    auto substep = [&](auto curc, uint32_t aso, uint32_t bso, int rkk, auto bc, auto nldc, int ls, int lslot, int l0) {
-        constexpr int CUR = decltype(curc)::value;
-        constexpr int NLD = decltype(nldc)::value;
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[CUR][j], fa[CUR][i], acc[i][j], 0, 0, 0);
-            if (i < 2) {
-#pragma unroll
-                for (int t = 2 * i; t < 2 * i + 2; ++t) {
-                    fa[CUR ^ 1][t] = read_one(AOP, a_base, aso, rkk, t);
-                    fb[CUR ^ 1][t] = read_one(BOP, b_base, bso, rkk, t);
+                    for (int t = 2 * i; t < 2 * i + 2; ++t) {
+                        read_a(aso, rkk, t, CUR ^ 1);
+                        read_b(bso, rkk, t, CUR ^ 1);
+                    }
                 }
+#pragma unroll
+                for (int t = 0; t < NLD; ++t) {
+                    if constexpr (LDB) load_b(rsrc, left, l0 + i * NLD + t, dst);
+                    else load_a(rsrc, left, l0 + i * NLD + t, dst);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        using N0 = std::integral_constant<int, 0>;
+        using N1 = std::integral_constant<int, 1>;
+        using N2 = std::integral_constant<int, 2>;
+        using LA = std::false_type;
+        using LB = std::true_type;
+        auto wrap = [](int x) { return x >= 5 ? x - 5 : x; };
+        // stage s sits in slots sa (a) and sa + 1 (b), modulo 5
 #pragma unroll
-            for (int t = 0; t < NLD; ++t) issue(bc, ls, lslot, l0 + i * NLD + t);
-            __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < 2; ++t) {
+            const i32x4 ra = rsrc_of(false, it.s0 + t), rb = rsrc_of(true, it.s0 + t);
+            const int left = left_of(it.s0 + t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) load_a(ra, left, i, 2 * t * SLOT);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) load_b(rb, left, i, (2 * t + 1) * SLOT);
         }
-    };
-    using C0 = std::integral_constant<int, 0>;
-    using C1 = std::integral_constant<int, 1>;
-    using C2 = std::integral_constant<int, 2>;
-
-    // stage s in slots sa (a) and sa + 1 (b), modulo 5
-    auto wrap = [](int x) { return x >= 5 ? x - 5 : x; };
-    auto issue_first = [&](int s0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < INS; ++i) issue(A_{}, s0, 0, i);
-#pragma unroll
-        for (int i = 0; i < INS; ++i) issue(B_{}, s0, 1, i);
-#pragma unroll
-        for (int i = 0; i < INS; ++i) issue(A_{}, s0 + 1, 2, i);
-#pragma unroll
-        for (int i = 0; i < INS; ++i) issue(B_{}, s0 + 1, 3, i);
-    };
-    Item cur = item_of(0);
-    load_item(cur, true);
-    issue_first(cur.s0);
-    for (int k = 0;;) {
-        zero_acc();
-        // stage s0 has landed once at most stage s0 + 1's loads are in flight
-        // (the last item's stores are in the count too; loads complete in order
-        // among themselves)
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * INS, 0));
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 0));
         __builtin_amdgcn_s_barrier();
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            fa[0][t] = read_one(AOP, a_base, 0u, 0, t);
-            fb[0][t] = read_one(BOP, b_base, WIDE_SLOT * 2, 0, t);
+            read_a(0u, 0, t, 0);
+            read_b(SLOT * 2, 0, t, 0);
         }
         int sa = 0;
-        for (int s = cur.s0; s < cur.s1; ++s) {
-            const uint32_t ao = slot_off(sa), bo = slot_off(wrap(sa + 1));
+        for (int s = it.s0; s < it.s1; ++s) {
+            const uint32_t ao = opaque(sa * SLOT), bo = opaque(wrap(sa + 1) * SLOT);
+            const i32x4 ra = rsrc_of(false, s + 2), rb = rsrc_of(true, s + 2);
+            const int left = left_of(s + 2), as = wrap(sa + 4) * SLOT;
             __builtin_amdgcn_sched_barrier(0);
-            substep(C0{}, ao, bo, 1, A_{}, C1{}, s + 2, wrap(sa + 4), 0);
-            substep(C1{}, ao, bo, 2, A_{}, C1{}, s + 2, wrap(sa + 4), 4);
-            substep(C0{}, ao, bo, 3, A_{}, C0{}, 0, 0, 0);
+            substep(Set0{}, ao, bo, 1, LA{}, N1{}, ra, left, as, 0);
+            substep(Set1{}, ao, bo, 2, LA{}, N1{}, ra, left, as, 4);
+            substep(Set0{}, ao, bo, 3, LA{}, N0{}, ra, left, as, 0);
             // stage s + 1 has landed (only stage s + 2's a loads may be in
             // flight), and this wave has read stage s (its last reads fill the
             // next sub-step's fragments)
-            __builtin_amdgcn_s_waitcnt(waitcnt_imm(INS, 0));
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
             __builtin_amdgcn_s_barrier();
             __builtin_amdgcn_sched_barrier(0);
             const int sn = wrap(sa + 2);
-            substep(C1{}, slot_off(sn), slot_off(wrap(sn + 1)), 0, B_{}, C2{}, s + 2, sa, 0);
+            substep(Set1{}, opaque(sn * SLOT), opaque(wrap(sn + 1) * SLOT), 0, LB{}, N2{}, rb, left, sa * SLOT, 0);
             __builtin_amdgcn_sched_barrier(0);
             sa = sn;
         }
-        // the sums stay in accumulation registers here (left to itself the
-        // compiler copies all of them out at the loop's end, and spills)
+    } else {
+        constexpr int SLOT = A_ELEMS + B_ELEMS;
+        constexpr int LOADS = A_INS + B_INS;
+        auto load_stage = [&](int s, int slot) __attribute__((always_inline)) {
+            const i32x4 ra = rsrc_of(false, s), rb = rsrc_of(true, s);
+            const int left = left_of(s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < A_INS; ++i) load_a(ra, left, i, slot * SLOT);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
-        // the zero-chunk loads past the end; then no wave reads the ring any more
-        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+            for (int i = 0; i < B_INS; ++i) load_b(rb, left, i, slot * SLOT + A_ELEMS);
+        };
+        auto substep = [&](auto curc, uint32_t so, int rkk) __attribute__((always_inline)) {
+            constexpr int CUR = decltype(curc)::value;
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+#pragma unroll
+            for (int i = 0; i < TM; ++i) read_a(so, rkk, i, CUR ^ 1);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) read_b(so + A_ELEMS * 2, rkk, j, CUR ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[CUR][j], fa[CUR][i], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        };
+#pragma unroll
+        for (int t = 0; t < NS; ++t) load_stage(it.s0 + t, t);
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 1) * LOADS <= 63 ? (NS - 1) * LOADS : 63, 0));
         __builtin_amdgcn_s_barrier();
-        // the next item's first stages stream in during this one's epilogue
-        const bool more = k + 1 < nitems;
-        const Item nxt = item_of(more ? k + 1 : k);
-        load_item(nxt, more);
-        issue_first(nxt.s0);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (PIECES) {
-            // a piece's sums as they lie in the lanes: [wave][i][j][q][lane][4]
-            float* d = p.part + (size_t)(rest.slot + k) * 65536 + wave * 16384 + lane * 4;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < TM; ++i) read_a(0u, 0, i, 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<f32x4*>(d + ((i * 4 + j) * 4 + q) * 256) =
-                            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < (DUAL ? 2 : 4); ++j) {
-                    // an opaque copy of the lane index: the block's addresses
-                    // are formed here, not kept in registers across the item
-                    int el = lane;
-                    if constexpr (DUAL) asm volatile("" : "+v"(el), "+a"(acc[i][j]), "+a"(acc[i][j + 2]));
-                    else asm volatile("" : "+v"(el), "+a"(acc[i][j]));
-                    finish_block<EPI>(p, cur.m0, cur.n0, wm * 128 + i * 32, wn * (DUAL ? 64 : 128) + j * 32, el,
-                                      acc[i][j], acc[i][DUAL ? j + 2 : j]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+        for (int j = 0; j < TN; ++j) read_b(A_ELEMS * 2, 0, j, 0);
+        int slot = 0;
+        for (int s = it.s0; s < it.s1; ++s) {
+            const int next = slot + 1 == NS ? 0 : slot + 1;
+            const uint32_t so = opaque(slot * SLOT);
+            __builtin_amdgcn_sched_barrier(0);
+            substep(Set0{}, so, 1);
+            substep(Set1{}, so, 2);
+            substep(Set0{}, so, 3);
+            // stage s + 1 has landed (stages s + 2 .. s + NS - 1 may be in flight),
+            // and this wave has read stage s
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm((NS - 2) * LOADS, 0));
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            load_stage(s + NS, slot);
+            substep(Set1{}, opaque(next * SLOT), 0);
+            slot = next;
         }
-        if (!more) break;
-        cur = nxt;
-        ++k;
     }
-    // the loads past the last item
+    // the sums stay in accumulation registers here and leave them block by block
+    // (left to itself the compiler copies all of them out at the loop's end, and
+    // spills)
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) asm volatile("" : "+a"(acc[i][j]));
+    // the loads past the end
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+
+    if (it.slot >= 0) {
+        float* d = p.part + ((size_t)it.slot * 4 + wave) * (TM * TN * 1024) + lane * 4;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                asm volatile("" : "+a"(acc[i][j]));
+                store_sums(d + (i * TN + j) * 1024, acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        return;
+    }
+    constexpr int JB = DUAL ? TN / 2 : TN;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            // an opaque copy of the lane index: the block's addresses are formed
+            // here, not kept in registers through the loop
+            int el = lane;
+            if constexpr (DUAL) asm volatile("" : "+v"(el), "+a"(acc[i][j]), "+a"(acc[i][j + JB]));
+            else asm volatile("" : "+v"(el), "+a"(acc[i][j]));
+            finish_block<P::EPI>(p, m0, n0, wm * (BM / 2) + i * 32, wn * (P::COLS / 2) + j * 32, el, acc[i][j],
+                                 acc[i][DUAL ? j + JB : j]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 }
 
-template <int AOP, int BOP, bool DUAL, int EPI, bool RAGGED>
-__global__ __launch_bounds__(256) void wide_gemm_kernel(GemmArgs p, int whole, int workers) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[5 * WIDE_SLOT];
-    const int b = blockIdx.x;
-    if (b < whole) wide_tiles<AOP, BOP, DUAL, EPI, RAGGED, false>(p, smem, b, whole, p.full);
-    else wide_tiles<AOP, BOP, DUAL, EPI, RAGGED, true>(p, smem, b - whole, workers, workers);
+struct NoProduct {};
+
+// Items of product A and (unless NoProduct) product B, the one with the longer
+// items first.
+template <class A, class B>
+__global__ __launch_bounds__(256) void gemm_kernel(GemmArgs a, GemmArgs b, int items_a, int items_b, int b_first) {
+    __shared__ __attribute__((aligned(16))) uint16_t smem[LDS_BYTES / 2];
+    const int blk = blockIdx.x;
+    if constexpr (std::is_same_v<B, NoProduct>) {
+        gemm_item<A>(a, smem, blk);
+    } else {
+        const bool is_b = b_first ? blk < items_b : blk >= items_a;
+        if (!is_b) gemm_item<A>(a, smem, b_first ? blk - items_b : blk);
+        else gemm_item<B>(b, smem, b_first ? blk : blk - items_a);
+    }
 }
 
-// The pieces of the tiles past p.full, added in the order of the contraction
-// (whatever workgroup finished first), then the epilogue: one wave per 32 x 32
-// block (dual: pair of blocks), 4 to a workgroup.  workers: the product kernel's
-// workgroups.
-template <bool DUAL, int EPI>
-__global__ __launch_bounds__(256) void wide_reduce_kernel(GemmArgs p, int workers) {
-    constexpr int GROUP_M = 8;
-    constexpr int BLOCKS = DUAL ? 32 : 64;   // per tile
-    const int lane = threadIdx.x & 63;
-    const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int rtile = id / BLOCKS, blk = id % BLOCKS;
-    const int wv = blk / (BLOCKS / 4), i = blk / (BLOCKS / 16) % 4, j = blk % (BLOCKS / 16);
-    const int KB = p.segs * p.kb_seg;
-    const long long total = (long long)(p.tiles_m * p.tiles_n - p.full) * KB;
-    // workers [w0, w1] hold the tile's stages
-    const long long first = (long long)rtile * KB;
-    int w = (int)(first * workers / total);
-    while (total * (w + 1) / workers <= first) ++w;
+// The parts' sums of one 32 x 32 block (dual: pair) of a split tile, added in
+// order of the contraction (whatever workgroup finished first), then the epilogue.
+template <class P>
+__device__ __forceinline__ void reduce_item(const GemmArgs& p, int id, int lane) {
+    constexpr int TM = P::TM, TN = P::TN, JB = P::DUAL ? TN / 2 : TN;
+    constexpr int BLOCKS = 4 * TM * JB;
+    const int t = id / BLOCKS, blk = id % BLOCKS;
+    if (t >= p.rest) return;
+    const int wv = blk / (TM * JB), i = blk / JB % TM, j = blk % JB;
+    constexpr size_t TILE = (size_t)4 * TM * TN * 1024;
     f32x16 x, y;
 #pragma unroll
     for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
-    for (; w < workers && total * w / workers < first + KB; ++w) {
-        if (total * w / workers == total * (w + 1) / workers) continue;
-        const WideRest rest = wide_rest(p, KB, workers, w);
-        const float* src = p.part + (size_t)(rest.slot + (rest.tile == rtile ? 0 : 1)) * 65536 + wv * 16384 + lane * 4;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(src + ((i * 4 + j) * 4 + q) * 256);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[4 * q + e] += a[e];
-            if constexpr (DUAL) {
-                const f32x4 b = *reinterpret_cast<const f32x4*>(src + ((i * 4 + j + 2) * 4 + q) * 256);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[4 * q + e] += b[e];
-            }
-        }
+    const float* src = p.part + t * TILE + (size_t)(wv * TM * TN + i * TN + j) * 1024 + lane * 4;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s, src += p.rest * TILE) {
+        add_sums(src, x);
+        if constexpr (P::DUAL) add_sums(src + JB * 1024, y);
     }
-    const int tile = p.full + rtile;
-    const int per_group = GROUP_M * p.tiles_n;
-    const int group = tile / per_group;
-    const int first_m = group * GROUP_M;
-    const int gsize = min(p.tiles_m - first_m, GROUP_M);
-    const int in_group = tile - group * per_group;
-    finish_block<EPI>(p, (first_m + in_group % gsize) * 256, (in_group / gsize) * (DUAL ? 128 : 256),
-                      (wv & 1) * 128 + i * 32, (wv >> 1) * (DUAL ? 64 : 128) + j * 32, lane, x, y);
+    int m0, n0;
+    tile_corner<P::BM, P::COLS>(p, p.whole + t, m0, n0);
+    finish_block<P::EPI>(p, m0, n0, (wv & 1) * (P::BM / 2) + i * 32, (wv >> 1) * (P::COLS / 2) + j * 32, lane,
+                         x, y);
 }
-
-// The splits' sums of 8 adjacent columns, added in split order 0 .. splits - 1
-// (the same result whatever workgroup finished first), then the epilogue.
-template <bool DUAL, int EPI>
-__global__ __launch_bounds__(256) void tile_reduce_kernel(GemmArgs p) {
-    const long long groups = (long long)p.rows * (p.cols / 8);
-    const size_t stride = (size_t)p.rows * p.part_cols;
-    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < groups; t += (long long)gridDim.x * 256) {
-        const int m = (int)(t / (p.cols / 8)), n = (int)(t % (p.cols / 8)) * 8;
-        const float* src = p.part + (size_t)m * p.part_cols + n;
-        float x[8] = {}, y[8] = {};
-        for (int s = 0; s < p.splits; ++s, src += stride) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const f32x4 v = *reinterpret_cast<const f32x4*>(src + 4 * h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[4 * h + e] += v[e];
-                if constexpr (DUAL) {
-                    const f32x4 w = *reinterpret_cast<const f32x4*>(src + p.cols + 4 * h);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[4 * h + e] += w[e];
-                }
-            }
-        }
-        finish8<EPI>(p, m, n, x, y);
+template <class A, class B>
+__global__ __launch_bounds__(256) void gemm_reduce_kernel(GemmArgs a, GemmArgs b, int blocks_a) {
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (std::is_same_v<B, NoProduct>) {
+        reduce_item<A>(a, blockIdx.x * 4 + w, lane);
+    } else {
+        if ((int)blockIdx.x < blocks_a) reduce_item<A>(a, blockIdx.x * 4 + w, lane);
+        else reduce_item<B>(b, (blockIdx.x - blocks_a) * 4 + w, lane);
     }
 }
 
