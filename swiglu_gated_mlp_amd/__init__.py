@@ -178,8 +178,15 @@ def _gemm_packed_at_least(Wg, K: int, N: int, name: str = "Wg") -> None:
                          % (name, Wg.numel() * Wg.element_size(), K, N, need))
 
 
+# the current stream's handle without building a Stream object (a tenth of the
+# time; the calls below are a few microseconds of host time each)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -388,9 +395,10 @@ def _resolve_workspace(workspace, need: int, device: torch.device, s: int):
     return ws, (0 if ws is None else ws.numel() * ws.element_size())
 
 
-def _new(shape, device, s: int) -> torch.Tensor:
-    """An uninitialised bf16 output, allocated on the stream that writes it."""
-    if s == torch.cuda.current_stream(device).cuda_stream:
+def _new(shape, device, s: int, stream=None) -> torch.Tensor:
+    """An uninitialised bf16 output, allocated on the stream that writes it (s;
+    stream: the caller's argument, None for the current one)."""
+    if stream is None or s == torch.cuda.current_stream(device).cuda_stream:
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
     with torch.cuda.stream(torch.cuda.ExternalStream(s, device=device)):
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
@@ -400,9 +408,14 @@ def _scratch(workspace, need: int, device, s: int):
     """As _resolve_workspace; a call under graph capture without a workspace of
     its own gets a buffer of the graph's pool, so that no buffer that a graph
     writes on replay is handed to another call."""
-    if workspace is None and need and torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-        return ws, need
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device), need
+        buf = _workspace_for(device, s).buf
+        if buf is not None and buf.numel() >= need:
+            return buf, buf.numel()
     return _resolve_workspace(workspace, need, device, s)
 
 

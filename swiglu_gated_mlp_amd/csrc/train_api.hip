@@ -161,55 +161,65 @@ struct Launch {
     int64_t part_bytes() const { return t[0].part_bytes() + (jobs == 2 ? t[1].part_bytes() : 0); }
 };
 
-double launch_us(Launch& l, const Shape* s, int cus) {
-    const bool b_first = l.jobs == 2 && item_us(l.t[1].bm, l.t[1].kb_per_split) > item_us(l.t[0].bm, l.t[0].kb_per_split);
-    l.second_first = b_first;
-    Dispatch d(cus);
-    for (int q = 0; q < l.jobs; ++q) {
-        const int i = b_first ? 1 - q : q;
-        d.run(l.t[i].whole, item_us(l.t[i].bm, s[i].kb));
-        d.run(l.t[i].rest * l.t[i].splits, item_us(l.t[i].bm, l.t[i].kb_per_split));
-    }
-    return d.end() + (l.part_bytes() ? kReduceUs + l.part_bytes() * kPartUs : 0.0);
-}
+// A product's tiles with what they cost: the items' time in all and of the longest.
+struct Candidate {
+    Tiles t;
+    double whole_us, part_us;   // of an item
+    double total() const { return t.whole * whole_us + (double)t.rest * t.splits * part_us; }
+    double longest() const { return std::max(t.whole ? whole_us : 0.0, t.rest ? part_us : 0.0); }
+};
 
 // The fastest of the candidate tiles and splits.
 Launch search_launch(int jobs, const Kind* kind, int64_t M, int64_t K, int64_t N, int cus) {
     if (cus <= 0) cus = 256;
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
-    Shape s[2];
-    Tiles cand[2][40];
+    Candidate cand[2][40];
     int n[2] = {0, 0};
     for (int i = 0; i < jobs; ++i) {
-        s[i] = shape_of(kind[i], M, K, N);
-        const int sizes[2] = {256, s[i].rows <= 64 && !s[i].strided ? 64 : 128};
+        const Shape s = shape_of(kind[i], M, K, N);
+        auto add = [&](const Tiles& t) {
+            cand[i][n[i]++] = Candidate{t, item_us(t.bm, s.kb), item_us(t.bm, t.kb_per_split)};
+        };
+        const int sizes[2] = {256, s.rows <= 64 && !s.strided ? 64 : 128};
         for (int bm : sizes) {
-            const Tiles t = make_tiles(s[i], bm);
+            const Tiles t = make_tiles(s, bm);
             const int64_t all = (int64_t)t.tiles_m * t.tiles_n;
             for (int p : kSplits) {
-                if (p > 1 && (p > s[i].kb / 3 || all * p > 4 * (int64_t)cus)) break;
-                cand[i][n[i]++] = split_tiles(t, s[i].kb, 0, p);
+                if (p > 1 && (p > s.kb / 3 || all * p > 4 * (int64_t)cus)) break;
+                add(split_tiles(t, s.kb, 0, p));
             }
             // whole rounds, and the rest of the tiles split to fill one
             const int64_t rest = all % cus;
-            if (bm == 256 && all > cus && rest > 0 && s[i].kb >= 6)
-                cand[i][n[i]++] = split_tiles(t, s[i].kb, (int)(all - rest),
-                                              (int)std::max<int64_t>(2, std::min<int64_t>(cus / rest, s[i].kb / 3)));
+            if (bm == 256 && all > cus && rest > 0 && s.kb >= 6)
+                add(split_tiles(t, s.kb, (int)(all - rest),
+                                (int)std::max<int64_t>(2, std::min<int64_t>(cus / rest, s.kb / 3))));
         }
     }
-    Launch best{}, l{};
+    Launch best{};
     double best_us = 1e30;
-    l.jobs = jobs;
     for (int i = 0; i < n[0]; ++i)
         for (int j = 0; j < (jobs == 2 ? n[1] : 1); ++j) {
-            l.kind[0] = kind[0];
-            l.t[0] = cand[0][i];
-            if (jobs == 2) {
-                l.kind[1] = kind[1];
-                l.t[1] = cand[1][j];
-                if (l.t[0].bm == 256 && l.t[1].bm != 256) continue;   // no kernel for it
+            const Candidate* c[2] = {&cand[0][i], jobs == 2 ? &cand[1][j] : nullptr};
+            if (c[1] && c[0]->t.bm == 256 && c[1]->t.bm != 256) continue;   // no kernel for it
+            Launch l{};
+            l.jobs = jobs;
+            for (int q = 0; q < jobs; ++q) {
+                l.kind[q] = kind[q];
+                l.t[q] = c[q]->t;
             }
-            const double us = launch_us(l, s, cus);
+            const double reduce_us = l.part_bytes() ? kReduceUs + l.part_bytes() * kPartUs : 0.0;
+            // no dispatch beats an even share of the work, or its longest item
+            const double total = c[0]->total() + (c[1] ? c[1]->total() : 0.0);
+            const double longest = std::max(c[0]->longest(), c[1] ? c[1]->longest() : 0.0);
+            if (std::max(total / cus, longest) + reduce_us >= best_us) continue;
+            l.second_first = c[1] && c[1]->longest() > c[0]->longest();
+            Dispatch d(cus);
+            for (int q = 0; q < jobs; ++q) {
+                const Candidate& x = *c[l.second_first ? 1 - q : q];
+                d.run(x.t.whole, x.whole_us);
+                d.run(x.t.rest * x.t.splits, x.part_us);
+            }
+            const double us = d.end() + reduce_us;
             if (us < best_us) {
                 best_us = us;
                 best = l;
@@ -482,10 +492,9 @@ swiglu_status swiglu_train_backward(const swiglu_bf16* dY, const swiglu_bf16* A,
     if (dW1) { b.out(dW1, K * N); b.out(dW2, K * N); }
     if (workspace) b.out(workspace, (int64_t)(workspace_bytes / 2));
     if ((st = b.check()) != SWIGLU_OK) return st;
-    const int cus = cu_count_now();
-    if (!workspace || workspace_bytes < (size_t)train_workspace(M, K, N, cus)) return SWIGLU_ERR_WORKSPACE;
+    const Passes p = plan_backward(G ? -1 : (int)D_DUAL, dA, dW1, M, K, N, cu_count_now());
+    if (!workspace || workspace_bytes < (size_t)(d_bytes(M, N) + p.part_bytes())) return SWIGLU_ERR_WORKSPACE;
     const Call c{M, K, N, (hipStream_t)stream, (uint16_t*)workspace, (float*)((char*)workspace + d_bytes(M, N))};
-    const Passes p = plan_backward(G ? -1 : (int)D_DUAL, dA, dW1, M, K, N, cus);
     hipError_t e;
     if (G) {
         e = run_dgate(c, dY, G, U, c.D);
@@ -522,10 +531,9 @@ swiglu_status swiglu_mlp_train_backward(const swiglu_bf16* dZ, const swiglu_bf16
     if (dW1) { b.out(dW1, K * N); b.out(dW2, K * N); b.out(dW3, K * N); }
     if (workspace) b.out(workspace, (int64_t)(workspace_bytes / 2));
     if ((st = b.check()) != SWIGLU_OK) return st;
-    const int cus = cu_count_now();
-    if (!workspace || workspace_bytes < (size_t)train_workspace(M, K, N, cus)) return SWIGLU_ERR_WORKSPACE;
+    const Passes p = plan_backward(D_DY, dA, dW1, M, K, N, cu_count_now());
+    if (!workspace || workspace_bytes < (size_t)(d_bytes(M, N) + p.part_bytes())) return SWIGLU_ERR_WORKSPACE;
     const Call c{M, K, N, (hipStream_t)stream, (uint16_t*)workspace, (float*)((char*)workspace + d_bytes(M, N))};
-    const Passes p = plan_backward(D_DY, dA, dW1, M, K, N, cus);
     swt::GemmArgs a{};
     a.A0 = dZ; a.lda = K;
     a.B0 = W3; a.ldb = K;

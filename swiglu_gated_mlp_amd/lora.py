@@ -13,6 +13,8 @@ def _cached(fn, *args, device=None) -> int:
     key = (fn, args, None if device is None else device.index)
     need = _need.get(key)
     if need is None:
+        if len(_need) >= 4096:
+            _need.clear()
         need = _need[key] = fn(*args)
     return need
 
@@ -56,7 +58,7 @@ def _pack(fn: str, sizer, pairs, Lp, stream):
         raise ValueError("invalid adapters: %d of [%d,%d] x [%d,%d]" % (L, K, r, r, N))
     s = _stream(stream)
     if Lp is None:
-        Lp = _new(nbytes // 2, pairs[0][0].device, s)
+        Lp = _new(nbytes // 2, pairs[0][0].device, s, stream)
     elif Lp.numel() * Lp.element_size() < nbytes:
         raise ValueError("Lp too small: need %d bytes" % nbytes)
     _check(fn, getattr(lib(), fn)(*ptrs, _dev_bf16(Lp, "Lp"), K, N, L, r, s))
@@ -101,7 +103,7 @@ def _call(fn: str, need_fn, sizer, A, W, Lp, ids, scales, N, rank, out, name, wo
                          % (Lp.numel() * Lp.element_size(), L, rank, need_lp))
     _shape(out, (M, N), name)
     s = _stream(stream)
-    out = _new((M, N), A.device, s) if out is None else out
+    out = _new((M, N), A.device, s, stream) if out is None else out
     ws, ws_bytes = _scratch(workspace, _cached(need_fn, M, K, N, rank, device=A.device), A.device, s)
     st = getattr(lib(), fn)(a, _dev_bf16(W, "W"), lp, idp, scp, _dev_bf16(out, name), M, K, N, L, rank, _ptr(ws),
                             ws_bytes, s)

@@ -28,6 +28,8 @@ def _cached(fn, M: int, K: int, N: int, device) -> int:
     key = (fn, M, K, N, device.index)
     need = _need.get(key)
     if need is None:
+        if len(_need) >= 4096:
+            _need.clear()
         need = _need[key] = fn(M, K, N)
     return need
 
@@ -50,9 +52,9 @@ def swiglu_train_forward(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, Y:
         _shape(t, (M, N), name)
     a, w1, w2 = _dev_bf16(A, "A"), _dev_bf16(W1, "W1"), _dev_bf16(W2, "W2")
     s = _stream(stream)
-    Y = _new((M, N), A.device, s) if Y is None else Y
-    G = _new((M, N), A.device, s) if G is None else G
-    U = _new((M, N), A.device, s) if U is None else U
+    Y = _new((M, N), A.device, s, stream) if Y is None else Y
+    G = _new((M, N), A.device, s, stream) if G is None else G
+    U = _new((M, N), A.device, s, stream) if U is None else U
     ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, A.device), A.device, s)
     st = lib().swiglu_train_forward(a, w1, w2, _dev_bf16(Y, "Y"), _dev_bf16(G, "G"), _dev_bf16(U, "U"), M, K, N,
                                     _ptr(ws), ws_bytes, s)
@@ -60,7 +62,7 @@ def swiglu_train_forward(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, Y:
     return Y, G, U
 
 
-def _grads(needed: bool, given, shape, names, device, s: int):
+def _grads(needed: bool, given, shape, names, device, s: int, stream):
     """Gradient outputs: the caller's, new ones, or (not needed) None."""
     if not needed:
         if any(t is not None for t in given):
@@ -69,7 +71,7 @@ def _grads(needed: bool, given, shape, names, device, s: int):
     out = []
     for t, name in zip(given, names):
         _shape(t, shape, name)
-        out.append(_new(shape, device, s) if t is None else t)
+        out.append(_new(shape, device, s, stream) if t is None else t)
     return out
 
 
@@ -89,8 +91,8 @@ def swiglu_train_backward(dY: torch.Tensor, A: torch.Tensor, W1: torch.Tensor, W
     ins = [_dev_bf16(t, n) for t, n in ((dY, "dY"), (A, "A"), (W1, "W1"), (W2, "W2"))]
     kept = [0 if t is None else _dev_bf16(t, n) for t, n in ((G, "G"), (U, "U"))]
     s = _stream(stream)
-    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s)
-    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s)
+    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
+    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
     ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, A.device), A.device, s)
     outs = [0 if t is None else _dev_bf16(t, n) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
     st = lib().swiglu_train_backward(*ins, *kept, *outs, M, K, N, _ptr(ws), ws_bytes, s)
@@ -116,9 +118,9 @@ def swiglu_mlp_train_backward(dZ: torch.Tensor, A: torch.Tensor, W1: torch.Tenso
     ins = [_dev_bf16(t, n) for t, n in ((dZ, "dZ"), (A, "A"), (W1, "W1"), (W2, "W2"), (W3, "W3"), (G, "G"), (U, "U"))]
     y = _dev_bf16(Y, "Y") if Y is not None else 0
     s = _stream(stream)
-    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s)
-    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s)
-    dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), A.device, s)
+    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
+    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
+    dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), A.device, s, stream)
     ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, A.device), A.device, s)
     outs = [0 if t is None else _dev_bf16(t, n)
             for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"), (dW3, "dW3"))]
