@@ -862,13 +862,14 @@ constexpr int stream_smem_elems() {
 // half, one accumulator set -- so the units are twice the fused product's
 // panels and the CUs share them as evenly (p.panels counts half-panels; the
 // single Y-tile pass maps each wave's 32 columns to its half).
-// LORA: each row's low-rank adapter (la) is added to the sums in the epilogue
-// (lora_block).
+// LORA: each row's low-rank adapter (la) is added to the sums: 1 after the
+// K loop (lora_tile_sums), or where a tile's rows have too many adapters for that,
+// in the epilogue (lora_block); 2 in the epilogue, from la->delta.
 template <int BM, bool SPLIT, bool RAGGED, bool PANELS = false, bool IL = false, bool F8 = false,
-          bool SEQ = false, bool GEMM = false, bool LORA = false>
+          bool SEQ = false, bool GEMM = false, int LORA = 0>
 __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_t* smem, int first, int stride,
                                                      int total, const LoraArgs* la = nullptr) {
-    static_assert(!(LORA && (SPLIT || IL || F8 || SEQ)), "adapters: bf16 per-tile or single-weight pack, whole K");
+    static_assert(!(LORA != 0 && (SPLIT || IL || F8 || SEQ)), "adapters: bf16 per-tile or single-weight pack, whole K");
     static_assert(!(GEMM && (IL || F8 || SEQ)), "plain GEMM: bf16 single-weight pack");
     static_assert(!(IL && SPLIT), "the interleaved layout has no split-K schedule");
     static_assert(!(F8 && (IL || SPLIT)), "FP8 operands: per-tile layout, data-parallel only");
@@ -1257,6 +1258,9 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
             stage(I1{}, s + 1);
             stage(I2{}, s + 2);
         }
+        int tl = lane;
+        if constexpr (LORA == 1) asm volatile("" : "+v"(tl));
+        std::conditional_t<LORA == 1, LoraTile<TM, GEMM ? 1 : 2>, LoraNone> tile(la, cur.m0, tl);
         if (ns - s >= 1) stage(I0{}, s);
         if (ns - s >= 2) stage(I1{}, s + 1);
         // the zero-chunk loads of the two stages past the end are still in
@@ -1308,6 +1312,12 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
             }
         }
 
+        if constexpr (LORA == 1) {
+            const int tc = cur.n0 + 32 * wave;
+            tile.begin(cur.m0, GEMM ? ((tc >> 7) * PACK_ROWS + (tc & (PACK_BN - 1))) / 32 : tc / 32,
+                       GEMM ? ((tc >> 7) * PACK_ROWS + (tc & (PACK_BN - 1)) + PACK_BN) / 32 : tc / 32);
+        }
+
         // the next item's first two stages stream in during this epilogue
         // (past the last item they read the zero chunk): activations and
         // stage 0's weights now, stage 1's weights once the accumulators are
@@ -1317,6 +1327,12 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
         const Item nxt = item_of(more ? wn : w);
         load_item(nxt, more);
         issue_first_a();
+        // LORA 1: the row tile's adapters; blocks: they are added below instead
+        bool blocks = false;
+        if constexpr (LORA == 1) {
+            tile.run(acc);
+            blocks = tile.len < 0;
+        }
 #pragma unroll
         for (int j = A_INS; j < LOADS; ++j) issue_one(j, 0, 0, I0{});
 
@@ -1347,15 +1363,25 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
         };
         // GEMM pass gh: bf16 of accumulator set gh (no SiLU) into the Y tile
         auto fill_gemm = [&](int gh) {
+            // LORA 2: the next block's part is loaded while one is at work
+            f32x16 ld[2][1];
+            const int nt[1] = {LORA != 0 ? lora_tile(gh) : 0};
+            if constexpr (LORA == 2) lora_read_block(ld[0][0], *la, 1, cur.m0 + (el & 31), 0, nt[0] * 32, el);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int r = i * 32 + (el & 31);
-                if constexpr (LORA) {
-                    f32x16 d[1];
-                    const int nt[1] = {lora_tile(gh)};
-                    lora_block<1, 1>(d, *la, lora_row(i), cur.m0 + r, nt, el);
-                    acc[gh][i][0] += d[0];
+                if constexpr (LORA == 2) {
+                    if (i + 1 < TM) lora_read_block(ld[(i + 1) & 1][0], *la, 1, cur.m0 + r + 32, 0, nt[0] * 32, el);
                 }
+                if constexpr (LORA != 0) asm volatile("" : "+a"(acc[gh][i][0]));   // leaves its registers here
+                if constexpr (LORA == 1) {
+                    if (blocks) {
+                        ld[0][0] = acc[gh][i][0];
+                        lora_block<1, 1>(ld[0], *la, lora_row(i), cur.m0 + r, nt, el);
+                        acc[gh][i][0] = ld[0][0];
+                    }
+                }
+                if constexpr (LORA == 2) acc[gh][i][0] += ld[i & 1][0];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     u32x2 out;
@@ -1369,6 +1395,12 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
             }
         };
         if constexpr (GEMM) fill_gemm(0);
+        f32x16 ld[2][2];
+        const int nt[2] = {LORA != 0 && !GEMM ? lora_tile(0) : 0, LORA != 0 && !GEMM ? lora_tile(1) : 0};
+        if constexpr (LORA == 2 && !GEMM) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) lora_read_block(ld[0][g], *la, 2, cur.m0 + (el & 31), g, nt[g] * 32, el);
+        }
 #pragma unroll
         for (int i = 0; i < (GEMM ? 0 : TM); ++i) {
             const int r = i * 32 + (el & 31);
@@ -1389,10 +1421,22 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
                                                      4 * ((q & 1) ^ ((r >> 4) & 1)) + 2 * (el >> 5)) = out;
                     }
             } else {
-                f32x16 d[2];
-                if constexpr (LORA) {
-                    const int nt[2] = {lora_tile(0), lora_tile(1)};
-                    lora_block<2, 2>(d, *la, lora_row(i), cur.m0 + r, nt, el);
+                if constexpr (LORA == 2) {
+                    if (i + 1 < TM) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+                            lora_read_block(ld[(i + 1) & 1][g], *la, 2, cur.m0 + r + 32, g, nt[g] * 32, el);
+                    }
+                }
+                if constexpr (LORA != 0) asm volatile("" : "+a"(acc[0][i][0]), "+a"(acc[1][i][0]));
+                if constexpr (LORA == 1) {
+                    if (blocks) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) ld[0][g] = acc[g][i][0];
+                        lora_block<2, 2>(ld[0], *la, lora_row(i), cur.m0 + r, nt, el);
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) acc[g][i][0] = ld[0][g];
+                    }
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -1400,9 +1444,9 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float gv = acc[0][i][0][4 * q + e], uv = acc[1][i][0][4 * q + e];
-                        if constexpr (LORA) {
-                            gv += d[0][4 * q + e];
-                            uv += d[1][4 * q + e];
+                        if constexpr (LORA == 2) {
+                            gv += ld[i & 1][0][4 * q + e];
+                            uv += ld[i & 1][1][4 * q + e];
                         }
                         if constexpr (F8) {
                             gv *= p.sg;
@@ -1720,8 +1764,16 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora)
         const int n = n0 + 16 * c + 4 * kq;
         if constexpr (sizeof...(Lora) > 0) {
             const LoraArgs& la = (lora, ...);
-            const int id = m < M ? lora_id(la, m) : -1;
-            if (id >= 0) {
+            if (la.delta) {
+                if constexpr (GEMM) {
+                    const int col = (n / PACK_BN) * PACK_ROWS + n % PACK_BN + (HALF ? PACK_BN * half : 0);
+                    g += lora_read4(la, 1, m, 0, col);
+                    if constexpr (!HALF) u += lora_read4(la, 1, m, 0, col + PACK_BN);
+                } else {
+                    g += lora_read4(la, 2, m, 0, n);
+                    u += lora_read4(la, 2, m, 1, n);
+                }
+            } else if (const int id = m < M ? lora_id(la, m) : -1; id >= 0) {
                 if constexpr (GEMM) {
                     const int col = (n / PACK_BN) * PACK_ROWS + n % PACK_BN + (HALF ? PACK_BN * half : 0);
                     if (col < N) g += lora_delta4<1>(la, m, id, 0, col);

@@ -277,8 +277,15 @@ hipError_t launch_stream(const swk::FusedArgs& a, int total, int grid, hipStream
     const bool ragged = (a.K % (F8 ? 128 : swk::BK)) != 0;
     if constexpr (!SPLIT && !IL && !F8 && !SEQ) {
         if (la) {
-            const void* fn = ragged ? reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, true, PANELS, GEMM>)
-                                    : reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, false, PANELS, GEMM>);
+            // up to 256 rows (every panel schedule) the adapters' part is in memory
+            const void* fn =
+                ragged ? reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, true, PANELS, GEMM, PANELS ? 2 : 1>)
+                       : reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, false, PANELS, GEMM, PANELS ? 2 : 1>);
+            if constexpr (BM == 128 && !PANELS) {
+                if (la->delta)
+                    fn = ragged ? reinterpret_cast<const void*>(&swk::stream_lora_kernel<128, true, false, GEMM, 2>)
+                                : reinterpret_cast<const void*>(&swk::stream_lora_kernel<128, false, false, GEMM, 2>);
+            }
             swk::FusedArgs args = a;
             swk::LoraArgs lora = *la;
             void* kargs[] = {&args, &lora, &total};
@@ -1164,6 +1171,8 @@ swiglu_status check_lora(int64_t M, int64_t K, int64_t N, int64_t adapters, int6
 struct LoraPack {
     int groups, chunks, KB, ntiles;
     int64_t a_elems, b_elems;   // parts A and B
+    int64_t flag_elems;         // the flags, as 2-byte elements
+    int64_t elems() const { return a_elems + b_elems + flag_elems; }
 };
 
 LoraPack lora_pack_of(int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups) {
@@ -1175,13 +1184,13 @@ LoraPack lora_pack_of(int64_t K, int64_t N, int64_t adapters, int64_t rank, int 
     l.ntiles = (int)(groups == 2 ? ceil_div(N, 128) * 4 : ceil_div(N, 256) * 8);
     l.a_elems = adapters * groups * l.chunks * l.KB * 1024;
     l.b_elems = adapters * groups * l.chunks * l.ntiles * 512;
+    l.flag_elems = ceil_div(adapters, 4) * 8;
     return l;
 }
 
 size_t lora_packed_bytes(int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups) {
     if (check_lora(0, K, N, adapters, rank) != SWIGLU_OK) return 0;
-    const LoraPack l = lora_pack_of(K, N, adapters, rank, groups);
-    return (size_t)(l.a_elems + l.b_elems) * 2;
+    return (size_t)lora_pack_of(K, N, adapters, rank, groups).elems() * 2;
 }
 
 swiglu_status lora_pack_impl(const uint16_t* La1, const uint16_t* Lb1, const uint16_t* La2, const uint16_t* Lb2,
@@ -1197,22 +1206,43 @@ swiglu_status lora_pack_impl(const uint16_t* La1, const uint16_t* Lb1, const uin
     if (!aligned16(Lp)) return SWIGLU_ERR_MISALIGNED;
     for (int i = 0; i < 2 * groups; ++i)
         if (!aligned16(ins[i])) return SWIGLU_ERR_MISALIGNED;
-    const Range out = range_of(Lp, (l.a_elems + l.b_elems) * 2);
+    const Range out = range_of(Lp, l.elems() * 2);
     for (int i = 0; i < 2 * groups; ++i)
         if (overlap(out, range_of(ins[i], adapters * rank * (i & 1 ? N : K) * 2))) return SWIGLU_ERR_ALIASING;
     int Ki = (int)K, Ni = (int)N, r = (int)rank, g = groups, chunks = l.chunks, KB = l.KB, nt = l.ntiles;
-    long long pa = l.a_elems / 8, pieces = (l.a_elems + l.b_elems) / 8;
-    void* args[] = {&La1, &La2, &Lb1, &Lb2, &Lp, &g, &Ki, &Ni, &r, &chunks, &KB, &nt, &pa, &pieces};
-    const hipError_t e =
-        hipLaunchKernel(reinterpret_cast<const void*>(&swk::lora_pack_kernel),
-                        dim3((unsigned)std::min<int64_t>(ceil_div(pieces, 256), 1 << 20)), dim3(256), args, 0,
-                        (hipStream_t)stream);
+    long long pa = l.a_elems / 8, pb = l.b_elems / 8, pieces = l.elems() / 8;
+    void* args[] = {&La1, &La2, &Lb1, &Lb2, &Lp, &g, &Ki, &Ni, &r, &chunks, &KB, &nt, &pa, &pb, &pieces};
+    hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&swk::lora_pack_kernel),
+                                   dim3((unsigned)std::min<int64_t>(ceil_div(pieces, 256), 1 << 20)), dim3(256), args, 0,
+                                   (hipStream_t)stream);
+    if (e == hipSuccess) {
+        const uint16_t* B = Lp + l.a_elems;
+        int* flags = (int*)(Lp + l.a_elems + l.b_elems);
+        long long per = l.b_elems / 8 / adapters;
+        int count = (int)adapters, share = (int)std::min<int64_t>(ceil_div(per, 1024), 64);
+        void* fargs[] = {(void*)&B, (void*)&flags, &per, &share, &count};
+        e = hipLaunchKernel(reinterpret_cast<const void*>(&swk::lora_flag_kernel),
+                            dim3((unsigned)(std::min<int64_t>(adapters, 4096) * share)), dim3(256), fargs, 0,
+                            (hipStream_t)stream);
+    }
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
 }
 
-int64_t lora_t_bytes(int64_t M, int64_t rank, int groups) {
-    return (M * ceil_div(rank, 16) * groups * 64 + 255) / 256 * 256;
-}
+// How the adapters' part reaches the sums (lora_device.hpp): up to 256 rows from
+// the factors in fp32 parts, through memory (delta) except on the decode schedules
+// of up to 16 rows with narrow column groups; above 256 rows on the matrix units, from
+// the factors' bf16 pairs.
+constexpr int64_t kLoraDeltaMaxM = 256;
+
+struct LoraLayout {
+    bool delta, parts_fp32;
+    int parts;
+    int unit;                       // rows of the tiles that have adapter lists
+    int64_t t_bytes, list_bytes, delta_bytes;   // T, the lists, delta: multiples of 256
+    int64_t bytes() const { return t_bytes + list_bytes + delta_bytes; }
+};
+
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
 // The product's schedule: AUTO's, or data-parallel for a chunk of rows.
 Plan lora_plan(int64_t M, int64_t K, int64_t N, int groups, bool chunked) {
@@ -1222,33 +1252,73 @@ Plan lora_plan(int64_t M, int64_t K, int64_t N, int groups, bool chunked) {
     return make_plan(M, K, N, chunked ? SWIGLU_VARIANT_DATA_PARALLEL : SWIGLU_VARIANT_AUTO, cu_count_now());
 }
 
+// The decode configuration keeps several workgroups a CU (their other loads cover
+// the adapters'): the wide column groups of launch_decode_cfg and
+// launch_decode_gemm do not.
+bool lora_in_decode(const Plan& p, int64_t M, int64_t N, int groups) {
+    if (p.variant != SWIGLU_VARIANT_DECODE || M > 16) return false;
+    const bool long_k = p.KB >= 96;
+    return groups == 2 ? !(long_k && 4 * ceil_div(N, 128) >= 3 * p.cus)
+                       : !(long_k && 2 * ceil_div(gemm_tiled_cols(N), 64) >= p.cus);
+}
+
+LoraLayout lora_layout(const Plan& p, int64_t M, int64_t K, int64_t N, int64_t rank, int groups) {
+    LoraLayout l{};
+    const int64_t numbers = ceil_div(rank, 16) * groups * 16;   // of a row's t
+    l.parts = 1;
+    if (M <= kLoraDeltaMaxM) {
+        l.parts_fp32 = true;
+        l.delta = !lora_in_decode(p, M, N, groups);
+        // parts of the contraction while row blocks are few: at least 16 k blocks
+        // (one a wave) each
+        const int64_t blocks = ceil_div(M, 16);
+        l.parts = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(K, 64) / 16, 8, 64 / blocks}));
+        l.t_bytes = align256(l.parts * M * numbers * 4);
+        l.delta_bytes = l.delta ? align256(M * groups * N * 4) : 0;
+    } else {
+        l.t_bytes = ceil_div(M, 32) * 32 * numbers * 4;   // hi and lo
+        // lists for the row tiles of the product's schedule (the tail tiles of 128
+        // rows of a 256-row launch are halves of its tiles)
+        l.unit = p.t.BM == 256 ? 256 : 128;
+        l.list_bytes = align256(ceil_div(M, l.unit) * swk::LORA_LIST * 4);
+    }
+    return l;
+}
+
 size_t lora_workspace(int64_t M, int64_t K, int64_t N, int64_t rank, int groups) {
     if (check_lora(M, K, N, 1, rank) != SWIGLU_OK || M == 0) return 0;
     const int64_t limit = stream_rows_limit(K, 2);
-    if (M > limit) return (size_t)lora_t_bytes(balanced_chunk(M, limit), rank, groups);
-    const Plan p = lora_plan(M, K, N, groups, false);
-    return (size_t)lora_t_bytes(M, rank, groups) +
-           split_workspace_bytes(p, M, groups == 2 ? N : gemm_tiled_cols(N));
+    const bool chunked = M > limit;
+    const int64_t rows = chunked ? balanced_chunk(M, limit) : M;
+    size_t need = 0;
+    // chunks of rows: all alike but the last, which may be shorter
+    for (int64_t m : {rows, chunked ? M % rows : (int64_t)0}) {
+        if (m == 0) continue;
+        const Plan p = lora_plan(m, K, N, groups, chunked);
+        const LoraLayout l = lora_layout(p, m, K, N, rank, groups);
+        need = std::max(need, (size_t)l.bytes() +
+                                  split_workspace_bytes(p, m, groups == 2 ? N : gemm_tiled_cols(N)));
+    }
+    return need;
 }
 
-template <int WAVES, int TT>
-hipError_t launch_shrink(swk::LoraShrinkArgs a, hipStream_t s) {
+template <int TT>
+hipError_t launch_shrink(swk::LoraShrinkArgs a, bool parts_fp32, hipStream_t s) {
     const int64_t blocks = ceil_div(a.M, 16), ty = ceil_div(a.groups * a.chunks, TT);
     // workgroups that share a row block's distinct adapters, while the grid is small
-    const int64_t z = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / (blocks * ty)));
+    const int64_t z = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, a.M), 1024 / (blocks * ty * a.parts)));
+    const void* fn = parts_fp32 ? reinterpret_cast<const void*>(&swk::lora_shrink_kernel<TT, true>)
+                                : reinterpret_cast<const void*>(&swk::lora_shrink_kernel<TT, false>);
     void* kargs[] = {&a};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swk::lora_shrink_kernel<WAVES, TT>),
-                           dim3((unsigned)blocks, (unsigned)ty, (unsigned)std::min<int64_t>(z, a.M)),
-                           dim3(64 * WAVES), kargs, 0, s);
+    return hipLaunchKernel(fn, dim3((unsigned)blocks, (unsigned)ty, (unsigned)(z * a.parts)), dim3(1024), kargs, 0, s);
 }
 
-// A few row blocks: 16 waves on each (block, tile), where the latency of the
-// loads counts; many: 4 waves and up to 4 tiles, so that A is read once.
-hipError_t run_shrink(const swk::LoraShrinkArgs& a, hipStream_t s) {
+// Few row blocks: one tile of T's numbers a workgroup; many: up to 4, so that A is
+// read fewer times.
+hipError_t run_shrink(const swk::LoraShrinkArgs& a, bool parts_fp32, hipStream_t s) {
     const int64_t blocks = ceil_div(a.M, 16), tiles = a.groups * a.chunks;
-    if (blocks * tiles <= 512) return launch_shrink<16, 1>(a, s);
-    if (tiles >= 4) return launch_shrink<4, 4>(a, s);
-    return tiles >= 2 ? launch_shrink<4, 2>(a, s) : launch_shrink<4, 1>(a, s);
+    if (blocks * tiles <= 256 || tiles == 1) return launch_shrink<1>(a, parts_fp32, s);
+    return tiles >= 4 ? launch_shrink<4>(a, parts_fp32, s) : launch_shrink<2>(a, parts_fp32, s);
 }
 
 // One chunk of rows, arguments checked.
@@ -1256,19 +1326,38 @@ hipError_t run_lora(const uint16_t* A, const uint16_t* W, const uint16_t* Lp, co
                     uint16_t* Y, int64_t M, int64_t K, int64_t N, int64_t adapters, int64_t rank, int groups,
                     bool chunked, void* workspace, hipStream_t s) {
     const LoraPack l = lora_pack_of(K, N, adapters, rank, groups);
+    const int64_t nt = groups == 2 ? N : gemm_tiled_cols(N);
+    const Plan p = lora_plan(M, K, N, groups, chunked);
+    const LoraLayout lay = lora_layout(p, M, K, N, rank, groups);
+    char* const ws = (char*)workspace;
+    float* const delta = (float*)(ws + lay.t_bytes + lay.list_bytes);
     swk::LoraShrinkArgs sh{};
     sh.A = A; sh.P = Lp; sh.ids = ids; sh.scales = scales;
     sh.T = (uint16_t*)workspace;
+    sh.Tf = (float*)workspace;
+    sh.lists = (int*)(ws + lay.t_bytes);
+    sh.flags = (const int*)(Lp + l.a_elems + l.b_elems);
+    sh.unit = lay.unit;
     sh.M = (int)M; sh.K = (int)K; sh.KB = l.KB;
     sh.adapters = (int)adapters; sh.groups = groups; sh.chunks = l.chunks; sh.rank = (int)rank;
-    hipError_t e = run_shrink(sh, s);
+    sh.parts = lay.parts;
+    hipError_t e = run_shrink(sh, lay.parts_fp32, s);
     if (e != hipSuccess) return e;
 
     swk::LoraArgs la{};
-    la.T = sh.T; la.B = Lp + l.a_elems; la.ids = ids;
-    la.adapters = (int)adapters; la.chunks = l.chunks; la.ntiles = l.ntiles;
-    const int64_t nt = groups == 2 ? N : gemm_tiled_cols(N);
-    const Plan p = lora_plan(M, K, N, groups, chunked);
+    la.T = sh.T; la.Tf = sh.Tf; la.B = Lp + l.a_elems; la.ids = ids;
+    la.adapters = (int)adapters; la.chunks = l.chunks; la.ntiles = l.ntiles; la.parts = lay.parts;
+    la.M = (int)M; la.N = (int)N;
+    la.lists = sh.lists; la.unit = lay.unit;
+    if (lay.delta) {
+        void* xargs[] = {&la, (void*)&delta};
+        e = hipLaunchKernel(groups == 2 ? reinterpret_cast<const void*>(&swk::lora_expand_kernel<2>)
+                                        : reinterpret_cast<const void*>(&swk::lora_expand_kernel<1>),
+                            dim3((unsigned)ceil_div(groups * (N / 4), 8), (unsigned)ceil_div(M, 32)), dim3(256), xargs,
+                            0, s);
+        if (e != hipSuccess) return e;
+        la.delta = delta;
+    }
     if (p.variant == SWIGLU_VARIANT_DECODE) {
         swk::DecodeArgs d{};
         d.A = A; d.Wp = W; d.Y = Y;
@@ -1284,7 +1373,7 @@ hipError_t run_lora(const uint16_t* A, const uint16_t* W, const uint16_t* Lp, co
         return groups == 2 ? launch_stream_dp<false>(a, p, s, &la)
                            : launch_stream_dp<false, false, false, true>(a, p, s, &la);
     // splits: the plain kernels' partial sums, reduced with the adapters
-    a.part = reinterpret_cast<float*>((char*)workspace + lora_t_bytes(M, rank, groups));
+    a.part = reinterpret_cast<float*>(ws + lay.bytes());
     const int grid = p.tiles * p.splits;
     if (groups == 2)
         e = p.t.BM == 128 ? launch_stream<128, true>(a, grid, grid, s) : launch_stream<256, true>(a, grid, grid, s);
@@ -1292,7 +1381,7 @@ hipError_t run_lora(const uint16_t* A, const uint16_t* W, const uint16_t* Lp, co
         e = p.t.BM == 128 ? launch_stream<128, true, false, false, false, false, true>(a, grid, grid, s)
                           : launch_stream<256, true, false, false, false, false, true>(a, grid, grid, s);
     if (e != hipSuccess) return e;
-    const int64_t rgrid = std::max<int64_t>(1, std::min<int64_t>(ceil_div(M * (nt / 4), 256), (int64_t)p.cus * 8));
+    const int64_t rgrid = ceil_div(ceil_div(M, 32) * ceil_div(nt, 32), 4);
     int Mi = (int)M, Ni = (int)N, NTi = (int)nt, Si = p.splits;
     const float* part = a.part;
     void* args[] = {(void*)&part, (void*)&Y, &la, &Mi, &Ni, &NTi, &Si};

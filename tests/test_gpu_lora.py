@@ -170,6 +170,31 @@ def test_rows_are_independent(dev, M, K, N):
     assert not torch.isfinite(Cb[M // 3]).any()
 
 
+@pytest.mark.parametrize("M,K,N,r", [(700, 200, 776, 24), (2100, 72, 520, 40)])
+def test_neighbours_adapters_leave_a_row_as_it_is(dev, M, K, N, r):
+    """Long batches: a row of adapter 0 gets the same bits beside rows of one, of
+    three or of many other adapters, and beside adapters with NaN or infinities."""
+    L = 12
+    t = case(dev, M, K, N, L, r, ("1", "2", ""), "mixed")
+    own = torch.arange(M, device=dev) % 5 < 2
+    rest = torch.randint(1, L, (M,), generator=torch.Generator().manual_seed(2)).to(dev)
+    out = []
+    for others in (0, -1, 1, 1 + rest % 3, rest):
+        ids = torch.where(own, torch.zeros_like(rest), torch.as_tensor(others, device=dev)).int()
+        b = dict(t, ids=ids)
+        Y, C = gated(b, r), plain(b, r)
+        check_gated(Y, b, r"%s" % M)
+        check_plain(C, b, "%s" % M)
+        out.append((Y[own], C[own]))
+        for x in ("1", "2", ""):
+            b["Lb" + x] = t["Lb" + x].clone()
+            b["Lb" + x][1:, r - 1, N - 1] = float("nan")
+            b["Lb" + x][1:, 0, 1] = float("inf")
+        out.append((gated(b, r)[own], plain(b, r)[own]))
+    for y, c in out[1:]:
+        assert torch.equal(y, out[0][0]) and torch.equal(c, out[0][1])
+
+
 def fenced(t, fill):
     n, pad = t.numel(), 4096
     buf = torch.full((n + 2 * pad,), fill, dtype=t.dtype, device=t.device)

@@ -78,10 +78,11 @@ def test_pack_pointers_and_sizes():
             assert L.swiglu_lora_pack(*p, *args, None) == want
     assert L.swiglu_lora_pack(LA1, LB1, LP, LB2, LP, *args, None) == ALIAS
     assert L.swiglu_gemm_lora_pack(LA1, LP + 32, LP, *args, None) == ALIAS
-    # per adapter, projection and chunk: 64-deep k blocks of 2 KiB, 32-column tiles of 1 KiB
-    assert L.swiglu_lora_packed_bytes(64, 72, 3, 16) == 3 * 2 * (1 * 2048 + 4 * 1024)
-    assert L.swiglu_lora_packed_bytes(72, 136, 1, 17) == 2 * 2 * (2 * 2048 + 8 * 1024)
-    assert L.swiglu_gemm_lora_packed_bytes(72, 264, 2, 1) == 2 * (2 * 2048 + 16 * 1024)
+    # per adapter, projection and chunk: 64-deep k blocks of 2 KiB, 32-column tiles of 1 KiB;
+    # a 4-byte flag an adapter, in whole 16 bytes
+    assert L.swiglu_lora_packed_bytes(64, 72, 3, 16) == 3 * 2 * (1 * 2048 + 4 * 1024) + 16
+    assert L.swiglu_lora_packed_bytes(72, 136, 1, 17) == 2 * 2 * (2 * 2048 + 8 * 1024) + 16
+    assert L.swiglu_gemm_lora_packed_bytes(72, 264, 5, 1) == 5 * (2 * 2048 + 16 * 1024) + 32
 
 
 def test_binding_refusals():
