@@ -863,7 +863,7 @@ constexpr int stream_smem_elems() {
 // panels and the CUs share them as evenly (p.panels counts half-panels; the
 // single Y-tile pass maps each wave's 32 columns to its half).
 // LORA: each row's low-rank adapter (la) is added to the sums: 1 after the
-// K loop (lora_tile_sums), or where a tile's rows have too many adapters for that,
+// K loop (LoraTile), or where a tile's rows have too many adapters for that,
 // in the epilogue (lora_block); 2 in the epilogue, from la->delta.
 template <int BM, bool SPLIT, bool RAGGED, bool PANELS = false, bool IL = false, bool F8 = false,
           bool SEQ = false, bool GEMM = false, int LORA = 0>

@@ -5,6 +5,11 @@ functions on top of them.
 The swiglu_* functions marshal arguments for the C entry points of the same
 names (``include/swiglu.h``).  ``swiglu`` and ``swiglu_mlp`` are differentiable:
 their forward and backward passes are those entry points.
+
+Capturing a backward pass into a graph: take the gradients with
+``torch.autograd.grad``, or let no eager graph of the same leaves live.  The
+accumulation into a leaf runs on the stream where it was first recorded, and a
+capture that has to wait for that stream ends the process.
 """
 from __future__ import annotations
 
