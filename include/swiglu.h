@@ -511,7 +511,7 @@ swiglu_status swiglu_mlp_train_backward(
  *   picks.
  * swiglu_gemm_packed_lora: C [M,N] = A W + adapters, W [K,N] in the single-weight
  *   pack of swiglu_gemm_pack_weight, on the schedule of swiglu_gemm_packed with
- *   a workspace.
+ *   a workspace, or with K split further where that leaves CUs idle.
  * All: K and N multiples of 8, adapters >= 1, 1 <= rank <= 256 (above:
  * ERR_UNSUPPORTED_SHAPE), adapters * (K + N) at most 2^31; ids int32 and scales
  * fp32 (device, 4-byte aligned; read when the call's kernels run), other

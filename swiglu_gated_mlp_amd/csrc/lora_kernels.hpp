@@ -279,62 +279,63 @@ __global__ __launch_bounds__(256) void lora_reduce_kernel(const float* __restric
     const int ctiles = (NT + 31) / 32;
     const int i = w / ctiles, n0 = (w - i * ctiles) * 32;
     const bool work = i * 32 < M;
-    // the columns' adapters: gated, both groups of one tile; GEMM, two tiles
-    const int col = GEMM ? (n0 / PACK_BN) * PACK_ROWS + n0 % PACK_BN : n0;
-    constexpr int NH = GEMM ? 1 : 2;
-    if (work && !la.delta) {
-        const int m = i * 32 + (lane & 31);
-        const int rid = m < M ? lora_id(la, m) : -1;
-#pragma unroll
-        for (int h = 0; h < 3 - NH; ++h) {
-            int nt[NH];
-            f32x16 x[NH];
-#pragma unroll
-            for (int k = 0; k < NH; ++k) {
-                nt[k] = (col + (GEMM ? h * PACK_BN : 0)) / 32;
-                x[k] = f32x16{};
-            }
-            lora_block<NH, NH>(x, la, rid, m, nt, lane);
-#pragma unroll
-            for (int k = 0; k < NH; ++k)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<f32x4*>(&rows[wave][GEMM ? h : k][(lane & 31) * P + 8 * q + 4 * (lane >> 5)]) =
-                        f32x4{x[k][4 * q], x[k][4 * q + 1], x[k][4 * q + 2], x[k][4 * q + 3]};
-        }
-    }
-    __syncthreads();
-    if (!work) return;
+    // the block's sums: row 8 t + lane / 8, four columns
     const size_t stride = (size_t)M * 2 * (size_t)NT;
     const int n = n0 + 4 * (lane & 7);
-    if (n >= NT) return;
+    f32x4 g[4], u[4];
+    // the columns' adapters: gated, both groups of one tile; GEMM, two tiles
+    const int col = GEMM ? (n0 / PACK_BN) * PACK_ROWS + n0 % PACK_BN : n0;
+    if (work && !la.delta) {
+        const int m = i * 32 + (lane & 31);
+        const int nt[2] = {col / 32, (GEMM ? col + PACK_BN : col) / 32};
+        f32x16 x[2] = {};
+        lora_block<2, GEMM ? 1 : 2>(x, la, m < M ? lora_id(la, m) : -1, m, nt, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<f32x4*>(&rows[wave][h][(lane & 31) * P + 8 * q + 4 * (lane >> 5)]) =
+                    f32x4{x[h][4 * q], x[h][4 * q + 1], x[h][4 * q + 2], x[h][4 * q + 3]};
+    }
+    __syncthreads();
+    if (!work || n >= NT) return;
+    if (work && n < NT) {
+        const float* src = part + (size_t)(i * 32 + (lane >> 3)) * 2 * (size_t)NT + n;
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const float* q = src + s * stride + t * (size_t)16 * NT;
+                f32x4 x[2] = {};
+                if (i * 32 + 8 * t + (lane >> 3) < M) {
+                    x[0] = *reinterpret_cast<const f32x4*>(q);
+                    x[1] = *reinterpret_cast<const f32x4*>(q + NT);
+                }
+                g[t] = s == 0 ? x[0] : g[t] + x[0];
+                u[t] = s == 0 ? x[1] : u[t] + x[1];
+            }
+    }
     const int oc = GEMM ? (n / PACK_BN) * PACK_ROWS + n % PACK_BN : n;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int r = 8 * t + (lane >> 3), m = i * 32 + r;
         if (m >= M) continue;
-        const float* src = part + (size_t)m * 2 * (size_t)NT + n;
-        f32x4 g = *reinterpret_cast<const f32x4*>(src), u = *reinterpret_cast<const f32x4*>(src + NT);
-#pragma unroll 4
-        for (int s = 1; s < S; ++s) {
-            g += *reinterpret_cast<const f32x4*>(src + s * stride);
-            u += *reinterpret_cast<const f32x4*>(src + s * stride + NT);
-        }
         if (la.delta) {
-            g += lora_read4(la, GEMM ? 1 : 2, m, 0, oc);
-            u += lora_read4(la, GEMM ? 1 : 2, m, GEMM ? 0 : 1, GEMM ? oc + PACK_BN : oc);
+            g[t] += lora_read4(la, GEMM ? 1 : 2, m, 0, oc);
+            u[t] += lora_read4(la, GEMM ? 1 : 2, m, GEMM ? 0 : 1, GEMM ? oc + PACK_BN : oc);
         } else {
-            g += *reinterpret_cast<const f32x4*>(&rows[wave][0][r * P + 4 * (lane & 7)]);
-            u += *reinterpret_cast<const f32x4*>(&rows[wave][1][r * P + 4 * (lane & 7)]);
+            g[t] += *reinterpret_cast<const f32x4*>(&rows[wave][0][r * P + 4 * (lane & 7)]);
+            u[t] += *reinterpret_cast<const f32x4*>(&rows[wave][1][r * P + 4 * (lane & 7)]);
         }
         if constexpr (GEMM) {
             if (oc < N)
-                *reinterpret_cast<u32x2*>(Y + (size_t)m * N + oc) = u32x2{pack2(g[0], g[1]), pack2(g[2], g[3])};
+                *reinterpret_cast<u32x2*>(Y + (size_t)m * N + oc) = u32x2{pack2(g[t][0], g[t][1]), pack2(g[t][2], g[t][3])};
             if (oc + PACK_BN < N)
-                *reinterpret_cast<u32x2*>(Y + (size_t)m * N + oc + PACK_BN) = u32x2{pack2(u[0], u[1]), pack2(u[2], u[3])};
+                *reinterpret_cast<u32x2*>(Y + (size_t)m * N + oc + PACK_BN) =
+                    u32x2{pack2(u[t][0], u[t][1]), pack2(u[t][2], u[t][3])};
         } else {
             *reinterpret_cast<u32x2*>(Y + (size_t)m * N + n) =
-                u32x2{pack2(silu_f(g[0]) * u[0], silu_f(g[1]) * u[1]), pack2(silu_f(g[2]) * u[2], silu_f(g[3]) * u[3])};
+                u32x2{pack2(silu_f(g[t][0]) * u[t][0], silu_f(g[t][1]) * u[t][1]),
+                      pack2(silu_f(g[t][2]) * u[t][2], silu_f(g[t][3]) * u[t][3])};
         }
     }
 }
