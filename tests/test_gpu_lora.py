@@ -130,6 +130,16 @@ def test_plain(dev, M, K, N, L, r, kind):
     check_plain(plain(t, r), t, "%s %s" % ((M, K, N, L, r), kind))
 
 
+@pytest.mark.parametrize("kind", ["runs", "mixed", "none"])
+@pytest.mark.parametrize("M,K,N,r", [(66, 2056, 264, 16), (130, 2048, 264, 40), (256, 1096, 1032, 8),
+                                     (257, 4864, 520, 64), (600, 4096, 264, 24), (1023, 1032, 776, 16)])
+def test_split_contraction(dev, M, K, N, r, kind):
+    """Few output tiles: K is split, the adapters join where the sums do."""
+    t = case(dev, M, K, N, 9, r, ("1", "2", ""), kind)
+    check_gated(gated(t, r), t, "%s %s" % ((M, K, N, r), kind))
+    check_plain(plain(t, r), t, "%s %s" % ((M, K, N, r), kind))
+
+
 @pytest.mark.parametrize("kind", ["none", "outside", "same"])
 @pytest.mark.parametrize("M,K,N,L,r", [(5, 200, 264, 4, 16), (70, 4096, 512, 3, 16), (100, 72, 136, 4, 40),
                                        (600, 264, 1032, 4, 16)])
@@ -170,7 +180,7 @@ def test_rows_are_independent(dev, M, K, N):
     assert not torch.isfinite(Cb[M // 3]).any()
 
 
-@pytest.mark.parametrize("M,K,N,r", [(700, 200, 776, 24), (2100, 72, 520, 40)])
+@pytest.mark.parametrize("M,K,N,r", [(700, 200, 776, 24), (2100, 72, 520, 40), (600, 2048, 520, 40)])
 def test_neighbours_adapters_leave_a_row_as_it_is(dev, M, K, N, r):
     """Long batches: a row of adapter 0 gets the same bits beside rows of one, of
     three or of many other adapters, and beside adapters with NaN or infinities."""
