@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs la, float* __
 // lora_block forms the adapters' part in a matrix instruction's lanes, LDS turns it
 // into rows, and the sums are read and the outputs stored along rows (eight lanes
 // to 128 bytes of sums: in the other order, 32 rows a load at a stride of a whole
-// row, the kernel took 45 us for 2000 x 896 outputs of rank 64, this way 20; with
+// row, the kernel took 45 us for 2000 x 896 outputs of rank 64, this way 19; with
 // the adapters' part on the vector units 30).
 // ---------------------------------------------------------------------------
 template <bool GEMM>
