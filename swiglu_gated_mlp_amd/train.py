@@ -149,7 +149,7 @@ class _Swiglu(torch.autograd.Function):
             Y, kept = swiglu_fused(rows, W1, W2), ()
         else:
             Y, *kept = swiglu_train_forward(rows, W1, W2)
-        ctx.lead = A.shape[:-1]
+        ctx.shape = A.shape
         ctx.save_for_backward(rows, W1, W2, *kept)
         return Y.view(*A.shape[:-1], W1.shape[1])
 
@@ -160,7 +160,7 @@ class _Swiglu(torch.autograd.Function):
         need_a, need_1, need_2 = ctx.needs_input_grad[:3]
         dA, dW1, dW2 = swiglu_train_backward(_rows(dY), rows, W1, W2, *kept, need_dA=need_a,
                                              need_dW=need_1 or need_2)
-        return (dA.view(*ctx.lead, -1) if need_a else None, dW1 if need_1 else None, dW2 if need_2 else None, None)
+        return (dA.view(ctx.shape) if need_a else None, dW1 if need_1 else None, dW2 if need_2 else None, None)
 
 
 class _SwigluMlp(torch.autograd.Function):
@@ -169,7 +169,7 @@ class _SwigluMlp(torch.autograd.Function):
         rows = _rows(A)
         Y, G, U = swiglu_train_forward(rows, W1, W2)
         Z = swiglu_gemm_bf16(Y, W3)
-        ctx.lead = A.shape[:-1]
+        ctx.shape = A.shape
         ctx.save_for_backward(rows, W1, W2, W3, G, U, Y)
         return Z.view(*A.shape[:-1], W3.shape[1])
 
@@ -178,7 +178,7 @@ class _SwigluMlp(torch.autograd.Function):
     def backward(ctx, dZ):
         need = ctx.needs_input_grad
         grads = swiglu_mlp_train_backward(_rows(dZ), *ctx.saved_tensors, need_dA=need[0], need_dW=any(need[1:]))
-        dA = grads[0].view(*ctx.lead, -1) if need[0] else None
+        dA = grads[0].view(ctx.shape) if need[0] else None
         return (dA,) + tuple(g if n else None for g, n in zip(grads[1:], need[1:]))
 
 

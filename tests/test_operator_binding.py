@@ -1,0 +1,56 @@
+"""The Python side of the training and adapter operators without a GPU: the calls run
+on CPU tensors, and a stand-in for the library records what reaches its entry points
+(its host functions, the workspace sizes, are the library's own)."""
+import pytest
+import torch
+
+import swiglu_gated_mlp_amd as sw
+
+BF = dict(dtype=torch.bfloat16)
+
+
+class StandIn:
+    """The library with its launching entry points replaced: each call is recorded and
+    handed to `launch(name, args)`."""
+
+    def __init__(self, real, launch=None):
+        self.real, self.launch, self.calls = real, launch, []
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(self.real, name)
+
+        def call(*args):
+            self.calls.append((name, args))
+            if self.launch is not None:
+                self.launch(name, args)
+            return 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = StandIn(sw.lib())
+    for m in (sw, sw.train, sw.lora):
+        monkeypatch.setattr(m, "lib", lambda: lib)
+        monkeypatch.setattr(m, "_dev_bf16", lambda t, name: t.data_ptr(), raising=False)
+        monkeypatch.setattr(m, "_stream", lambda stream: 0 if stream is None else int(stream))
+    monkeypatch.setattr(sw.lora, "_dev_vec", lambda t, dtype, n, name: t.data_ptr())
+    return lib
+
+
+@pytest.mark.parametrize("lead", [(0,), (2, 0), (0, 3)])
+@pytest.mark.parametrize("fn", ["kept", "recomputed", "block"])
+def test_backward_of_an_empty_batch(library, fn, lead):
+    """No rows: an empty gradient of A in A's own shape, gradients for the weights."""
+    K, N = 64, 72
+    A = torch.zeros(*lead, K, **BF).requires_grad_()
+    W = [torch.zeros(*s, **BF).requires_grad_() for s in ((K, N), (K, N), (N, K))]
+    if fn == "block":
+        out = sw.swiglu_mlp(A, *W)
+    else:
+        W.pop()
+        out = sw.swiglu(A, *W, recompute=fn == "recomputed")
+    assert out.shape == (*lead, W[-1].shape[1])
+    grads = torch.autograd.grad(out, [A] + W, torch.zeros_like(out))
+    assert [g.shape for g in grads] == [t.shape for t in [A] + W]
