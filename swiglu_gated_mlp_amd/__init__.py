@@ -395,12 +395,18 @@ def _resolve_workspace(workspace, need: int, device: torch.device, s: int):
     return ws, (0 if ws is None else ws.numel() * ws.element_size())
 
 
+def _on(s: int, device) -> torch.cuda.StreamContext:
+    """The stream of handle s made current.  Handle 0 is the default stream, which
+    ExternalStream cannot name: it takes 0 for no handle and gives a stream of the pool."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(s, device=device) if s else torch.cuda.default_stream(device))
+
+
 def _new(shape, device, s: int, stream=None) -> torch.Tensor:
     """An uninitialised bf16 output, allocated on the stream that writes it (s;
     stream: the caller's argument, None for the current one)."""
     if stream is None or s == torch.cuda.current_stream(device).cuda_stream:
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(s, device=device)):
+    with _on(s, device):
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
 
 
@@ -444,7 +450,7 @@ class Workspace:
             if stream is None or stream == torch.cuda.current_stream(self.device).cuda_stream:
                 self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
             else:
-                with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
+                with _on(stream, self.device):
                     self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         return self.buf
 

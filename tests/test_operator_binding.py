@@ -54,3 +54,57 @@ def test_backward_of_an_empty_batch(library, fn, lead):
     assert out.shape == (*lead, W[-1].shape[1])
     grads = torch.autograd.grad(out, [A] + W, torch.zeros_like(out))
     assert [g.shape for g in grads] == [t.shape for t in [A] + W]
+
+
+class Streams:
+    """torch's streams by their handles: the current one, the ones under capture, and on
+    which each buffer was allocated."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.capturing, self.allocated = 3, set(), []
+        empty = torch.empty
+
+        class Stream:
+            def __init__(self, handle):
+                self.cuda_stream = handle
+
+        class Using:
+            def __init__(use, stream):
+                use.handle = stream.cuda_stream
+
+            def __enter__(use):
+                use.before, self.current = self.current, use.handle
+
+            def __exit__(use, *exc):
+                self.current = use.before
+
+        def recorded(*args, **kw):
+            self.allocated.append(self.current)
+            return empty(*args, **kw)
+
+        monkeypatch.setattr(torch, "empty", recorded)
+        for name, value in (
+                ("current_stream", lambda device=None: Stream(self.current)),
+                ("default_stream", lambda device=None: Stream(0)),
+                # a handle of 0 gives a stream of the pool, as in torch
+                ("ExternalStream", lambda handle, device=None: Stream(handle or 999)),
+                ("stream", Using), ("current_device", lambda: 0), ("is_initialized", lambda: True),
+                ("is_current_stream_capturing", lambda: self.current in self.capturing)):
+            monkeypatch.setattr(torch.cuda, name, value)
+        monkeypatch.setattr(sw, "_raw_stream", lambda device: self.current)
+
+
+@pytest.fixture
+def streams(monkeypatch):
+    return Streams(monkeypatch)
+
+
+CPU = torch.device("cpu")
+
+
+@pytest.mark.parametrize("handle", [0, 3, 7])
+def test_buffers_belong_to_the_stream_that_uses_them(streams, handle):
+    """Also where that is the default stream, whose handle is 0, and another is current."""
+    sw._new((2, 8), CPU, handle, handle)
+    sw.Workspace(CPU).get(64, handle)
+    assert streams.allocated == [handle, handle] and streams.current == 3
