@@ -411,12 +411,16 @@ def _new(shape, device, s: int, stream=None) -> torch.Tensor:
 
 
 def _scratch(workspace, need: int, device, s: int):
-    """As _resolve_workspace; a call under graph capture without a workspace of
-    its own gets a buffer of the graph's pool, so that no buffer that a graph
-    writes on replay is handed to another call."""
+    """As _resolve_workspace; a call without a workspace of its own on a stream under
+    graph capture (s, which need not be the current one) gets a buffer of the graph's
+    pool on that stream, so that no buffer that a graph writes on replay is handed to
+    another call."""
     if workspace is None:
         if need == 0:
             return None, 0
+        if s != torch.cuda.current_stream(device).cuda_stream:
+            with _on(s, device):
+                return _scratch(workspace, need, device, s)
         if torch.cuda.is_current_stream_capturing():
             return torch.empty(need, dtype=torch.uint8, device=device), need
         buf = _workspace_for(device, s).buf

@@ -59,3 +59,55 @@ def test_default_stream_given_beside_another(dev):
             assert stream_of(sw.Workspace(dev).get(1 << 20, 0)) == 0
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def operators(dev, M, K, N, seed):
+    """A batch, and its training and adapter calls as fn(stream) -> outputs."""
+    L, r = 5, 16
+    g = torch.Generator(device=dev).manual_seed(seed)
+
+    def rnd(*shape):
+        return (torch.randn(*shape, generator=g, device=dev) * shape[-2] ** -0.5).to(torch.bfloat16)
+
+    dZ, dY, A, G, U, Y = rnd(M, K), rnd(M, N), rnd(M, K), rnd(M, N), rnd(M, N), rnd(M, N)
+    W1, W2, W3 = rnd(K, N), rnd(K, N), rnd(N, K)
+    ids = (torch.arange(M, device=dev) * 7 // 3 % (L + 1) - 1).int()
+    scales = torch.rand(L, generator=g, device=dev) + 0.5
+    Wp, Wg = sw.swiglu_pack_weights(W1, W2), sw.swiglu_gemm_pack_weight(W1)
+    Lp = sw.swiglu_lora_pack(rnd(L, K, r), rnd(L, r, N), rnd(L, K, r), rnd(L, r, N))
+    Lg = sw.swiglu_gemm_lora_pack(rnd(L, K, r), rnd(L, r, N))
+    return (lambda s=None: sw.swiglu_train_forward(A, W1, W2, stream=s) +
+            sw.swiglu_train_backward(dY, A, W1, W2, stream=s) +
+            sw.swiglu_mlp_train_backward(dZ, A, W1, W2, W3, G, U, Y, stream=s) +
+            (sw.swiglu_fused_packed_lora(A, Wp, Lp, ids, scales, N, r, stream=s),
+             sw.swiglu_gemm_packed_lora(A, Wg, Lg, ids, scales, N, r, stream=s)))
+
+
+# adapters' factors read in the lanes, from memory, and on the matrix units; split and whole products
+BATCHES = [(16, 200, 264), (130, 1096, 776), (600, 2048, 520)]
+
+
+def test_capture_forked_to_another_stream(dev):
+    """Calls given a side stream of a capture, with the capturing stream's own allocations
+    and writes beside them: every replay gives the eager results."""
+    runs = [operators(dev, *b, seed) for seed, b in enumerate(BATCHES)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    side, graph, outs = torch.cuda.Stream(), torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        for run in runs:
+            outs.append(run(side))
+            for log in range(9, 25):   # blocks of every size the calls could have left behind
+                torch.empty(1 << log, dtype=torch.uint8, device=dev).fill_(0xFF)
+        main.wait_stream(side)
+    for _ in range(4):
+        for out in outs:
+            for t in out:
+                t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.isfinite(torch.randn(1 << 16, device=dev).sum())
+        for out, ref in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))

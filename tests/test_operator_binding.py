@@ -108,3 +108,14 @@ def test_buffers_belong_to_the_stream_that_uses_them(streams, handle):
     sw._new((2, 8), CPU, handle, handle)
     sw.Workspace(CPU).get(64, handle)
     assert streams.allocated == [handle, handle] and streams.current == 3
+
+
+@pytest.mark.parametrize("capturing", [{3, 7}, {7}])
+def test_workspace_of_a_captured_stream(streams, capturing):
+    """A call on stream 7 under capture, with stream 3 current (the capture forked, or not
+    joined by 3): its own buffer of stream 7, never one kept for other calls."""
+    streams.capturing = capturing
+    first, nbytes = sw._scratch(None, 64, CPU, 7)
+    assert nbytes >= 64 and streams.allocated == [7]
+    second, _ = sw._scratch(None, 64, CPU, 7)
+    assert second.data_ptr() != first.data_ptr() and streams.allocated == [7, 7] and streams.current == 3
