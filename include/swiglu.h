@@ -44,7 +44,10 @@
  *    leave every output untouched.  A failed launch returns SWIGLU_ERR_HIP and
  *    swiglu_last_hip_error() gives the hipError_t (per calling thread).
  *  - Thread safety: every entry point is re-entrant.  Calls on different
- *    streams may overlap as long as their outputs and workspaces differ.
+ *    streams, or from different threads on one stream, may overlap as long as
+ *    their outputs and workspaces differ: a call may be several launches that
+ *    pass data through its workspace, and another thread's launches on the same
+ *    stream may fall between them.
  */
 #ifndef SWIGLU_H_
 #define SWIGLU_H_
@@ -223,7 +226,8 @@ int swiglu_choose_variant(int64_t M, int64_t K, int64_t N);
  * Every call on one device shares that device's array, which keeps the last
  * call's contents (nothing in it needs clearing: each split writes all of
  * its partial sums before the reduction reads them).  Calls that overlap in
- * time on one device race on it: issue them on one stream, or order them.
+ * time on one device race on it: issue them from one thread at a time on one
+ * stream, or order them.
  * ---------------------------------------------------------------------- */
 #define SWIGLU_NOALLOC_SCRATCH_BYTES (32u << 20)
 swiglu_status swiglu_fused_packed_noalloc(const swiglu_bf16 *A,

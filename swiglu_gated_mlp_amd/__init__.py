@@ -378,21 +378,22 @@ def swiglu_mlp_workspace_bytes(M: int, K: int, N: int, variant: int = VARIANT_AU
     return int(lib().swiglu_mlp_workspace_bytes(M, K, N, int(variant)))
 
 
-def _resolve_workspace(workspace, need: int, device: torch.device, s: int):
-    """(pointer-able tensor or None, its bytes) for a call needing `need`
-    bytes: a caller tensor as given, a Workspace grown to `need`, or the
-    cached per-stream Workspace."""
-    if need == 0 and not isinstance(workspace, torch.Tensor):
-        ws = None
-    elif isinstance(workspace, Workspace):
-        ws = workspace.get(need, s)
-    elif workspace is None:
-        ws = _workspace_for(device, s).get(need, s)
-    else:
-        ws = workspace
-    if ws is not None and ws.device.type != "cuda":
+def _scratch(workspace, need: int, device: torch.device, s: int):
+    """(pointer-able tensor or None, its bytes) for a call on the stream of handle s
+    needing `need` bytes: a caller tensor as given, a Workspace grown to `need`, or,
+    without either, a buffer of this call alone, allocated on s.  None is kept for the
+    next call: a call is several launches, and another thread's, or a graph's on replay,
+    may fall between them.  On return the buffer goes back to the allocator, which hands
+    it out again only to work that s orders after the call (a captured one: in the
+    graph's pool)."""
+    if workspace is not None and workspace.device.type != "cuda":
         raise ValueError("workspace must be a GPU tensor")
-    return ws, (0 if ws is None else ws.numel() * ws.element_size())
+    if isinstance(workspace, torch.Tensor):
+        return workspace, workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, 0
+    ws = _empty(need, torch.uint8, device, s) if workspace is None else workspace.get(need, s)
+    return ws, ws.numel()
 
 
 def _on(s: int, device) -> torch.cuda.StreamContext:
@@ -401,32 +402,27 @@ def _on(s: int, device) -> torch.cuda.StreamContext:
     return torch.cuda.stream(torch.cuda.ExternalStream(s, device=device) if s else torch.cuda.default_stream(device))
 
 
+def _current(device) -> int:
+    """Handle of the device's current stream."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(torch.cuda.current_device() if device.index is None else device.index)
+
+
+def _empty(shape, dtype, device, s: int) -> torch.Tensor:
+    """An uninitialised tensor, allocated on the stream of handle s."""
+    if s == _current(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(s, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _new(shape, device, s: int, stream=None) -> torch.Tensor:
     """An uninitialised bf16 output, allocated on the stream that writes it (s;
     stream: the caller's argument, None for the current one)."""
-    if stream is None or s == torch.cuda.current_stream(device).cuda_stream:
+    if stream is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=device)
-    with _on(s, device):
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
-
-
-def _scratch(workspace, need: int, device, s: int):
-    """As _resolve_workspace; a call without a workspace of its own on a stream under
-    graph capture (s, which need not be the current one) gets a buffer of the graph's
-    pool on that stream, so that no buffer that a graph writes on replay is handed to
-    another call."""
-    if workspace is None:
-        if need == 0:
-            return None, 0
-        if s != torch.cuda.current_stream(device).cuda_stream:
-            with _on(s, device):
-                return _scratch(workspace, need, device, s)
-        if torch.cuda.is_current_stream_capturing():
-            return torch.empty(need, dtype=torch.uint8, device=device), need
-        buf = _workspace_for(device, s).buf
-        if buf is not None and buf.numel() >= need:
-            return buf, buf.numel()
-    return _resolve_workspace(workspace, need, device, s)
+    return _empty(shape, torch.bfloat16, device, s)
 
 
 def swiglu_choose_variant(M: int, K: int, N: int) -> int:
@@ -434,9 +430,10 @@ def swiglu_choose_variant(M: int, K: int, N: int) -> int:
 
 
 class Workspace:
-    """Device scratch for the split-K schedule (fp32 partial sums), grown on
-    demand.  Its contents never need clearing.  One Workspace must not be
-    shared by calls that may run concurrently."""
+    """Device scratch that calls given it use one after another (sums of splits,
+    operands of a later launch), grown on demand.  Its contents never need clearing.
+    One Workspace must not be shared by calls that may run concurrently, nor by
+    threads, not even on one stream: a call is several launches."""
 
     def __init__(self, device=None):
         self.device = torch.device(device or "cuda")
@@ -451,23 +448,9 @@ class Workspace:
             return None
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = None
-            if stream is None or stream == torch.cuda.current_stream(self.device).cuda_stream:
-                self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            else:
-                with _on(stream, self.device):
-                    self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            s = _current(self.device) if stream is None else stream
+            self.buf = _empty(nbytes, torch.uint8, self.device, s)
         return self.buf
-
-
-_default_ws: dict = {}
-
-
-def _workspace_for(device: torch.device, stream_handle: int) -> Workspace:
-    key = (device.index, stream_handle)
-    ws = _default_ws.get(key)
-    if ws is None:
-        ws = _default_ws[key] = Workspace(device)
-    return ws
 
 
 def swiglu_fused_packed(A: torch.Tensor, Wp: torch.Tensor, N: int, Y: torch.Tensor | None = None,
@@ -476,7 +459,7 @@ def swiglu_fused_packed(A: torch.Tensor, Wp: torch.Tensor, N: int, Y: torch.Tens
     """Y = SiLU(A W1) * (A W2) from packed weights; returns Y [M,N] bf16.
 
     ``workspace`` may be a uint8 tensor of at least swiglu_workspace_bytes()
-    bytes, a Workspace, or None (a cached per-stream Workspace is used)."""
+    bytes, a Workspace, or None (a buffer of this call alone)."""
     M, K = A.shape
     _packed_at_least(Wp, K, N)
     _shape(Y, (M, N), "Y")
@@ -485,7 +468,7 @@ def swiglu_fused_packed(A: torch.Tensor, Wp: torch.Tensor, N: int, Y: torch.Tens
     s = _stream(stream)
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-    ws, ws_bytes = _resolve_workspace(workspace, _workspace_need(M, K, N, int(variant), A.device), A.device, s)
+    ws, ws_bytes = _scratch(workspace, _workspace_need(M, K, N, int(variant), A.device), A.device, s)
     st = lib().swiglu_fused_packed(_dev_bf16(A, "A"), _dev_bf16(Wp, "Wp"), _dev_bf16(Y, "Y"), M, K, N,
                                    _ptr(ws), ws_bytes, int(variant), s)
     _check("swiglu_fused_packed", st)
@@ -551,14 +534,14 @@ def swiglu_gemm_pack_weight(W: torch.Tensor, Wg: torch.Tensor | None = None, str
 def swiglu_gemm_packed(A: torch.Tensor, Wg: torch.Tensor, N: int, C: torch.Tensor | None = None,
                        workspace: torch.Tensor | Workspace | None = None, stream=None) -> torch.Tensor:
     """C = bf16(A @ W) with fp32 accumulation from a single-weight pack.
-    ``workspace`` as in swiglu_fused_packed (None: the cached per-stream one,
-    so split-K runs where the plan asks for it)."""
+    ``workspace`` as in swiglu_fused_packed (split-K runs where the plan asks
+    for it)."""
     M, K = A.shape
     _gemm_packed_at_least(Wg, K, N)
     _shape(C, (M, N), "C")
     C = torch.empty((M, N), dtype=torch.bfloat16, device=A.device) if C is None else C
     s = _stream(stream)
-    ws, ws_bytes = _resolve_workspace(workspace, _cached_need("gemm", (M, K, N), A.device), A.device, s)
+    ws, ws_bytes = _scratch(workspace, _cached_need("gemm", (M, K, N), A.device), A.device, s)
     st = lib().swiglu_gemm_packed(_dev_bf16(A, "A"), _dev_bf16(Wg, "Wg"), _dev_bf16(C, "C"), M, K, N,
                                   _ptr(ws), ws_bytes, s)
     _check("swiglu_gemm_packed", st)
@@ -637,7 +620,7 @@ def swiglu_mlp_packed(A: torch.Tensor, Wp: torch.Tensor, W3g: torch.Tensor, N: i
     s = _stream(stream)
     Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device) if Y is None else Y
     Z = torch.empty((M, K), dtype=torch.bfloat16, device=A.device) if Z is None else Z
-    ws, ws_bytes = _resolve_workspace(workspace, _cached_need("mlp", (M, K, N, int(variant)), A.device),
+    ws, ws_bytes = _scratch(workspace, _cached_need("mlp", (M, K, N, int(variant)), A.device),
                                       A.device, s)
     st = lib().swiglu_mlp_packed(_dev_bf16(A, "A"), _dev_bf16(Wp, "Wp"), _dev_bf16(W3g, "W3g"),
                                  _dev_bf16(Y, "Y"), _dev_bf16(Z, "Z"), M, K, N, _ptr(ws), ws_bytes,
@@ -655,7 +638,7 @@ def swiglu_mlp_down(Y: torch.Tensor, W3g: torch.Tensor, K: int, Z: torch.Tensor 
     _shape(Z, (M, K), "Z")
     Z = torch.empty((M, K), dtype=torch.bfloat16, device=Y.device) if Z is None else Z
     s = _stream(stream)
-    ws, ws_bytes = _resolve_workspace(workspace, _cached_need("gemm", (M, N, K), Y.device), Y.device, s)
+    ws, ws_bytes = _scratch(workspace, _cached_need("gemm", (M, N, K), Y.device), Y.device, s)
     st = lib().swiglu_mlp_down(_dev_bf16(Y, "Y"), _dev_bf16(W3g, "W3g"), _dev_bf16(Z, "Z"), M, K, N,
                                _ptr(ws), ws_bytes, s)
     _check("swiglu_mlp_down", st)
@@ -681,7 +664,7 @@ def swiglu_mlp_unfused(A: torch.Tensor, W1g: torch.Tensor, W2g: torch.Tensor, W3
     Y = mk(M, N) if Y is None else Y
     Z = mk(M, K) if Z is None else Z
     s = _stream(stream)
-    ws, ws_bytes = _resolve_workspace(workspace, _cached_need("gemm", (M, N, K), A.device), A.device, s)
+    ws, ws_bytes = _scratch(workspace, _cached_need("gemm", (M, N, K), A.device), A.device, s)
     st = lib().swiglu_mlp_unfused(_dev_bf16(A, "A"), _dev_bf16(W1g, "W1g"), _dev_bf16(W2g, "W2g"),
                                   _dev_bf16(W3g, "W3g"), _dev_bf16(G, "G"), _dev_bf16(U, "U"),
                                   _dev_bf16(Y, "Y"), _dev_bf16(Z, "Z"), M, K, N, _ptr(ws), ws_bytes, s)

@@ -1,5 +1,7 @@
 """The training and adapter operators as a program issues them: empty batches, other
 streams, captures and several threads."""
+import threading
+
 import pytest
 import torch
 
@@ -111,3 +113,65 @@ def test_capture_forked_to_another_stream(dev):
         assert torch.isfinite(torch.randn(1 << 16, device=dev).sum())
         for out, ref in zip(outs, want):
             assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_threads_on_one_stream(dev):
+    """Calls of different sizes from several threads, all on the default stream, give what
+    one thread's calls give; and no call keeps memory after it."""
+    runs = [operators(dev, *b, seed) for seed, b in enumerate(BATCHES)]
+    want = [run() for run in runs]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated(dev)
+    for run in runs:
+        run()
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated(dev) == before
+    wrong, gate = [], threading.Barrier(len(runs), timeout=60)
+
+    def thread(run, ref):
+        try:
+            gate.wait()
+            for i in range(30):
+                wrong.extend((i, j) for j, (a, b) in enumerate(zip(run(), ref)) if not torch.equal(a, b))
+        except Exception as e:   # noqa: BLE001
+            wrong.append(e)
+            gate.abort()
+
+    threads = [threading.Thread(target=thread, args=a) for a in zip(runs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_block_gradients_from_threads(dev):
+    """Forward and backward passes of the differentiable block in two threads: the backward
+    passes run on autograd's thread beside the other's calls."""
+    def weights(M, K, N):
+        g = torch.Generator(device=dev).manual_seed(M)
+        return [(torch.randn(*s, generator=g, device=dev) * s[0] ** -0.5).to(torch.bfloat16).requires_grad_()
+                for s in ((M, K), (K, N), (K, N), (N, K))]
+
+    def step(leaves):
+        Z = sw.swiglu_mlp(*leaves)
+        return (Z.detach(),) + torch.autograd.grad(Z, leaves, torch.ones_like(Z))
+
+    sets = [weights(333, 896, 1160), weights(70, 264, 2056)]
+    want = [step(s) for s in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def thread(leaves, ref):
+        try:
+            for i in range(30):
+                wrong.extend((i, j) for j, (a, b) in enumerate(zip(step(leaves), ref)) if not torch.equal(a, b))
+        except Exception as e:   # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=thread, args=a) for a in zip(sets, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

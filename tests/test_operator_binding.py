@@ -1,6 +1,8 @@
 """The Python side of the training and adapter operators without a GPU: the calls run
 on CPU tensors, and a stand-in for the library records what reaches its entry points
 (its host functions, the workspace sizes, are the library's own)."""
+import threading
+
 import pytest
 import torch
 
@@ -119,3 +121,55 @@ def test_workspace_of_a_captured_stream(streams, capturing):
     assert nbytes >= 64 and streams.allocated == [7]
     second, _ = sw._scratch(None, 64, CPU, 7)
     assert second.data_ptr() != first.data_ptr() and streams.allocated == [7, 7] and streams.current == 3
+
+
+# a call's name, and the argument that holds its workspace
+WORKSPACE_AT = {"swiglu_train_forward": 9, "swiglu_train_backward": 12, "swiglu_mlp_train_backward": 15,
+                "swiglu_fused_packed_lora": 11, "swiglu_gemm_packed_lora": 11, "swiglu_fused_packed": 6,
+                "swiglu_gemm_packed": 6, "swiglu_mlp_packed": 8, "swiglu_mlp_down": 6, "swiglu_mlp_unfused": 11}
+M, K, N, L, R = 130, 4096, 264, 3, 16   # every product splits K (of 65 rows where it is on its own)
+
+
+def calls():
+    a, y, w, v = (torch.zeros(*s, **BF) for s in ((M, K), (M, N), (K, N), (N, K)))
+    wp = torch.zeros(sw.swiglu_packed_bytes(K, N) // 2, **BF)
+    wg, vg = (torch.zeros(sw.swiglu_gemm_packed_bytes(*s) // 2, **BF) for s in ((K, N), (N, K)))
+    lp = torch.zeros(sw.swiglu_lora_packed_bytes(K, N, L, R) // 2, **BF)
+    ids, scales = torch.zeros(M, dtype=torch.int32), torch.ones(L)
+    return {"swiglu_train_forward": lambda: sw.swiglu_train_forward(a, w, w),
+            "swiglu_train_backward": lambda: sw.swiglu_train_backward(y, a, w, w),
+            "swiglu_mlp_train_backward": lambda: sw.swiglu_mlp_train_backward(a, a, w, w, v, y, y, y),
+            "swiglu_fused_packed_lora": lambda: sw.swiglu_fused_packed_lora(a, wp, lp, ids, scales, N, R),
+            "swiglu_gemm_packed_lora": lambda: sw.swiglu_gemm_packed_lora(a, wg, lp, ids, scales, N, R),
+            "swiglu_fused_packed": lambda: sw.swiglu_fused_packed(a, wp, N, variant=sw.VARIANT_SPLIT_K),
+            "swiglu_gemm_packed": lambda: sw.swiglu_gemm_packed(a[:65], wg, N),
+            "swiglu_mlp_packed": lambda: sw.swiglu_mlp_packed(a, wp, vg, N, variant=sw.VARIANT_SPLIT_K),
+            "swiglu_mlp_down": lambda: sw.swiglu_mlp_down(a[:65], wg, N),
+            "swiglu_mlp_unfused": lambda: sw.swiglu_mlp_unfused(y[:65], vg, vg, wg, K)}
+
+
+@pytest.mark.parametrize("name", sorted(WORKSPACE_AT))
+def test_threads_do_not_share_a_workspace(library, streams, name):
+    """Two threads in the same call on one stream: a call is several launches, and
+    another thread's may fall between them, so each call has a buffer of its own."""
+    streams.current = 0
+    gate = threading.Barrier(2, timeout=60)
+    library.launch = lambda fn, args: gate.wait()   # both are in the library at once
+    failed = []
+
+    def thread():
+        try:
+            calls()[name]()
+        except Exception as e:   # noqa: BLE001
+            failed.append(e)
+            gate.abort()
+
+    threads = [threading.Thread(target=thread) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    at = WORKSPACE_AT[name]
+    (p, n), (q, m) = [args[at:at + 2] for fn, args in library.calls]
+    assert n > 0 and m > 0 and (p + n <= q or q + m <= p), "both at %#x" % p
