@@ -190,5 +190,8 @@ def swiglu(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, recompute: bool 
 
 
 def swiglu_mlp(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, W3: torch.Tensor) -> torch.Tensor:
-    """Differentiable gated MLP block Z = (SiLU(A @ W1) * (A @ W2)) @ W3, A [..., K]."""
+    """Differentiable gated MLP block Z = (SiLU(A @ W1) * (A @ W2)) @ W3, A [..., K],
+    W3 [N,K] (any [N, ...] where no gradient is wanted)."""
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (A, W1, W2, W3)):
+        _shape(W3, (W1.shape[1], A.shape[-1]), "W3")
     return _SwigluMlp.apply(A, W1, W2, W3)

@@ -173,3 +173,17 @@ def test_threads_do_not_share_a_workspace(library, streams, name):
     at = WORKSPACE_AT[name]
     (p, n), (q, m) = [args[at:at + 2] for fn, args in library.calls]
     assert n > 0 and m > 0 and (p + n <= q or q + m <= p), "both at %#x" % p
+
+
+def test_block_refuses_what_its_backward_pass_would(library):
+    """W3 of other columns than A's has no backward pass: refused before the forward pass
+    runs where a gradient is wanted, and computed where none is."""
+    a, w = torch.zeros(4, 64, **BF), torch.zeros(64, 72, **BF)
+    wide = torch.zeros(72, 80, **BF)
+    for leaf in (a, w, wide):
+        with pytest.raises(ValueError, match=r"W3 must be \[72, 64\] \(got \[72, 80\]\)"):
+            sw.swiglu_mlp(*(t.clone().requires_grad_() if t is leaf else t for t in (a, w, w.clone(), wide)))
+    assert library.calls == []
+    assert sw.swiglu_mlp(a, w, w, wide).shape == (4, 80)
+    with torch.no_grad():
+        assert sw.swiglu_mlp(a.clone().requires_grad_(), w, w, wide).shape == (4, 80)
