@@ -105,8 +105,10 @@ __device__ __forceinline__ void st16(uint16_t* p, u32x4 v) { *reinterpret_cast<u
 // transposing LDS read waits for all loads in flight (vmcnt(0)), as it cannot
 // know that they fill other slots.  There is no register to write early; the
 // kernels wait with explicit counts, and the compiler's own waits for loads it
-// does track only wait for more than they must.  (m0, which holds the LDS address,
-// has no other use in these kernels.)
+// does track only wait for more than they must.  m0 holds the LDS address and is named
+// as overwritten, so that no pass of the compiler carries a value of its own in it past
+// a load.  (Its warning for a reserved register is off here: it says that the value in m0
+// is not kept over the statement, which is what is meant.)
 // ---------------------------------------------------------------------------
 constexpr int RSRC_END = 0x7FFFFFF0;          // every offset of a valid lane is below
 constexpr uint32_t OFF_NONE = 0xFFFFFFF0u;    // past every descriptor's end
@@ -114,11 +116,14 @@ __device__ __forceinline__ i32x4 stage_rsrc(const uint16_t* base, bool valid) {
     const uint64_t p = (uint64_t)base;
     return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, valid ? RSRC_END : 0, 0x00020000};
 }
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16_buffer(i32x4 rsrc, uint32_t off, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
                  "s"(rsrc)
-                 : "memory");
+                 : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // ---------------------------------------------------------------------------
 // The epilogue of one 32 x 32 MFMA block without LDS.  A lane holds 16 sums of
