@@ -7,8 +7,8 @@
 #include "host_common.hpp"
 #include "train_kernels.hpp"
 
-#include <array>
-#include <map>
+#include <algorithm>
+#include <mutex>
 
 using namespace swh;
 
@@ -228,20 +228,34 @@ Launch search_launch(int jobs, const Kind* kind, int64_t M, int64_t K, int64_t N
     return best;
 }
 
-// search_launch, remembered by shape (the choice depends on nothing else).
+// search_launch, remembered by shape (the choice depends on nothing else), in a table
+// of fixed size: nothing is allocated, so nothing can throw across the C interface.  A
+// shape has four places to lie in; with all of them taken the next one replaces one.
 Launch plan_launch(int jobs, const Kind* kind, int64_t M, int64_t K, int64_t N, int cus) {
+    struct Entry {
+        int64_t key[5];
+        Launch l;
+    };
+    constexpr int kEntries = 2048, kPlaces = 4;
+    static Entry seen[kEntries];
     static std::mutex mu;
-    static std::map<std::array<int64_t, 5>, Launch> seen;
-    const std::array<int64_t, 5> key = {jobs == 2 ? 16 * (kind[1] + 1) + kind[0] : kind[0], M, K, N, cus};
+    // M > 0: an entry of zeros is a free one
+    const int64_t key[5] = {jobs == 2 ? 16 * (kind[1] + 1) + kind[0] : kind[0], M, K, N, cus};
+    uint64_t h = 0;
+    for (const int64_t x : key) h = (h ^ (uint64_t)x) * 0x9E3779B97F4A7C15u;   // 2^64 / golden ratio
+    Entry* const at = seen + (h >> 32) % (kEntries / kPlaces) * kPlaces;
     {
         std::lock_guard<std::mutex> lock(mu);
-        const auto it = seen.find(key);
-        if (it != seen.end()) return it->second;
+        for (int i = 0; i < kPlaces; ++i)
+            if (std::equal(key, key + 5, at[i].key)) return at[i].l;
     }
     const Launch l = search_launch(jobs, kind, M, K, N, cus);
     std::lock_guard<std::mutex> lock(mu);
-    if (seen.size() >= 4096) seen.clear();
-    seen[key] = l;
+    int to = (int)(h >> 62);   // two bits that the place in the table does not depend on
+    for (int i = kPlaces - 1; i >= 0; --i)
+        if (at[i].key[1] == 0) to = i;
+    std::copy(key, key + 5, at[to].key);
+    at[to].l = l;
     return l;
 }
 
