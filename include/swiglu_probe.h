@@ -1,8 +1,9 @@
 /*
- * swiglu_probe.h -- diagnostic kernels of libswiglu that measure what this
+ * swiglu_probe.h -- diagnostics of libswiglu: kernels that measure what this
  * device actually sustains, for reading the fused kernel's roofline fraction
  * against more than the datasheet (the datasheet peaks assume the top clock
- * and ideal memory).  Not part of the fused product.
+ * and ideal memory), and the plans of the training calls.  Not part of the
+ * fused product.
  *
  * Same conventions as swiglu.h: device pointers, `stream` is a hipStream_t
  * (NULL = default), calls enqueue and return, errors are swiglu_status codes.
@@ -31,6 +32,24 @@ swiglu_status swiglu_probe_mfma(float *sink, int blocks, int iters, void *stream
  * `sink` (device, >= blocks * 256 uint32).  blocks >= 1. */
 swiglu_status swiglu_probe_read(const void *src, size_t bytes, uint32_t *sink, int blocks,
                                 void *stream);
+
+/* Host call, no launch: how a launch of the training calls is cut into work items at
+ * (M,K,N) on the current device.  `launch` is one of swiglu_train_launch; plan
+ * receives, for each of its one or two products, the tile's rows and columns
+ * (dual products: of both halves), the tiles run whole, the others, the parts
+ * each of these is split into over the contraction, and a part's 64-deep blocks.
+ * Returns the number of products, 0 for an invalid shape (or M == 0) or launch. */
+typedef enum {
+    SWIGLU_TRAIN_FORWARD = 0,    /* Y, G, U */
+    SWIGLU_TRAIN_RECOMPUTED = 1, /* dG, dU from Gate and Up computed again */
+    SWIGLU_TRAIN_DY = 2,         /* dG, dU from dY = dZ W3^T (no weight gradients) */
+    SWIGLU_TRAIN_DY_DW3 = 3,     /* the same, and dW3 */
+    SWIGLU_TRAIN_DA = 4,
+    SWIGLU_TRAIN_DW = 5,         /* dW1 | dW2 */
+    SWIGLU_TRAIN_DA_DW = 6,
+    SWIGLU_TRAIN_LAUNCHES = 7
+} swiglu_train_launch;
+int swiglu_probe_train_plan(int launch, int64_t M, int64_t K, int64_t N, int32_t plan[12]);
 
 #ifdef __cplusplus
 }

@@ -83,6 +83,7 @@ SIGNATURES = {
     # include/swiglu_probe.h (diagnostic ceilings)
     "swiglu_probe_mfma": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_read": ([_P, ctypes.c_size_t, _P, ctypes.c_int, _P], ctypes.c_int),
+    "swiglu_probe_train_plan": ([ctypes.c_int, _I64, _I64, _I64, _P], ctypes.c_int),
 }
 
 _lock = threading.Lock()
@@ -692,6 +693,22 @@ def swiglu_probe_read(src: torch.Tensor, sink: torch.Tensor, blocks: int, stream
         raise ValueError("sink must be a GPU int32 tensor of >= blocks*256 elements")
     _check("swiglu_probe_read", lib().swiglu_probe_read(src.data_ptr(), nbytes, sink.data_ptr(), blocks,
                                                         _stream(stream)))
+
+
+#: launches of the training calls (swiglu_train_launch)
+TRAIN_LAUNCHES = ("forward", "recomputed", "dy", "dy_dw3", "da", "dw", "da_dw")
+
+
+def swiglu_probe_train_plan(launch: str, M: int, K: int, N: int) -> list:
+    """How a launch of the training calls is cut at (M,K,N): for each of its products a
+    dict of the tile's rows and columns, the tiles run whole, the rest, the parts each of
+    these is split into, and the 64-deep blocks of a part."""
+    out = (ctypes.c_int32 * 12)()
+    n = lib().swiglu_probe_train_plan(TRAIN_LAUNCHES.index(launch), M, K, N, out)
+    if n == 0:
+        raise ValueError("invalid shape M=%d K=%d N=%d" % (M, K, N))
+    keys = ("rows", "cols", "whole", "rest", "splits", "blocks")
+    return [dict(zip(keys, out[6 * i:6 * i + 6])) for i in range(n)]
 
 
 # training (gradients and differentiable forms of the product and the block)

@@ -3,6 +3,7 @@
 // tiles and splits, and the launches.  Every check runs before the first HIP
 // call.
 #include "swiglu.h"
+#include "swiglu_probe.h"
 
 #include "host_common.hpp"
 #include "train_kernels.hpp"
@@ -558,6 +559,21 @@ swiglu_status swiglu_mlp_train_backward(const swiglu_bf16* dZ, const swiglu_bf16
     hipError_t e = run_launch(p.l[0], a, dw3, c.part, c.s);
     if (e == hipSuccess && (dA || dW1)) e = run_gradients(c, p.l[p.n - 1], A, W1, W2, dA, dW1, dW2);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+int swiglu_probe_train_plan(int launch, int64_t M, int64_t K, int64_t N, int32_t* plan) {
+    static const Kind kinds[SWIGLU_TRAIN_LAUNCHES][2] = {{F_KEEP}, {D_DUAL}, {D_DY},      {D_DY, G_DW3},
+                                                         {G_DA},   {G_DW},   {G_DA, G_DW}};
+    if (check_train_shape(M, K, N) != SWIGLU_OK || M == 0 || launch < 0 || launch >= SWIGLU_TRAIN_LAUNCHES || !plan)
+        return 0;
+    const int jobs = launch == SWIGLU_TRAIN_DY_DW3 || launch == SWIGLU_TRAIN_DA_DW ? 2 : 1;
+    const Launch l = plan_launch(jobs, kinds[launch], M, K, N, cu_count_now());
+    for (int i = 0; i < jobs; ++i) {
+        const Tiles& t = l.t[i];
+        const int32_t v[6] = {t.bm, t.bn, t.whole, t.rest, t.splits, t.kb_per_split};
+        std::copy(v, v + 6, plan + 6 * i);
+    }
+    return jobs;
 }
 
 }  // extern "C"

@@ -105,3 +105,20 @@ def test_binding_refusals():
         sw.swiglu_mlp_train_backward(y, a, w, w, w.t(), y, y, y)
     with pytest.raises(ValueError, match="Y is needed"):
         sw.swiglu_mlp_train_backward(a, a, w, w, torch.zeros(72, 64, **bf), y, y, None)
+
+
+def test_plan_probe():
+    assert len(sw.TRAIN_LAUNCHES) == 7
+    for launch in sw.TRAIN_LAUNCHES:
+        for shape in ((1, 8, 8), (333, 896, 4864), (4096, 3584, 18944)):
+            plan = sw.swiglu_probe_train_plan(launch, *shape)
+            assert len(plan) == (2 if launch in ("dy_dw3", "da_dw") else 1)
+            for p in plan:
+                assert p["whole"] + p["rest"] > 0 and p["splits"] >= 1 and p["blocks"] >= 1
+                assert (p["rest"] == 0) == (p["splits"] == 1)
+        with pytest.raises(ValueError, match="invalid shape"):
+            sw.swiglu_probe_train_plan(launch, 0, 64, 72)
+        with pytest.raises(ValueError, match="invalid shape"):
+            sw.swiglu_probe_train_plan(launch, 4, 60, 72)
+    L = sw.lib()
+    assert L.swiglu_probe_train_plan(7, 4, 64, 72, None) == 0 and L.swiglu_probe_train_plan(0, 4, 64, 72, None) == 0
