@@ -265,7 +265,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs la, float* __
 // lora_block forms the adapters' part in a matrix instruction's lanes, LDS turns it
 // into rows, and the sums are read and the outputs stored along rows (eight lanes
 // to 128 bytes of sums: in the other order, 32 rows a load at a stride of a whole
-// row, the kernel took 45 us for 2000 x 896 outputs of rank 64, this way 19; with
+// row, the kernel took 45 us for 2000 x 896 outputs of rank 64, this way 20; with
 // the adapters' part on the vector units 30).
 // ---------------------------------------------------------------------------
 template <bool GEMM>
@@ -299,21 +299,19 @@ __global__ __launch_bounds__(256) void lora_reduce_kernel(const float* __restric
     }
     __syncthreads();
     if (!work || n >= NT) return;
-    if (work && n < NT) {
-        const float* src = part + (size_t)(i * 32 + (lane >> 3)) * 2 * (size_t)NT + n;
-        for (int s = 0; s < S; ++s)
+    const float* src = part + (size_t)(i * 32 + (lane >> 3)) * 2 * (size_t)NT + n;
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const float* q = src + s * stride + t * (size_t)16 * NT;
-                f32x4 x[2] = {};
-                if (i * 32 + 8 * t + (lane >> 3) < M) {
-                    x[0] = *reinterpret_cast<const f32x4*>(q);
-                    x[1] = *reinterpret_cast<const f32x4*>(q + NT);
-                }
-                g[t] = s == 0 ? x[0] : g[t] + x[0];
-                u[t] = s == 0 ? x[1] : u[t] + x[1];
+        for (int t = 0; t < 4; ++t) {
+            const float* q = src + s * stride + t * (size_t)16 * NT;
+            f32x4 x[2] = {};
+            if (i * 32 + 8 * t + (lane >> 3) < M) {
+                x[0] = *reinterpret_cast<const f32x4*>(q);
+                x[1] = *reinterpret_cast<const f32x4*>(q + NT);
             }
-    }
+            g[t] = s == 0 ? x[0] : g[t] + x[0];
+            u[t] = s == 0 ? x[1] : u[t] + x[1];
+        }
     const int oc = GEMM ? (n / PACK_BN) * PACK_ROWS + n % PACK_BN : n;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
