@@ -455,8 +455,9 @@ swiglu_status swiglu_mlp_unfused(const swiglu_bf16 *A, const swiglu_bf16 *W1g,
  * swiglu_train_forward: Y = SiLU(G) U, and G and U rounded to bf16 (each [M,N]),
  *   which the backward calls take.
  * swiglu_train_backward: dA [M,K], dW1, dW2 [K,N].  G and U kept by the forward
- *   call, or both NULL: computed again from A, W1 and W2 (never written).  dA
- *   may be NULL (not wanted), and so may dW1 and dW2, together.
+ *   call, or both NULL: computed again from A, W1 and W2 and not kept (where a
+ *   small product's contraction is split, the fp32 sums of its parts pass through
+ *   the workspace).  dA may be NULL (not wanted), and so may dW1 and dW2, together.
  * swiglu_mlp_train_backward: dA, dW1, dW2, dW3 [N,K] from dZ and the kept G, U
  *   and Y.  dA may be NULL; dW1, dW2, dW3 may be NULL together (Y is then not
  *   read and may be NULL too).
@@ -512,10 +513,13 @@ swiglu_status swiglu_mlp_train_backward(
  *   for a valid shape with M > 0.
  * swiglu_fused_packed_lora: Y [M,N] from A [M,K], the packed weights Wp of
  *   swiglu_pack_weights and Lp, on the schedule that swiglu_fused_packed's AUTO
- *   picks.
+ *   picks, or, above 64 rows, with K split where that leaves over half the CUs
+ *   idle.  Where K is split, rows without an adapter have their sums in another
+ *   order than swiglu_fused_packed adds them, and can differ from it in the last
+ *   bit.
  * swiglu_gemm_packed_lora: C [M,N] = A W + adapters, W [K,N] in the single-weight
  *   pack of swiglu_gemm_pack_weight, on the schedule of swiglu_gemm_packed with
- *   a workspace, or with K split further where that leaves CUs idle.
+ *   a workspace, or with K split further where that leaves CUs idle (as above).
  * All: K and N multiples of 8, adapters >= 1, 1 <= rank <= 256 (above:
  * ERR_UNSUPPORTED_SHAPE), adapters * (K + N) at most 2^31; ids int32 and scales
  * fp32 (device, 4-byte aligned; read when the call's kernels run), other

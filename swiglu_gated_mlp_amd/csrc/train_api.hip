@@ -107,12 +107,23 @@ Tiles split_tiles(Tiles t, int64_t kb, int whole, int splits) {
     return t;
 }
 
-// Microseconds of an item of `kb` contraction blocks, to choose by: measured on
-// this chip for a 64-deep stage and around it (first loads, epilogue).  256 x 256:
-// 15.0 / 18.2 / 25.8 / 38.1 / 64.1 us for a launch of 256 items of 1 / 3 / 8 / 16 /
-// 32 stages.
-double item_us(int bm, int64_t kb) { return bm == 256 ? 10.0 + 1.55 * kb : (bm == 128 ? 7.0 + 0.6 * kb : 6.0 + 0.5 * kb); }
-// parts' sums: a launch, and 4 bytes a sum written and read
+// Microseconds of an item of `kb` contraction blocks, to choose by: so many around the
+// 64-deep stages (first loads, epilogue) and so many a stage.  Measured on this chip, a
+// launch of 256 items of 1 / 3 / 8 / 16 / 32 / 76 stages (dA, even numbers alone: 2 / 8 /
+// 16 / 32 / 76):
+//   256 x 256  dW       15.8 / 18.7 / 26.0 / 38.9 / 64.0 / 133 us   dA  16.2 / 25.6 / 38.6 / 61.0 / 127
+//              forward  20.2 / 26.3 / 34.9 / 41.2 / 71.6 / 137 (three outputs a tile)
+//   128 x 128  dW        6.4 /  8.1 / 11.4 / 16.5 / 26.8 /  57      dA   7.7 / 11.7 / 16.0 / 25.8 /  52
+//              forward   7.5 /  8.7 / 12.0 / 17.6 / 26.9 /  52
+//    64 x 128  forward   5.8 /  6.7 /  9.9 / 16.2 / 26.2 /  67      dA   5.4 /  8.5 / 14.1 / 23.3 /  58
+// The last of these tiles is up to a fifth slower than counted here at 16 and 32 stages, and
+// a third to a half at 76, where 256 such items read 320 MB of weights (4.8 to 5.5 TB/s).
+double item_us(int bm, int64_t kb) {
+    return bm == 256 ? 10.0 + 1.55 * kb : (bm == 128 ? 7.0 + 0.6 * kb : 6.0 + 0.5 * kb);
+}
+// parts' sums: a launch, and 4 bytes a sum written and read at 5 TB/s.  Measured: 8 MB of
+// parts 4.8 us; 67 MB 14.3 us and 3.6 us more in the items that write them, so that large
+// parts cost about half of what is counted here.
 constexpr double kReduceUs = 6.0, kPartUs = 2.0 / 5.0e6;
 
 // When the last of a launch's items ends, each handed to the CU that falls free

@@ -21,11 +21,13 @@
 //   dW3              N          K               token      KS   KS
 //
 // D = [dG | dU] ([M][2N]) is the one intermediate in memory.  It is rounded to
-// bf16 because the matrix cores take bf16: each element is then off by at most
-// 2^-8 of itself, independently, and the sums over N or M terms that consume it
-// are formed in fp32, so dA and the weight gradients move by less than their own
-// rounding to bf16 does.  dY (block) and the recomputed G and U stay in fp32
-// from their sums to dG and dU.
+// bf16 because the matrix cores take bf16 (D as two of them would double the
+// gradients' products): each element is then off by at most 2^-8 of itself,
+// independently, and the sums over N or M terms that consume it are formed in
+// fp32.  That moves dA and the weight gradients about as far as their own rounding
+// to bf16 does: in the root mean square they are 0.0023 off the fp64 values,
+// relatively, where the rounding of the outputs alone leaves 0.0017.  dY (block)
+// and the recomputed G and U stay in fp32 from their sums to dG and dU.
 #pragma once
 
 #include "device_common.hpp"

@@ -87,7 +87,7 @@ def swiglu_train_backward(dY: torch.Tensor, A: torch.Tensor, W1: torch.Tensor, W
                           stream=None):
     """Gradients of Y = SiLU(A @ W1) * (A @ W2): returns (dA, dW1, dW2), None for
     those not requested.  G and U are those of swiglu_train_forward, or None:
-    they are then computed again from A, W1, W2 without leaving the kernel."""
+    they are then computed again from A, W1, W2 and not kept."""
     M, K, N = _weights(A, W1, W2)
     for t, name in ((dY, "dY"), (G, "G"), (U, "U")):
         _shape(t, (M, N), name)
@@ -185,7 +185,8 @@ class _SwigluMlp(torch.autograd.Function):
 def swiglu(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, recompute: bool = False) -> torch.Tensor:
     """Differentiable Y = SiLU(A @ W1) * (A @ W2), A [..., K].  Keeps Gate and Up
     (4 M N bytes) for the backward pass, or (recompute) computes them again in
-    it for 4 M K N more operations."""
+    it for 4 M K N more operations.  Without recompute they are written in every
+    call, also where no gradient is wanted (swiglu_fused writes Y alone)."""
     return _Swiglu.apply(A, W1, W2, recompute)
 
 
