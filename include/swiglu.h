@@ -449,7 +449,8 @@ swiglu_status swiglu_mlp_unfused(const swiglu_bf16 *A, const swiglu_bf16 *W1g,
  * swiglu_train_workspace_bytes: workspace of the backward calls at (M,K,N):
  *   [dG | dU] (4 M N bytes) and, for small products, fp32 sums of splits of the
  *   contraction; enough for the forward call too.  0 for an invalid shape and
- *   for M == 0.
+ *   for M == 0.  The sums do not grow with M: a workspace for calls of several M
+ *   is the largest of theirs.
  * swiglu_train_forward_workspace_bytes: workspace of the forward call alone
  *   (sums of splits; 0 where it needs none).
  * swiglu_train_forward: Y = SiLU(G) U, and G and U rounded to bf16 (each [M,N]),
@@ -510,7 +511,9 @@ swiglu_status swiglu_mlp_train_backward(
  *   they are loaded (K and N are those of the projection's weight).
  * swiglu_lora_workspace_bytes / swiglu_gemm_lora_workspace_bytes: workspace of
  *   a call (the factors, and fp32 sums where the schedule splits K); never 0
- *   for a valid shape with M > 0.
+ *   for a valid shape with M > 0.  It does not grow with M alone (64 to 256
+ *   rows can need more than 4096): a workspace for calls of several M is the
+ *   largest of theirs.
  * swiglu_fused_packed_lora: Y [M,N] from A [M,K], the packed weights Wp of
  *   swiglu_pack_weights and Lp, on the schedule that swiglu_fused_packed's AUTO
  *   picks, or, above 64 rows, with K split where that leaves over half the CUs

@@ -387,14 +387,17 @@ def _scratch(workspace, need: int, device: torch.device, s: int):
     may fall between them.  On return the buffer goes back to the allocator, which hands
     it out again only to work that s orders after the call (a captured one: in the
     graph's pool)."""
-    if workspace is not None and workspace.device.type != "cuda":
-        raise ValueError("workspace must be a GPU tensor")
-    if isinstance(workspace, torch.Tensor):
-        return workspace, workspace.numel() * workspace.element_size()
-    if need == 0:
+    if workspace is None:
+        ws = _empty(need, torch.uint8, device, s) if need else None
+    elif isinstance(workspace, torch.Tensor):
+        ws = workspace
+    else:
+        ws = workspace.get(need, s)
+    if ws is None:
         return None, 0
-    ws = _empty(need, torch.uint8, device, s) if workspace is None else workspace.get(need, s)
-    return ws, ws.numel()
+    if workspace is not None and ws.device.type != "cuda":
+        raise ValueError("workspace must be a GPU tensor")
+    return ws, ws.numel() * ws.element_size()
 
 
 def _on(s: int, device) -> torch.cuda.StreamContext:

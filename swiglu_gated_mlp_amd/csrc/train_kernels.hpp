@@ -368,9 +368,9 @@ __device__ __forceinline__ void add_sums(const float* s, f32x16& a) {
 //   LDS tiles: k-contiguous [rows][64], chunks swizzled by row (lds_off);
 // k-strided [64][columns], chunks swizzled by k (rm_off; DUAL: one [64][BN / 2]
 // tile for each half).
-//   Measured: at 7B width dA and both weight gradients of 8192 tokens 3.54 ms (1.26
+//   Measured: at 7B width dA and both weight gradients of 8192 tokens 3.51 ms (1.27
 // PFLOP/s, matrix cores busy 69 % of the cycles at 1.74 GHz: the chip's power sets
-// the clock), the forward product of 4096 tokens with its three outputs 1.00 ms (1.11
+// the clock), the forward product of 4096 tokens with its three outputs 0.99 ms (1.13
 // PFLOP/s), of 64 tokens at 0.5B width 10.9 us (a chain of 14 stages' loads).
 // ---------------------------------------------------------------------------
 template <int BM_, int BN_, int AOP_, int BOP_, bool DUAL_, int EPI_>
