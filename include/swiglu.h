@@ -559,6 +559,78 @@ swiglu_status swiglu_gemm_packed_lora(const swiglu_bf16 *A, const swiglu_bf16 *W
                                       void *workspace, size_t workspace_bytes,
                                       void *stream);
 
+/* ------------------------------------------------------------------------
+ * Int8 operands with a scale for each token and channel.  Symmetric: a row of
+ * activations (token) is sa[m] times whole numbers in -127 .. 127, a column of a
+ * weight (channel) sw[n] times such, and the products are sums of whole numbers
+ * (int32, exact in any order), scaled once in fp32:
+ *     C[m,n] = bf16_RNE((fp32(sum_k a8 w8) * sw[n]) * sa[m]),
+ *     Y[m,n] = bf16_RNE(SiLU(G) * U),  G, U alike from W1 and W2,
+ * on v_mfma_i32_32x32x32_i8 and v_mfma_i32_16x16x64_i8.
+ *
+ * swiglu_quantize_rows_int8: A [M,K] bf16 -> codes Q [M,K] and scales [M] with
+ *   t = max(max_k |A[m,k]|, 2^-96): scales = t / 127, Q = round(A * (127 / t)),
+ *   ties to even, every step in fp32.  A row that holds an infinity or NaN has
+ *   the scale NaN and codes 0: the outputs of its token are NaN, of no other.
+ * swiglu_quantize_columns_int8: W [K,N] bf16 -> Q [K,N] and scales [N], the same
+ *   along k (once, when weights are loaded; a quantized checkpoint has them).
+ * swiglu_packed_bytes_int8 / swiglu_gemm_packed_bytes_int8: bytes of the packed
+ *   weights (0 for a shape that is not supported).
+ * swiglu_pack_weights_int8: W1, W2 [K,N] -> Wp; swiglu_gemm_pack_weight_int8: one
+ *   weight W [K,N] -> Wg.  The layouts are those of swiglu_pack_weights and
+ *   swiglu_gemm_pack_weight with 16 int8 in the place of 8 bf16: a block is 128
+ *   deep and e = 0 .. 15, k = kb*128 + h*64 + (l/16)*16 + e.
+ * swiglu_fused_packed_int8: Y [M,N] from A [M,K] int8, sa [M], Wp, s1 and s2 [N].
+ * swiglu_gemm_packed_int8: C [M,N] from A, sa, Wg and sw [N].
+ * swiglu_mlp_packed_int8: the whole block from A [M,K] in bf16: its rows are
+ *   quantized, Y [M,N] is the fused product (bf16), Y's rows are quantized, and
+ *   Z [M,K] is their product with W3g (swiglu_gemm_pack_weight_int8 of [N,K]) and
+ *   s3 [K].
+ * swiglu_workspace_bytes_int8, swiglu_gemm_workspace_bytes_int8,
+ * swiglu_mlp_workspace_bytes_int8: workspace of those calls (int32 sums of splits
+ *   of K; the block's also codes and scales, so it is never 0 for M > 0).  It does
+ *   not grow with M alone: a workspace for calls of several M is the largest of
+ *   theirs.  ERR_WORKSPACE if it is missing or smaller.
+ * All: K a multiple of 16 and at most 131056 (no sum reaches 2^31), N of 8 (the
+ * block: N as K); the quantizing calls take multiples of 8.  Scales are fp32,
+ * 4-byte aligned, other pointers 16-byte aligned.  Outputs and the workspace
+ * overlap nothing; calls that may run concurrently must not share a workspace.
+ * M == 0 returns SWIGLU_OK without a launch.
+ * ---------------------------------------------------------------------- */
+swiglu_status swiglu_quantize_rows_int8(const swiglu_bf16 *A, int8_t *Q,
+                                        float *scales, int64_t M, int64_t K,
+                                        void *stream);
+swiglu_status swiglu_quantize_columns_int8(const swiglu_bf16 *W, int8_t *Q,
+                                           float *scales, int64_t K, int64_t N,
+                                           void *stream);
+size_t swiglu_packed_bytes_int8(int64_t K, int64_t N);
+size_t swiglu_gemm_packed_bytes_int8(int64_t K, int64_t N);
+swiglu_status swiglu_pack_weights_int8(const int8_t *W1, const int8_t *W2,
+                                       int8_t *Wp, int64_t K, int64_t N,
+                                       void *stream);
+swiglu_status swiglu_gemm_pack_weight_int8(const int8_t *W, int8_t *Wg,
+                                           int64_t K, int64_t N, void *stream);
+size_t swiglu_workspace_bytes_int8(int64_t M, int64_t K, int64_t N);
+size_t swiglu_gemm_workspace_bytes_int8(int64_t M, int64_t K, int64_t N);
+size_t swiglu_mlp_workspace_bytes_int8(int64_t M, int64_t K, int64_t N);
+swiglu_status swiglu_fused_packed_int8(const int8_t *A, const float *sa,
+                                       const int8_t *Wp, const float *s1,
+                                       const float *s2, swiglu_bf16 *Y,
+                                       int64_t M, int64_t K, int64_t N,
+                                       void *workspace, size_t workspace_bytes,
+                                       void *stream);
+swiglu_status swiglu_gemm_packed_int8(const int8_t *A, const float *sa,
+                                      const int8_t *Wg, const float *sw,
+                                      swiglu_bf16 *C, int64_t M, int64_t K,
+                                      int64_t N, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+swiglu_status swiglu_mlp_packed_int8(const swiglu_bf16 *A, const int8_t *Wp,
+                                     const float *s1, const float *s2,
+                                     const int8_t *W3g, const float *s3,
+                                     swiglu_bf16 *Y, swiglu_bf16 *Z, int64_t M,
+                                     int64_t K, int64_t N, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

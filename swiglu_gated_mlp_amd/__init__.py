@@ -80,6 +80,18 @@ SIGNATURES = {
     "swiglu_gemm_lora_workspace_bytes": ([_I64] * 4, ctypes.c_size_t),
     "swiglu_fused_packed_lora": ([_P] * 6 + [_I64] * 5 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
     "swiglu_gemm_packed_lora": ([_P] * 6 + [_I64] * 5 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_quantize_rows_int8": ([_P] * 3 + [_I64] * 2 + [_P], ctypes.c_int),
+    "swiglu_quantize_columns_int8": ([_P] * 3 + [_I64] * 2 + [_P], ctypes.c_int),
+    "swiglu_packed_bytes_int8": ([_I64] * 2, ctypes.c_size_t),
+    "swiglu_gemm_packed_bytes_int8": ([_I64] * 2, ctypes.c_size_t),
+    "swiglu_pack_weights_int8": ([_P] * 3 + [_I64] * 2 + [_P], ctypes.c_int),
+    "swiglu_gemm_pack_weight_int8": ([_P] * 2 + [_I64] * 2 + [_P], ctypes.c_int),
+    "swiglu_workspace_bytes_int8": ([_I64] * 3, ctypes.c_size_t),
+    "swiglu_gemm_workspace_bytes_int8": ([_I64] * 3, ctypes.c_size_t),
+    "swiglu_mlp_workspace_bytes_int8": ([_I64] * 3, ctypes.c_size_t),
+    "swiglu_fused_packed_int8": ([_P] * 6 + [_I64] * 3 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_gemm_packed_int8": ([_P] * 5 + [_I64] * 3 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_mlp_packed_int8": ([_P] * 8 + [_I64] * 3 + [_P, ctypes.c_size_t, _P], ctypes.c_int),
     # include/swiglu_probe.h (diagnostic ceilings)
     "swiglu_probe_mfma": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_read": ([_P, ctypes.c_size_t, _P, ctypes.c_int, _P], ctypes.c_int),
@@ -722,3 +734,9 @@ from .train import (swiglu, swiglu_mlp, swiglu_mlp_train_backward, swiglu_train_
 from .lora import (swiglu_fused_packed_lora, swiglu_gemm_lora_pack, swiglu_gemm_lora_packed_bytes,  # noqa: E402,F401
                    swiglu_gemm_lora_workspace_bytes, swiglu_gemm_packed_lora, swiglu_lora_pack,
                    swiglu_lora_packed_bytes, swiglu_lora_workspace_bytes)
+
+# int8 operands with a scale for each token and channel
+from .int8 import (swiglu_fused_packed_int8, swiglu_gemm_pack_weight_int8, swiglu_gemm_packed_bytes_int8,  # noqa: E402,F401
+                   swiglu_gemm_packed_int8, swiglu_gemm_workspace_bytes_int8, swiglu_mlp_packed_int8,
+                   swiglu_mlp_workspace_bytes_int8, swiglu_pack_weights_int8, swiglu_packed_bytes_int8,
+                   swiglu_quantize_columns_int8, swiglu_quantize_rows_int8, swiglu_workspace_bytes_int8)

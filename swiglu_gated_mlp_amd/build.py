@@ -2,10 +2,11 @@
 
     python -m swiglu_gated_mlp_amd.build
 
-Two translation units, compiled side by side, export the C ABI of
+Three translation units, compiled side by side, export the C ABI of
 include/swiglu.h: csrc/swiglu_api.hip (the products, kernels in
-csrc/fused_kernels.hpp) and csrc/train_api.hip (training, kernels in
-csrc/train_kernels.hpp).
+csrc/fused_kernels.hpp), csrc/train_api.hip (training, kernels in
+csrc/train_kernels.hpp) and csrc/int8_api.hip (the int8 products, kernels in
+csrc/int8_kernels.hpp and csrc/fused_kernels.hpp).
 """
 from __future__ import annotations
 
@@ -22,7 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libswiglu.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = [os.path.join(CSRC, f) for f in ("swiglu_api.hip", "train_api.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("swiglu_api.hip", "train_api.hip", "int8_api.hip")]
 ARCH = os.environ.get("SWIGLU_OFFLOAD_ARCH", "gfx950")
 
 

@@ -98,7 +98,41 @@ struct FusedArgs {
                           // (streaming kernel, one row tile): work item w takes
                           // panels [w*panels/total, (w+1)*panels/total), one per wave
     float sg, su;         // FP8 operands: scale products applied to the Gate and Up sums
+    const float* sa;      // int8 operands: a scale for each row of A,
+    const float* s1;      //   for each column of W1 (or the one weight)
+    const float* s2;      //   and of W2
 };
+
+// int8 operands take the bf16 kernels' path byte for byte: K then counts pairs of
+// int8, a 16-byte fragment piece holds 16 of them, and the sums are int32.
+template <bool I8>
+using Acc16 = std::conditional_t<I8, i32x16, f32x16>;
+template <bool I8>
+using Acc4 = std::conditional_t<I8, i32x4, f32x4>;
+
+template <bool I8>
+__device__ __forceinline__ Acc16<I8> mma32(bf16x8 w, bf16x8 a, Acc16<I8> c) {
+    if constexpr (I8)
+        return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, a), c, 0,
+                                                     0, 0);
+    else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, a, c, 0, 0, 0);
+}
+template <bool I8>
+__device__ __forceinline__ Acc4<I8> mma16(u32x4 w, bf16x8 a, Acc4<I8> c) {
+    if constexpr (I8)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, a), c, 0,
+                                                     0, 0);
+    else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), a, c, 0, 0, 0);
+}
+
+// Four columns' scales from column n on (a multiple of 4; past the last column any).
+__device__ __forceinline__ f32x4 scales4(const float* s, int n, int N) {
+    typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+    return *reinterpret_cast<const f32x4u*>(s + min(n, N - 4));
+}
+// An int32 sum's value: the column's scale first, as weights are small, so that
+// only a result that overflows overflows.
+__device__ __forceinline__ float scaled(int sum, float col, float row) { return ((float)sum * col) * row; }
 
 // ---------------------------------------------------------------------------
 // Split-K partials.  Layout [split][M][2N] fp32: the Gate sum of (m, n) at
@@ -106,8 +140,8 @@ struct FusedArgs {
 // columns of one token per 32x32 accumulator block, so it writes 16 bytes of
 // Gate and 16 bytes of Up per block.  Rows >= M and columns >= N are skipped.
 // ---------------------------------------------------------------------------
-template <int TM, int TN>
-__device__ __forceinline__ void store_partials(const f32x16 (&acc)[2][TM][TN], float* part, int split,
+template <int TM, int TN, class Acc>
+__device__ __forceinline__ void store_partials(const Acc (&acc)[2][TM][TN], float* part, int split,
                                                int M, int N, int row0, int col0, int lane) {
     float* base = part + (size_t)split * M * (2 * (size_t)N);
 #pragma unroll
@@ -124,8 +158,10 @@ __device__ __forceinline__ void store_partials(const f32x16 (&acc)[2][TM][TN], f
                 f32x4 g, u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    g[e] = acc[0][i][j][4 * q + e];
-                    u[e] = acc[1][i][j][4 * q + e];
+                    // int32 sums keep their bits
+                    const auto gs = acc[0][i][j][4 * q + e], us = acc[1][i][j][4 * q + e];
+                    g[e] = __builtin_bit_cast(float, gs);
+                    u[e] = __builtin_bit_cast(float, us);
                 }
                 *reinterpret_cast<f32x4*>(prow + n) = g;
                 *reinterpret_cast<f32x4*>(prow + N + n) = u;
@@ -136,7 +172,7 @@ __device__ __forceinline__ void store_partials(const f32x16 (&acc)[2][TM][TN], f
 // Y[m, n..n+3] = bf16(SiLU(sum_s G_s) * sum_s U_s), splits added in order
 // 0..S-1 (so the result does not depend on which workgroup finished first).
 // One thread per 4 outputs, grid-stride.
-__global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ part,
+[[maybe_unused]] static __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restrict__ part,
                                                             uint16_t* __restrict__ Y, int M, int N,
                                                             int S) {
     const long long groups = (long long)M * (N / 4);
@@ -163,7 +199,7 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(const float* __restr
 // the NT tiled columns of the pack (the "Gate" sum of tiled column n is output
 // column (n / 128) * 256 + n % 128, the "Up" sum that column + 128), added in
 // split order 0..S-1 and stored as bf16; output columns >= N are skipped.
-__global__ __launch_bounds__(256) void splitk_gemm_reduce_kernel(const float* __restrict__ part,
+[[maybe_unused]] static __global__ __launch_bounds__(256) void splitk_gemm_reduce_kernel(const float* __restrict__ part,
                                                                  uint16_t* __restrict__ C, int M, int N, int NT,
                                                                  int S) {
     const long long groups = (long long)M * (NT / 4);
@@ -825,7 +861,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fused_prefill_kernel(FusedArgs p
 //   fragment as first operand) as fused_prefill_kernel, so the two agree
 //   bitwise.
 // ---------------------------------------------------------------------------
-__device__ __attribute__((aligned(16))) uint16_t g_zero_chunk[8];
+static __device__ __attribute__((aligned(16))) uint16_t g_zero_chunk[8];
 
 // LDS elements of the streaming kernel: three ring slots of BM x 64
 // activations, then the BM x 128 Y tile of the epilogue (kept apart from the
@@ -862,15 +898,18 @@ constexpr int stream_smem_elems() {
 // half, one accumulator set -- so the units are twice the fused product's
 // panels and the CUs share them as evenly (p.panels counts half-panels; the
 // single Y-tile pass maps each wave's 32 columns to its half).
+// I8: int8 activations and packed weights (see Acc16; K, KB and the plan count
+// pairs of int8), the sums scaled by row and column in the epilogue.
 // LORA: each row's low-rank adapter (la) is added to the sums: 1 after the
 // K loop (LoraTile), or where a tile's rows have too many adapters for that,
 // in the epilogue (lora_block); 2 in the epilogue, from la->delta.
 template <int BM, bool SPLIT, bool RAGGED, bool PANELS = false, bool IL = false, bool F8 = false,
-          bool SEQ = false, bool GEMM = false, int LORA = 0>
+          bool SEQ = false, bool GEMM = false, int LORA = 0, bool I8 = false>
 __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_t* smem, int first, int stride,
                                                      int total, const LoraArgs* la = nullptr) {
     static_assert(!(LORA != 0 && (SPLIT || IL || F8 || SEQ)), "adapters: bf16 per-tile or single-weight pack, whole K");
-    static_assert(!(GEMM && (IL || F8 || SEQ)), "plain GEMM: bf16 single-weight pack");
+    static_assert(!(GEMM && (IL || F8 || SEQ)), "plain GEMM: single-weight pack");
+    static_assert(!(I8 && (IL || F8 || SEQ || LORA != 0)), "int8 operands: per-tile or single-weight pack");
     static_assert(!(IL && SPLIT), "the interleaved layout has no split-K schedule");
     static_assert(!(F8 && (IL || SPLIT)), "FP8 operands: per-tile layout, data-parallel only");
     static_assert(!(SEQ && (SPLIT || PANELS || IL || F8)), "sequential order: bf16 per-tile tiles only");
@@ -1020,14 +1059,14 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
         }
     };
 
-    f32x16 acc[2][TM][1];
+    Acc16<I8> acc[2][TM][1];
     auto zero_acc = [&]() {
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) acc[g][i][0][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) acc[g][i][0][r] = 0;
     };
     zero_acc();
     bf16x8 fa[2][TM];
@@ -1152,10 +1191,8 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
         }
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            acc[0][i][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[WS][0][kk], fa[cur][i], acc[0][i][0], 0, 0, 0);
-            if constexpr (WT == 2)
-                acc[1][i][0] =
-                    __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[WS][WT - 1][kk], fa[cur][i], acc[1][i][0], 0, 0, 0);
+            acc[0][i][0] = mma32<I8>(wf[WS][0][kk], fa[cur][i], acc[0][i][0]);
+            if constexpr (WT == 2) acc[1][i][0] = mma32<I8>(wf[WS][WT - 1][kk], fa[cur][i], acc[1][i][0]);
             if constexpr (RD) {
 #pragma unroll
                 for (int q = i * RPI; q < (i + 1) * RPI; ++q)
@@ -1318,6 +1355,27 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
                        GEMM ? ((tc >> 7) * PACK_ROWS + (tc & (PACK_BN - 1)) + PACK_BN) / 32 : tc / 32);
         }
 
+        // I8: the columns' scales of the wave's sums, and the rows', on their way
+        // before the next item's loads (a wait for them leaves those in flight)
+        f32x4 cs[2][4];
+        float rs[TM];
+        if constexpr (I8) {
+            int sl = lane;
+            asm volatile("" : "+v"(sl));
+#pragma unroll
+            for (int g = 0; g < WT; ++g) {
+                const int u = cur.n0 / 32 + wave;
+                const int tc = GH ? (u >> 1) * 32 : u * 32;   // (tiled) column of the wave's first
+                const int n = GEMM ? (tc >> 7) * PACK_ROWS + PACK_BN * (GH ? (u & 1) : g) + (tc & (PACK_BN - 1)) : tc;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    cs[g][q] = scales4(GEMM || g == 0 ? p.s1 : p.s2, n + 8 * q + 4 * (sl >> 5), N);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) rs[i] = p.sa[min(cur.m0 + i * 32 + (sl & 31), M - 1)];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+
         // the next item's first two stages stream in during this epilogue
         // (past the last item they read the zero chunk): activations and
         // stage 0's weights now, stage 1's weights once the accumulators are
@@ -1384,9 +1442,15 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
                 if constexpr (LORA == 2) acc[gh][i][0] += ld[i & 1][0];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (I8) v[e] = scaled(acc[gh][i][0][4 * q + e], cs[gh][q][e], rs[i]);
+                        else v[e] = acc[gh][i][0][4 * q + e];
+                    }
                     u32x2 out;
-                    out[0] = pack2(acc[gh][i][0][4 * q], acc[gh][i][0][4 * q + 1]);
-                    out[1] = pack2(acc[gh][i][0][4 * q + 2], acc[gh][i][0][4 * q + 3]);
+                    out[0] = pack2(v[0], v[1]);
+                    out[1] = pack2(v[2], v[3]);
                     const int chunk = wave * 4 + q;
                     *reinterpret_cast<u32x2*>(sY + r * PACK_BN + 8 * (chunk ^ (r & 15)) +
                                               4 * ((el >> 5) ^ ((r >> 4) & 1))) = out;
@@ -1443,7 +1507,14 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float gv = acc[0][i][0][4 * q + e], uv = acc[1][i][0][4 * q + e];
+                        float gv, uv;
+                        if constexpr (I8) {
+                            gv = scaled(acc[0][i][0][4 * q + e], cs[0][q][e], rs[i]);
+                            uv = scaled(acc[1][i][0][4 * q + e], cs[1][q][e], rs[i]);
+                        } else {
+                            gv = acc[0][i][0][4 * q + e];
+                            uv = acc[1][i][0][4 * q + e];
+                        }
                         if constexpr (LORA == 2) {
                             gv += ld[i & 1][0][4 * q + e];
                             uv += ld[i & 1][1][4 * q + e];
@@ -1541,28 +1612,29 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
 }
 
 template <int BM, bool SPLIT, bool RAGGED, bool PANELS = false, bool IL = false, bool F8 = false,
-          bool SEQ = false, bool GEMM = false>
+          bool SEQ = false, bool GEMM = false, bool I8 = false>
 __global__ __launch_bounds__(256) void stream_prefill_kernel(FusedArgs p, int total) {
     static_assert(!PANELS || !SPLIT, "panel schedule: one row tile, data-parallel");
     __shared__ __attribute__((aligned(16))) uint16_t smem[stream_smem_elems<BM>()];
-    stream_prefill_tiles<BM, SPLIT, RAGGED, PANELS, IL, F8, SEQ, GEMM>(p, smem, blockIdx.x, gridDim.x, total);
+    stream_prefill_tiles<BM, SPLIT, RAGGED, PANELS, IL, F8, SEQ, GEMM, 0, I8>(p, smem, blockIdx.x, gridDim.x, total);
 }
 
 // The 256-row tiles and the 128-row tail column tiles in one launch: blocks
 // 0 .. n_pers-1 work through the n_big 256-row tiles of `big` (block b takes
 // tiles b, b + n_pers, ...), the remaining blocks take one 128-row tile of
 // `tail` each and start on CUs as the 256-row work drains.
-template <bool RAGGED, bool IL = false, bool F8 = false, bool SEQ = false, bool GEMM = false>
+template <bool RAGGED, bool IL = false, bool F8 = false, bool SEQ = false, bool GEMM = false, bool I8 = false>
 __global__ __launch_bounds__(256) void stream_prefill_mixed_kernel(FusedArgs big, FusedArgs tail, int n_pers,
                                                                    int n_big) {
     __shared__ __attribute__((aligned(16))) uint16_t smem[stream_smem_elems<256>()];
     static_assert(stream_smem_elems<256>() >= stream_smem_elems<128>(), "one LDS block serves both tiles");
     const int b = blockIdx.x;
     if (b < n_pers) {
-        stream_prefill_tiles<256, false, RAGGED, false, IL, F8, SEQ, GEMM>(big, smem, b, n_pers, n_big);
+        stream_prefill_tiles<256, false, RAGGED, false, IL, F8, SEQ, GEMM, 0, I8>(big, smem, b, n_pers, n_big);
     } else {
         const int n_tail = gridDim.x - n_pers;
-        stream_prefill_tiles<128, false, RAGGED, false, IL, F8, SEQ, GEMM>(tail, smem, b - n_pers, n_tail, n_tail);
+        stream_prefill_tiles<128, false, RAGGED, false, IL, F8, SEQ, GEMM, 0, I8>(tail, smem, b - n_pers, n_tail,
+                                                                                  n_tail);
     }
 }
 
@@ -1588,6 +1660,9 @@ struct DecodeArgs {
     uint16_t* Y;          // [M,N]
     int M, K, N;
     int KB;               // ceil(K / 64)
+    const float* sa;      // int8 operands: the scales, as in FusedArgs
+    const float* s1;
+    const float* s2;
 };
 
 // GEMM: a plain product C = bf16(A x W) on a single-weight pack (packed tile
@@ -1604,15 +1679,18 @@ struct DecodeArgs {
 // instruction; the 16-byte chunks of row r XOR-ed with r & 7) and reads the
 // MFMA fragments from there, instead of loading each fragment (16 rows x 64
 // bytes, half lines) from global memory.
+// I8: int8 operands (see Acc16; K and KB count pairs of int8).
 // Lora: LoraArgs, or nothing.  With it, each row's low-rank adapter is added to
 // the summed Gate and Up (or plain) values before the epilogue.
-template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false, class... Lora>
+template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false, bool I8 = false,
+          class... Lora>
 __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora) {
     static_assert(GEMM || !HALF, "HALF splits the single-weight product only");
     constexpr int WAVES = 4;
     constexpr int NH = HALF ? 1 : 2;    // weight halves per workgroup
     constexpr int AROWS = 16 * MT;      // activation rows per K block
-    __shared__ f32x4 red[WAVES][MT][CG][NH][64];
+    static_assert(!I8 || sizeof...(Lora) == 0, "adapters: bf16 operands");
+    __shared__ Acc4<I8> red[WAVES][MT][CG][NH][64];
     __shared__ __attribute__((aligned(16))) uint16_t sA[LDSA ? WAVES * UNROLL * AROWS * PACK_BK : 8];
 
     const int tid = threadIdx.x;
@@ -1648,13 +1726,13 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora)
     }
     uint16_t* const sAw = sA + (LDSA ? wave * UNROLL * AROWS * PACK_BK : 0);
 
-    f32x4 accg[MT][CG], accu[MT][CG];
+    Acc4<I8> accg[MT][CG], accu[MT][CG];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int c = 0; c < CG; ++c) {
-            accg[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-            accu[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+            accg[t][c] = Acc4<I8>{0, 0, 0, 0};
+            accu[t][c] = Acc4<I8>{0, 0, 0, 0};
             // opaque zeros: with one shared zero register as every sum's
             // start, the allocator gave the loop-carried sums different
             // registers at the loop's entry and back edge and copied them at
@@ -1732,11 +1810,8 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora)
                         const bf16x8 a8 = __builtin_bit_cast(bf16x8, av[u][h][t]);
 #pragma unroll
                         for (int c = 0; c < CG; ++c) {
-                            accg[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                __builtin_bit_cast(bf16x8, wg[u][h][c]), a8, accg[t][c], 0, 0, 0);
-                            if constexpr (!HALF)
-                                accu[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                                    __builtin_bit_cast(bf16x8, wu[u][h][c]), a8, accu[t][c], 0, 0, 0);
+                            accg[t][c] = mma16<I8>(wg[u][h][c], a8, accg[t][c]);
+                            if constexpr (!HALF) accu[t][c] = mma16<I8>(wu[u][h][c], a8, accu[t][c]);
                         }
                     }
             }
@@ -1754,14 +1829,29 @@ __global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora)
     // epilogue: wave w finishes (token tile, column group) pairs w, w+4, ...
     for (int tc = wave; tc < MT * CG; tc += WAVES) {
         const int t = tc / CG, c = tc % CG;
-        f32x4 g = red[0][t][c][0][lane], u = red[0][t][c][NH - 1][lane];
+        Acc4<I8> sg = red[0][t][c][0][lane], su = red[0][t][c][NH - 1][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) {
-            g += red[w][t][c][0][lane];
-            if constexpr (!HALF) u += red[w][t][c][NH - 1][lane];
+            sg += red[w][t][c][0][lane];
+            if constexpr (!HALF) su += red[w][t][c][NH - 1][lane];
         }
         const int m = t * 16 + r16;
         const int n = n0 + 16 * c + 4 * kq;
+        f32x4 g, u;
+        if constexpr (I8) {
+            const int col = GEMM ? (n / PACK_BN) * PACK_ROWS + n % PACK_BN + (HALF ? PACK_BN * half : 0) : n;
+            const f32x4 c1 = scales4(p.s1, col, N);
+            const f32x4 c2 = HALF ? c1 : GEMM ? scales4(p.s1, col + PACK_BN, N) : scales4(p.s2, col, N);
+            const float row = p.sa[min(m, M - 1)];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[e] = scaled(sg[e], c1[e], row);
+                u[e] = scaled(su[e], c2[e], row);
+            }
+        } else {
+            g = sg;
+            u = su;
+        }
         if constexpr (sizeof...(Lora) > 0) {
             const LoraArgs& la = (lora, ...);
             if (la.delta) {
@@ -2249,7 +2339,7 @@ __global__ __launch_bounds__(256) void unpack_kernel(const uint16_t* __restrict_
 // contiguous.  Padding is zero.  One thread per 16-byte piece (piece index =
 // byte offset / 16).
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void pack_fp8_kernel(const uint8_t* __restrict__ W1,
+[[maybe_unused]] static __global__ __launch_bounds__(256) void pack_fp8_kernel(const uint8_t* __restrict__ W1,
                                                        const uint8_t* __restrict__ W2,
                                                        uint8_t* __restrict__ Wp, int K, int N, int KB,
                                                        long long npieces) {
@@ -2277,7 +2367,7 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(const uint8_t* __restrict
 // Element-wise SwiGLU of the unfused pipeline: Y = bf16(SiLU(G) * U), fp32 math.
 // 8 elements (16 bytes) per thread per step, grid-stride; scalar tail.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void silu_mul_kernel(const uint16_t* __restrict__ G,
+[[maybe_unused]] static __global__ __launch_bounds__(256) void silu_mul_kernel(const uint16_t* __restrict__ G,
                                                        const uint16_t* __restrict__ U,
                                                        uint16_t* __restrict__ Y, long long count) {
     const long long nvec = count / 8;

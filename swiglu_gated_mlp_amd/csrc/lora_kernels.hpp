@@ -19,7 +19,7 @@ namespace swk {
 //   flags   [adapter] int32: 1 where the adapter's Lb holds an infinity or NaN
 // one thread per 16 bytes, padding zero; the flags, zero before, by a second launch.
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void lora_pack_kernel(const uint16_t* __restrict__ La1,
+[[maybe_unused]] static __global__ __launch_bounds__(256) void lora_pack_kernel(const uint16_t* __restrict__ La1,
                                                         const uint16_t* __restrict__ La2,
                                                         const uint16_t* __restrict__ Lb1,
                                                         const uint16_t* __restrict__ Lb2, uint16_t* __restrict__ out,
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(256) void lora_pack_kernel(const uint16_t* __restri
 
 // pieces: 16-byte pieces of an adapter's Lb; `share` workgroups an adapter, and all
 // that find one store the same 1.
-__global__ __launch_bounds__(256) void lora_flag_kernel(const uint16_t* __restrict__ B, int* __restrict__ flags,
+[[maybe_unused]] static __global__ __launch_bounds__(256) void lora_flag_kernel(const uint16_t* __restrict__ B, int* __restrict__ flags,
                                                         long long pieces, int share, int adapters) {
     for (int l = blockIdx.x / share; l < adapters; l += gridDim.x / share) {
         const u32x4* b = reinterpret_cast<const u32x4*>(B) + l * pieces;

@@ -17,6 +17,7 @@
 
 #include "fused_kernels.hpp"
 #include "host_common.hpp"
+#include "launch.hpp"
 #include "lora_kernels.hpp"
 #include "probe_kernels.hpp"
 
@@ -32,6 +33,7 @@ thread_local int g_last_hip_error = 0;
 }
 
 using namespace swh;
+using namespace swl;
 
 namespace {
 
@@ -44,22 +46,6 @@ bool log_enabled() {
     return on == 1;
 }
 
-// The streaming kernel keeps each activation address as a 32-bit byte offset
-// from the stage base (row * K * bytes).  Calls whose activation slice would
-// reach 2 GiB are split into row chunks of at most this many rows (a multiple
-// of 256), each with A and Y advanced to its first row.
-int64_t stream_rows_limit(int64_t K, int elem_bytes) {
-    const int64_t rows = (((int64_t)1 << 31) / (K * elem_bytes)) / 256 * 256;
-    return rows >= 256 ? rows : 256;
-}
-
-// Equal chunks (multiples of 256 rows) of at most `limit` rows covering M.
-int64_t balanced_chunk(int64_t M, int64_t limit) {
-    const int64_t n = (M + limit - 1) / limit;
-    const int64_t per = (M + n - 1) / n;
-    return std::min(limit, (per + 255) / 256 * 256);
-}
-
 // FP8 operands: K a multiple of 16 (16-byte activation rows), packed weights
 // in 32 KiB blocks per (128 columns, 128 k)
 swiglu_status check_shape_fp8(int64_t M, int64_t K, int64_t N) {
@@ -69,18 +55,6 @@ swiglu_status check_shape_fp8(int64_t M, int64_t K, int64_t N) {
 }
 
 int64_t packed_bytes_fp8(int64_t K, int64_t N) { return ceil_div(N, swk::PACK_BN) * ceil_div(K, 128) * 32768; }
-
-int64_t packed_elems(int64_t K, int64_t N) {
-    return ceil_div(N, swk::PACK_BN) * ceil_div(K, swk::PACK_BK) * swk::PACK_ROWS * swk::PACK_BK;
-}
-
-// Single-weight pack of W [K,N] for the plain GEMM: 256 columns per packed
-// tile (the dual kernels' Gate and Up halves), so ceil(N/256) tiles whose
-// 128-column "output" width n_tiled the dual schedules are planned on.
-int64_t gemm_packed_elems(int64_t K, int64_t N) {
-    return ceil_div(N, swk::PACK_ROWS) * ceil_div(K, swk::PACK_BK) * swk::PACK_ROWS * swk::PACK_BK;
-}
-int64_t gemm_tiled_cols(int64_t N) { return ceil_div(N, swk::PACK_ROWS) * swk::PACK_BN; }
 
 // Device address of `scratch` on the current device: looked up once per
 // device (with that device current) and kept; each device holds its own copy
@@ -102,274 +76,6 @@ hipError_t scratch_device_ptr(void** out) {
     }
     *out = ptrs[dev];
     return hipSuccess;
-}
-
-// ---------------------------------------------------------------------------
-// kernel configurations
-// ---------------------------------------------------------------------------
-// Output tile for a token count and schedule.  M <= 64 (forced data-parallel
-// or split-K; AUTO uses the decode kernel there): 32/64-row register-path
-// tiles.  Split-K above that: 128 x 64 tiles (two workgroups fit a CU, and a
-// narrow tile gives more tiles to split).  Data-parallel: 128 x 128 up to
-// 2048 tokens, then 256 x 128 (each wave 128 rows x 64 columns of Gate and Up).
-struct TileCfg {
-    int BM, BN;
-};
-
-// Split-K keeps small row tiles for small M; the data-parallel schedule is
-// the streaming kernel at every M (one row of 128-row tiles for M <= 128, on
-// the panel schedule when its column tiles leave CUs idle).
-// Data-parallel tiles: 256 x 128 (persistent, with the 128-row tail of the
-// mixed launch) above 512 rows, and from 385 rows when the last row tile is
-// at least three quarters full and the 256-row grid fills the CUs; else
-// 128 x 128 (measured against 128-row tiles everywhere up to 2048 rows:
-// 7B width M=512 152 -> 141 us, M=768 201 -> 178 us, M=2048 479 -> 422 us,
-// 72B width M=1024 865 -> 751 us; 0.5B width M=1024 29.4 -> 25.0 us).
-TileCfg packed_tile_for(int64_t M, int variant, int64_t N, int cus) {
-    if (variant == SWIGLU_VARIANT_SPLIT_K) {
-        if (M <= 32) return {32, 128};
-        if (M <= 64) return {64, 128};
-        return {128, 128};
-    }
-    if (M <= 512) {
-        if (M > 384 && (M % 256 == 0 || M % 256 >= 192) && ceil_div(M, 256) * ceil_div(N, 128) >= cus)
-            return {256, 128};
-        return {128, 128};
-    }
-    return {256, 128};
-}
-
-// workgroups per CU the split count aims for
-constexpr int kSplitWavesPerCu = 2;
-
-// Split-K above this many output tiles is pointless (the tiles alone fill
-// the device many times over).
-constexpr int kMaxSplitTiles = 16384;
-
-struct Plan {
-    TileCfg t;
-    int tiles_m, tiles_n, tiles;
-    int tail_ntiles;   // data-parallel 256-row tiles: last column tiles run as 128x128 tiles
-    int panels;        // data-parallel, one 128-row tile: 32-column panels spread over the CUs
-    int splits, kb_per_split, KB;
-    int variant;   // resolved: DATA_PARALLEL, SPLIT_K or DECODE
-    int decode_mt; // DECODE: 16-token tiles per workgroup
-    int cus;       // compute units the plan was made for
-};
-
-constexpr int kDecodeMaxM = 64;
-bool variant_known(int v) { return v >= SWIGLU_VARIANT_AUTO && v <= SWIGLU_VARIANT_SEQUENTIAL; }
-
-Plan make_plan(int64_t M, int64_t K, int64_t N, int variant, int cus) {
-    Plan p{};
-    if (cus <= 0) cus = 256;
-    p.cus = cus;
-    p.KB = (int)ceil_div(K, swk::BK);
-    int v = variant;
-    int auto_split_cap = 0;   // AUTO's split-K: most splits worth their partial-sum traffic
-    if (v == SWIGLU_VARIANT_AUTO) {
-        // Decode up to 32 rows; from 33 to 64 rows only while the weight
-        // panels cannot fill the CUs (a small product, where the decode
-        // kernel's single pass wins), otherwise the panel schedule streams
-        // the weights faster (measured: 7B M=64 57 us against 76 us).
-        const int64_t panels = 4 * ceil_div(N, swk::PACK_BN);
-        if (M <= 32 || (M <= kDecodeMaxM && panels < cus)) {
-            v = SWIGLU_VARIANT_DECODE;
-        } else if (M <= kDecodeMaxM) {
-            v = SWIGLU_VARIANT_DATA_PARALLEL;
-        } else {
-            // Split-K writes and re-reads S fp32 partial sums of Gate and Up,
-            // 16*S*M*N bytes against the 4*K*N bytes of weights: worth it only
-            // while the data-parallel tiles leave most CUs idle, and with at
-            // most K / (16 M) splits (extra traffic <= a quarter of the
-            // weights).  A data-parallel grid that fills half the CUs streams
-            // the weights faster than split-K does.
-            const TileCfg dp = packed_tile_for(M, SWIGLU_VARIANT_DATA_PARALLEL, N, cus);
-            const int64_t dp_tiles = ceil_div(M, dp.BM) * ceil_div(N, dp.BN);
-            auto_split_cap = (int)std::min<int64_t>(K / (16 * M), 1 << 20);
-            v = (2 * dp_tiles >= cus || p.KB < 4 || auto_split_cap < 2) ? SWIGLU_VARIANT_DATA_PARALLEL
-                                                                         : SWIGLU_VARIANT_SPLIT_K;
-        }
-    }
-    p.variant = v;
-    p.decode_mt = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-    // the sequential order runs on the data-parallel tiles (no panel schedule)
-    const bool dp_tiles = v == SWIGLU_VARIANT_DATA_PARALLEL || v == SWIGLU_VARIANT_SEQUENTIAL;
-    p.t = packed_tile_for(M, dp_tiles ? SWIGLU_VARIANT_DATA_PARALLEL : v, N, cus);
-    p.tiles_m = (int)ceil_div(M, p.t.BM);
-    p.tiles_n = (int)ceil_div(N, p.t.BN);
-    p.tiles = p.tiles_m * p.tiles_n;
-    // Wave quantisation of the 256 x 128 schedule: when the last round of
-    // tiles would leave most CUs idle, the column tiles that make up that round
-    // run afterwards as 128 x 128 tiles (twice as many, half the work each).
-    p.tail_ntiles = 0;
-    if (dp_tiles && p.t.BM == 256 && p.tiles > cus) {
-        const int rem = p.tiles % cus;
-        if (rem > 0 && rem * 10 <= cus * 6) {
-            const int nt = (int)ceil_div(rem, p.tiles_m);
-            if (nt < p.tiles_n) p.tail_ntiles = nt;
-        }
-    }
-    // One row of 128-row tiles that leaves CUs idle: the 32-column weight
-    // panels (four per tile) are spread evenly over the CUs instead, so every
-    // CU streams weights.
-    p.panels = 0;
-    if (v == SWIGLU_VARIANT_DATA_PARALLEL && p.t.BM == 128 && p.tiles_m == 1 && p.tiles_n < cus)
-        p.panels = 4 * p.tiles_n;
-    if (v == SWIGLU_VARIANT_SPLIT_K && p.tiles <= kMaxSplitTiles) {
-        // about kSplitWavesPerCu workgroups per CU, at least two K blocks per split
-        int s = (int)ceil_div((int64_t)kSplitWavesPerCu * cus, p.tiles);
-        if (auto_split_cap > 0) s = std::min(s, auto_split_cap);
-        s = std::max(1, std::min(s, p.KB / 2 > 0 ? p.KB / 2 : 1));
-        p.kb_per_split = (int)ceil_div(p.KB, s);
-        p.splits = (int)ceil_div(p.KB, p.kb_per_split);
-    } else {
-        p.splits = 1;
-        p.kb_per_split = p.KB;
-    }
-    return p;
-}
-
-// Split-K workspace: fp32 Gate and Up partial sums, [split][M][2N].
-size_t split_workspace_bytes(const Plan& p, int64_t M, int64_t N) {
-    if (p.variant != SWIGLU_VARIANT_SPLIT_K || p.splits <= 1) return 0;
-    return (size_t)p.splits * (size_t)M * 2 * (size_t)N * sizeof(float);
-}
-
-template <int BM, int BN, int WM, int WN, bool DUAL, bool PACKED, bool SPLIT>
-hipError_t launch_tile(const swk::FusedArgs& a, int grid, hipStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&swk::fused_tile_kernel<BM, BN, WM, WN, DUAL, PACKED, SPLIT>);
-    swk::FusedArgs args = a;
-    void* kargs[] = {&args};
-    return hipLaunchKernel(fn, dim3(grid), dim3(64 * WM * WN), kargs, 0, s);
-}
-
-// n_tiled: the packed weights' output columns (N for the fused product; 128
-// per packed tile for the single-weight GEMM).  HALF: one workgroup per
-// (column groups, weight half), twice the grid.
-// la: low-rank adapters (NULL: none).
-template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false>
-hipError_t launch_decode(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t s, const swk::LoraArgs* la) {
-    void (*plain)(swk::DecodeArgs) = &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA>;
-    void (*adapted)(swk::DecodeArgs, swk::LoraArgs) = &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA, swk::LoraArgs>;
-    const void* fn = la ? reinterpret_cast<const void*>(adapted) : reinterpret_cast<const void*>(plain);
-    swk::DecodeArgs args = a;
-    swk::LoraArgs lora = la ? *la : swk::LoraArgs{};
-    void* kargs[] = {&args, &lora};
-    return hipLaunchKernel(fn, dim3((unsigned)(ceil_div(n_tiled, 16 * CG) * (HALF ? 2 : 1))), dim3(256), kargs, 0,
-                           s);
-}
-
-template <int BM, int BN, int WM, int WN, bool SPLIT, int WSRC = swk::W_PACKED>
-hipError_t launch_prefill(const swk::FusedArgs& a, int grid, hipStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&swk::fused_prefill_kernel<BM, BN, WM, WN, SPLIT, WSRC>);
-    swk::FusedArgs args = a;
-    void* kargs[] = {&args};
-    return hipLaunchKernel(fn, dim3(grid), dim3(64 * WM * WN), kargs, 0, s);
-}
-
-// `total` work items (tiles, or tile x K split) on `grid` <= total workgroups;
-// each workgroup takes items b, b + grid, ...
-template <int BM, bool SPLIT, bool PANELS = false, bool IL = false, bool F8 = false, bool SEQ = false,
-          bool GEMM = false>
-hipError_t launch_stream(const swk::FusedArgs& a, int total, int grid, hipStream_t s,
-                         const swk::LoraArgs* la = nullptr) {
-    const bool ragged = (a.K % (F8 ? 128 : swk::BK)) != 0;
-    if constexpr (!SPLIT && !IL && !F8 && !SEQ) {
-        if (la) {
-            // up to 256 rows (every panel schedule) the adapters' part is in memory
-            const void* fn =
-                ragged ? reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, true, PANELS, GEMM, PANELS ? 2 : 1>)
-                       : reinterpret_cast<const void*>(&swk::stream_lora_kernel<BM, false, PANELS, GEMM, PANELS ? 2 : 1>);
-            if constexpr (BM == 128 && !PANELS) {
-                if (la->delta)
-                    fn = ragged ? reinterpret_cast<const void*>(&swk::stream_lora_kernel<128, true, false, GEMM, 2>)
-                                : reinterpret_cast<const void*>(&swk::stream_lora_kernel<128, false, false, GEMM, 2>);
-            }
-            swk::FusedArgs args = a;
-            swk::LoraArgs lora = *la;
-            void* kargs[] = {&args, &lora, &total};
-            return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, 0, s);
-        }
-    }
-    const void* fn =
-        ragged ? reinterpret_cast<const void*>(&swk::stream_prefill_kernel<BM, SPLIT, true, PANELS, IL, F8, SEQ, GEMM>)
-               : reinterpret_cast<const void*>(&swk::stream_prefill_kernel<BM, SPLIT, false, PANELS, IL, F8, SEQ, GEMM>);
-    swk::FusedArgs args = a;
-    void* kargs[] = {&args, &total};
-    return hipLaunchKernel(fn, dim3(grid), dim3(256), kargs, 0, s);
-}
-
-// The data-parallel streaming schedules (128- or 256-row tiles, the panel
-// schedule, the mixed 256/128-row launch) on either weight layout; SEQ: the
-// sequential Gate-then-Up order (per-tile layout, no panel schedule).
-template <bool IL, bool F8 = false, bool SEQ = false, bool GEMM = false>
-hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t s,
-                            const swk::LoraArgs* la = nullptr) {
-    const int grid = p.tiles;
-    if (p.t.BM == 128) {
-        if constexpr (SEQ) return launch_stream<128, false, false, false, false, true>(a, grid, grid, s);
-        if constexpr (!GEMM && !IL) {
-            // two rows of 128-row tiles that leave CUs idle on a wide product:
-            // one row of 256-row tiles on the panel schedule instead, the
-            // weights streamed once (7B width M=192 98.6 -> 84.2 us, 72B width
-            // M=256 259 -> 226 us; FP8 72B width M=192 144 -> 127 us; the 0.5B
-            // width's few short panels lose, 13.5 against 24 us, and keep the
-            // 128-row tiles, as does the interleaved layout, 95 against 107 us
-            // at the 7B width)
-            if (p.tiles_m == 2 && a.M <= 256 && p.tiles_n < p.cus && 2 * p.tiles_n >= p.cus) {
-                swk::FusedArgs pa = a;
-                pa.tiles_m = 1;
-                pa.panels = 4 * p.tiles_n;
-                const int g = std::min(pa.panels, p.cus);
-                return launch_stream<256, false, true, IL, F8, false, false>(pa, g, g, s, la);
-            }
-        }
-        if (p.panels > 0) {
-            // the single-weight GEMM's units are half-panels (one weight half
-            // each), as long as no workgroup gets more than its 4 waves
-            swk::FusedArgs pa = a;
-            pa.panels = GEMM ? 2 * p.panels : p.panels;
-            if (pa.panels <= 4 * p.cus) {
-                const int g = std::min(pa.panels, p.cus);
-                return launch_stream<128, false, true, IL, F8, false, GEMM>(pa, g, g, s, la);
-            }
-        }
-        return launch_stream<128, false, false, IL, F8, false, GEMM>(a, grid, grid, s, la);
-    }
-    // one workgroup per CU works through the 256-row tiles
-    if (p.tail_ntiles == 0)
-        return launch_stream<256, false, false, IL, F8, SEQ, GEMM>(a, grid, std::min(grid, p.cus), s, la);
-    // one launch: the 256-row tiles of the first column tiles, then
-    // the last tail_ntiles column tiles as 128-row tiles
-    swk::FusedArgs big = a, tail = a;
-    big.tiles_n = p.tiles_n - p.tail_ntiles;
-    tail.tiles_m = (int)ceil_div(a.M, 128);
-    tail.tiles_n = p.tail_ntiles;
-    tail.n_tile0 = big.tiles_n;
-    int n_big = big.tiles_m * big.tiles_n;
-    int n_pers = std::min(n_big, p.cus);
-    const int grid_all = n_pers + tail.tiles_m * tail.tiles_n;
-    const bool ragged = (a.K % (F8 ? 128 : swk::BK)) != 0;
-    if constexpr (!IL && !F8 && !SEQ) {
-        if (la) {
-            const void* lfn = ragged ? reinterpret_cast<const void*>(&swk::stream_lora_mixed_kernel<true, GEMM>)
-                                     : reinterpret_cast<const void*>(&swk::stream_lora_mixed_kernel<false, GEMM>);
-            swk::LoraArgs lora = *la;
-            void* largs[] = {&big, &tail, &lora, &n_pers, &n_big};
-            return hipLaunchKernel(lfn, dim3(grid_all), dim3(256), largs, 0, s);
-        }
-    }
-    const void* fn = ragged
-                         ? reinterpret_cast<const void*>(&swk::stream_prefill_mixed_kernel<true, IL, F8, SEQ, GEMM>)
-                         : reinterpret_cast<const void*>(&swk::stream_prefill_mixed_kernel<false, IL, F8, SEQ, GEMM>);
-    void* kargs[] = {&big, &tail, &n_pers, &n_big};
-    return hipLaunchKernel(fn, dim3(grid_all), dim3(256), kargs, 0, s);
-}
-
-// The data-parallel streaming plan (any M).
-Plan stream_dp_plan(int64_t M, int64_t K, int64_t N, int cus) {
-    return make_plan(M, K, N, SWIGLU_VARIANT_DATA_PARALLEL, cus);
 }
 
 // FP8 decode (M <= 32): groups of 32 output columns per workgroup (CG) and
@@ -395,86 +101,6 @@ hipError_t launch_decode_fp8(const swk::FusedArgs& a, int cus, hipStream_t s) {
     const int64_t wide = ceil_div(a.N, 128);
     if (wide <= cus && 4 * wide >= 3 * (int64_t)cus) return launch_decode_fp8_cfg<4, 1>(a, s);
     return a.M > 8 ? launch_decode_fp8_cfg<1, 2, true>(a, s) : launch_decode_fp8_cfg<1, 2>(a, s);
-}
-
-// The decode kernel's configuration for a plan: column groups per workgroup
-// (CG) and K blocks in flight per wave (UNROLL), measured on this chip: wider
-// groups read each activation fragment for more weight bytes and stream
-// longer contiguous runs of the packed blocks; they pay off for long K (>= 96
-// blocks), or from 17 tokens on, as long as the grid still gives about one
-// workgroup per CU.  Measured (us, one call, inputs rotated past the
-// last-level cache):
-//   K=3584 N=18944 M=1 / 16: <1,1,8> 42.9 / 45.8, <1,1,4> 43.0 / 46.3, <1,2,4> 46.1 / 47.5
-//   K=8192 N=29568 M=1 / 16: <1,8,2> 138.4 / 138.0, the same with L 142.3 / 142.0
-//   K=8192 N=29568 M=32: <2,8,1> 140.2, <2,4,1> 147.3, <2,2,2> 170.4
-//   K=3584 N=18944 M=32: <2,8,1> 52.2, <2,2,2> 54.7, <2,4,1> 61.8
-//   K=896 N=4864 M=64: <4,2,1> 9.9, <4,2,2> 10.5, <4,1,1> 11.8
-// With the activations staged through LDS (L = LDSA: one full-line load
-// per 8 rows instead of a half-line per row and fragment), which pays once
-// there are more than 8 distinct rows and the group is narrow:
-//   K=3584 N=18944 M=16: <1,1,8,L> 44.1-44.4 against 45.9-46.3; M=1 / 4 / 8: no gain
-//   K=896 N=4864 M=64: <4,2,1,L> 9.33-9.38 against 9.82-9.90; M=32 with 8 groups: 55.6 against 52.0
-// n_tiled: the packed weights' output columns.
-hipError_t launch_decode_cfg(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s,
-                             const swk::LoraArgs* la = nullptr) {
-    const bool long_k = p.KB >= 96;
-    const int64_t wg64 = ceil_div(n_tiled, 64), wg128 = ceil_div(n_tiled, 128);
-    switch (p.decode_mt) {
-        case 1:
-            if (long_k && 4 * wg128 >= 3 * p.cus) return launch_decode<1, 8, 2>(d, n_tiled, s, la);
-            return d.M > 8 ? launch_decode<1, 1, 8, false, false, true>(d, n_tiled, s, la)
-                           : launch_decode<1, 1, 8>(d, n_tiled, s, la);
-        case 2:
-            if (2 * wg128 >= p.cus) return launch_decode<2, 8, 1>(d, n_tiled, s, la);
-            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<2, 4, 1>(d, n_tiled, s, la)
-                                                    : launch_decode<2, 2, 2>(d, n_tiled, s, la);
-        default:
-            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<4, 4, 1>(d, n_tiled, s, la)
-                                                    : launch_decode<4, 2, 1, false, false, true>(d, n_tiled, s, la);
-    }
-}
-
-// The same for the single-weight GEMM (n_tiled = 128 per 256-column packed
-// tile), where a workgroup may take one weight half (HALF): half the bytes per
-// workgroup and twice the grid.  Measured on this chip (us, one call, inputs
-// rotated past the last-level cache):
-//   K=3584 N=18944 M=1: <1,1,14,H> 22.6, <1,1,8,H> 23.2, <1,1,8> 23.9
-//   K=3584 N=18944 M=16: <1,1,8> 26.7, <1,1,8,H> 29.7
-//   K=8192 N=29568 M=1 / 16: <1,4,4,H> 79.5 / 78.6, <1,1,8> 93.7 / 99.0
-//   K=18944 N=3584 M=1 / 16: <1,1,14,H> 23.3 / 31.3, <1,1,8,H> 23.6 / 30.8, <1,1,8> 30.6 / 42.6
-//   K=8192 N=29568 M=32: <2,8,1,H> 73.3, <2,4,1> 76.1, <2,2,2,H> 113.4
-//   K=29568 N=8192 M=32: <2,2,2,H> 92.8, <2,2,2> 129.3, <2,4,1,H> 123.9
-//   K=896 N=4864 M=64: <4,2,1,H> 8.0, <4,2,1> 9.5
-//   K=4864 N=896 M=64: <4,1,1,H> 21.8, <4,2,1,H> 24.4, <4,2,1> 31.8
-// and with the activations staged through LDS (L, as for the fused product):
-//   K=3584 N=18944 M=16: <1,1,8,H,L> 25.2, <1,1,8,L> 26.3, <1,1,8> 27.0
-//   K=18944 N=3584 M=16: <1,1,8,H,L> 27.4, <1,1,8,H> 30.9; K=4864 N=896 M=16: 7.9 against 9.5
-//   K=8192 N=29568 M=16: <1,4,4,H> 77.7, <1,4,4,H,L> 79.5
-//   K=896 N=4864 M=64: <4,1,1,H,L> 6.8, <4,2,1,H,L> 7.1, <4,2,1,H> 8.0
-//   K=4864 N=896 M=64: <4,1,1,H,L> 17.6, <4,1,1,H> 21.8
-// i.e. halves whenever the whole-pair grid leaves CUs short of work, the
-// deepest per-wave prefetch the registers allow at one or two tokens' rows,
-// and staged activations for narrow groups from 9 rows on.
-hipError_t launch_decode_gemm(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s,
-                             const swk::LoraArgs* la = nullptr) {
-    const bool long_k = p.KB >= 96;
-    const int64_t wg64 = ceil_div(n_tiled, 64);
-    switch (p.decode_mt) {
-        case 1:
-            if (long_k && 2 * wg64 >= p.cus) return launch_decode<1, 4, 4, true, true>(d, n_tiled, s, la);
-            if (d.M <= 8) return launch_decode<1, 1, 14, true, true>(d, n_tiled, s, la);
-            return launch_decode<1, 1, 8, true, true, true>(d, n_tiled, s, la);
-        case 2:
-            if (long_k) {
-                return 4 * wg64 >= 3 * p.cus ? launch_decode<2, 8, 1, true, true>(d, n_tiled, s, la)
-                                             : launch_decode<2, 2, 2, true, true>(d, n_tiled, s, la);
-            }
-            return 2 * ceil_div(n_tiled, 128) >= p.cus ? launch_decode<2, 8, 1, true>(d, n_tiled, s, la)
-                                                       : launch_decode<2, 2, 2, true>(d, n_tiled, s, la);
-        default:
-            if (long_k && 4 * wg64 >= 3 * p.cus) return launch_decode<4, 4, 1, true>(d, n_tiled, s, la);
-            return launch_decode<4, 1, 1, true, true, true>(d, n_tiled, s, la);
-    }
 }
 
 hipError_t launch_packed(const swk::FusedArgs& a, const Plan& p, hipStream_t s) {
@@ -915,29 +541,6 @@ swiglu_status swiglu_gemm_pack_weight(const swiglu_bf16* W, swiglu_bf16* Wg, int
     hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&swk::pack_kernel<false, true>),
                                    dim3((unsigned)ceil_div(nchunks, 256)), dim3(256), args, 0, (hipStream_t)stream);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
-}
-
-// The single-weight GEMM's plan: the fused product's AUTO rule on the pack's
-// tiled width (128 columns per packed tile), whose split-K needs fp32
-// partials over those tiled columns.  One addition: a compute-bound product
-// (from 1024 rows on) whose data-parallel tiles leave over half the CUs idle
-// -- a narrow output, like the MLP's down projection back to a small model
-// width -- splits K as well: there the idle matrix cores cost more than the
-// partial sums' traffic (measured: 0.5B-width down projection, M=4096
-// K=4864 N=896, 86.6 us data-parallel on 64 tiles, 70 us in 4 splits).
-Plan gemm_plan(int64_t M, int64_t K, int64_t N) {
-    const int cus = cu_count_now();
-    const int64_t nt = gemm_tiled_cols(N);
-    Plan p = make_plan(M, K, nt, SWIGLU_VARIANT_AUTO, cus);
-    if (p.variant == SWIGLU_VARIANT_DATA_PARALLEL && M >= 1024 && 2 * (int64_t)p.tiles < p.cus) {
-        const Plan q = make_plan(M, K, nt, SWIGLU_VARIANT_SPLIT_K, cus);
-        if (q.splits > 1) p = q;
-    }
-    return p;
-}
-
-size_t gemm_split_bytes(const Plan& p, int64_t M, int64_t N) {
-    return split_workspace_bytes(p, M, gemm_tiled_cols(N));
 }
 
 size_t swiglu_gemm_workspace_bytes(int64_t M, int64_t K, int64_t N) {

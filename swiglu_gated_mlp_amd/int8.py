@@ -1,0 +1,184 @@
+"""The gated MLP from int8 operands with a scale for each token and channel:
+argument marshalling for the C entry points of the same names
+(``include/swiglu.h``)."""
+from __future__ import annotations
+
+import torch
+
+from . import _check, _dev_bf16, _empty, _new, _ptr, _scratch, _shape, _stream, lib
+
+_need: dict = {}
+
+
+def _cached(fn, *args, device=None) -> int:
+    key = (fn, args, None if device is None else device.index)
+    need = _need.get(key)
+    if need is None:
+        if len(_need) >= 4096:
+            _need.clear()
+        need = _need[key] = fn(*args)
+    return need
+
+
+def swiglu_packed_bytes_int8(K: int, N: int) -> int:
+    return int(lib().swiglu_packed_bytes_int8(K, N))
+
+
+def swiglu_gemm_packed_bytes_int8(K: int, N: int) -> int:
+    return int(lib().swiglu_gemm_packed_bytes_int8(K, N))
+
+
+def swiglu_workspace_bytes_int8(M: int, K: int, N: int) -> int:
+    return int(lib().swiglu_workspace_bytes_int8(M, K, N))
+
+
+def swiglu_gemm_workspace_bytes_int8(M: int, K: int, N: int) -> int:
+    return int(lib().swiglu_gemm_workspace_bytes_int8(M, K, N))
+
+
+def swiglu_mlp_workspace_bytes_int8(M: int, K: int, N: int) -> int:
+    return int(lib().swiglu_mlp_workspace_bytes_int8(M, K, N))
+
+
+def _dev(t, dtype, name: str) -> int:
+    """A contiguous GPU tensor of dtype."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, str(dtype)[6:], t.dtype))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _matrix(t, name: str):
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix (got %s)" % (name, list(t.shape)))
+    return t.shape
+
+
+def _out(t, shape, dtype, device, s: int, stream):
+    if t is not None:
+        return t
+    return torch.empty(shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, device, s)
+
+
+def _quantize(fn: str, X, Q, scales, n: int, stream):
+    R, C = X.shape
+    _shape(Q, (R, C), "Q")
+    _shape(scales, (n,), "scales")
+    x, s = _dev_bf16(X, "A" if fn == "swiglu_quantize_rows_int8" else "W"), _stream(stream)
+    Q = _out(Q, (R, C), torch.int8, X.device, s, stream)
+    scales = _out(scales, (n,), torch.float32, X.device, s, stream)
+    _check(fn, getattr(lib(), fn)(x, _dev(Q, torch.int8, "Q"), _dev(scales, torch.float32, "scales"), R, C, s))
+    return Q, scales
+
+
+def swiglu_quantize_rows_int8(A: torch.Tensor, Q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                              stream=None):
+    """A [M,K] bf16 as (codes int8 [M,K], scales fp32 [M]), a scale for each row."""
+    return _quantize("swiglu_quantize_rows_int8", A, Q, scales, _matrix(A, "A")[0], stream)
+
+
+def swiglu_quantize_columns_int8(W: torch.Tensor, Q: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                                 stream=None):
+    """W [K,N] bf16 as (codes int8 [K,N], scales fp32 [N]), a scale for each column."""
+    return _quantize("swiglu_quantize_columns_int8", W, Q, scales, _matrix(W, "W")[1], stream)
+
+
+def _packed(fn: str, sizer, weights, Wp, name: str, stream):
+    (W, first), *rest = weights
+    K, N = _matrix(W, first)
+    for t, n in rest:
+        _shape(t, (K, N), n)
+    nbytes = _cached(sizer, K, N)
+    if nbytes == 0:
+        raise ValueError("invalid int8 weight shape [%d,%d] (K must be a multiple of 16, N of 8)" % (K, N))
+    ptrs, s = [_dev(t, torch.int8, n) for t, n in weights], _stream(stream)
+    if Wp is not None and Wp.numel() < nbytes:
+        raise ValueError("%s too small: need %d bytes" % (name, nbytes))
+    Wp = _out(Wp, (nbytes,), torch.int8, W.device, s, stream)
+    _check(fn, getattr(lib(), fn)(*ptrs, _dev(Wp, torch.int8, name), K, N, s))
+    return Wp
+
+
+def swiglu_pack_weights_int8(W1: torch.Tensor, W2: torch.Tensor, Wp: torch.Tensor | None = None,
+                             stream=None) -> torch.Tensor:
+    """Pack the codes W1, W2 int8 [K,N] for swiglu_fused_packed_int8."""
+    return _packed("swiglu_pack_weights_int8", swiglu_packed_bytes_int8, [(W1, "W1"), (W2, "W2")], Wp, "Wp", stream)
+
+
+def swiglu_gemm_pack_weight_int8(W: torch.Tensor, Wg: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Pack one weight's codes W int8 [K,N] for swiglu_gemm_packed_int8."""
+    return _packed("swiglu_gemm_pack_weight_int8", swiglu_gemm_packed_bytes_int8, [(W, "W")], Wg, "Wg", stream)
+
+
+def _weight_at_least(W, sizer, K: int, N: int, name: str) -> None:
+    need = _cached(sizer, K, N)
+    if need == 0:
+        raise ValueError("invalid int8 weight shape [%d,%d]" % (K, N))
+    if W.numel() * W.element_size() < need:
+        raise ValueError("%s holds %d bytes; a packed int8 [%d,%d] weight needs %d"
+                         % (name, W.numel() * W.element_size(), K, N, need))
+
+
+def _vectors(pairs, n: int):
+    for t, name in pairs:
+        _shape(t, (n,), name)
+    return [_dev(t, torch.float32, name) for t, name in pairs]
+
+
+def _product(fn: str, sizer, need_fn, A, sa, W, wname, scales, out, oname, workspace, stream):
+    M, K = _matrix(A, "A")
+    N = scales[0][0].shape[0]
+    _weight_at_least(W, sizer, K, N, wname)
+    _shape(out, (M, N), oname)
+    a, (r,) = _dev(A, torch.int8, "A"), _vectors([(sa, "sa")], M)
+    w, cols = _dev(W, torch.int8, wname), _vectors(scales, N)
+    s = _stream(stream)
+    out = _new((M, N), A.device, s, stream) if out is None else out
+    ws, ws_bytes = _scratch(workspace, _cached(need_fn, M, K, N, device=A.device), A.device, s)
+    _check(fn, getattr(lib(), fn)(a, r, w, *cols, _dev_bf16(out, oname), M, K, N, _ptr(ws), ws_bytes, s))
+    return out
+
+
+def swiglu_fused_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, s2: torch.Tensor,
+                             Y: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """Y = SiLU(G) * U bf16 [M,N] from the codes A int8 [M,K], their rows' scales sa
+    [M], the packed codes of W1 and W2 and their columns' scales s1, s2 [N] (fp32)."""
+    return _product("swiglu_fused_packed_int8", swiglu_packed_bytes_int8, swiglu_workspace_bytes_int8, A, sa, Wp,
+                    "Wp", [(s1, "s1"), (s2, "s2")], Y, "Y", workspace, stream)
+
+
+def swiglu_gemm_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wg: torch.Tensor, sw: torch.Tensor,
+                            C: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
+    """C = A @ W bf16 [M,N] from the codes A int8 [M,K], sa [M], one weight's packed
+    codes and its columns' scales sw [N] (fp32)."""
+    return _product("swiglu_gemm_packed_int8", swiglu_gemm_packed_bytes_int8, swiglu_gemm_workspace_bytes_int8, A, sa,
+                    Wg, "Wg", [(sw, "sw")], C, "C", workspace, stream)
+
+
+def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, s2: torch.Tensor, W3g: torch.Tensor,
+                           s3: torch.Tensor, Y: torch.Tensor | None = None, Z: torch.Tensor | None = None,
+                           workspace=None, stream=None):
+    """The gated MLP block from A bf16 [M,K]: its rows quantized, Y = SiLU(G) * U
+    (bf16), Y's rows quantized, Z = Y @ W3.  Returns (Y, Z)."""
+    M, K = _matrix(A, "A")
+    N = s1.shape[0]
+    _weight_at_least(Wp, swiglu_packed_bytes_int8, K, N, "Wp")
+    _weight_at_least(W3g, swiglu_gemm_packed_bytes_int8, N, K, "W3g")
+    for t, shape, name in ((Y, (M, N), "Y"), (Z, (M, K), "Z")):
+        _shape(t, shape, name)
+    a, wp, w3 = _dev_bf16(A, "A"), _dev(Wp, torch.int8, "Wp"), _dev(W3g, torch.int8, "W3g")
+    p1, p2 = _vectors([(s1, "s1"), (s2, "s2")], N)
+    p3, = _vectors([(s3, "s3")], K)
+    s = _stream(stream)
+    Y = _new((M, N), A.device, s, stream) if Y is None else Y
+    Z = _new((M, K), A.device, s, stream) if Z is None else Z
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_mlp_workspace_bytes_int8, M, K, N, device=A.device), A.device, s)
+    st = lib().swiglu_mlp_packed_int8(a, wp, p1, p2, w3, p3, _dev_bf16(Y, "Y"), _dev_bf16(Z, "Z"), M, K, N, _ptr(ws),
+                                      ws_bytes, s)
+    _check("swiglu_mlp_packed_int8", st)
+    return Y, Z
