@@ -491,6 +491,54 @@ swiglu_status swiglu_mlp_train_backward(
     int64_t N, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Training with Gate and Up kept as int8 instead of bf16: 1.0625 bytes an element
+ * of either for 2, and Y is not kept for the block's backward pass (M N bytes times
+ * 2.125 instead of 6).  A group of 32 columns of a row has one scale for Gate and
+ * one for Up:
+ *     s = max(max |x| / 127 rounded up to bf16, 2^-126),  code = round(x / s)
+ * of the fp32 sums x, within 2^-16 of a step exact; the backward calls compute from
+ * G = code s and U alike, and Y = bf16(SiLU(G) U) of those for dW3.  A kept element
+ * is off by at most half a step, max |x| of its group / 253.  A group that holds an
+ * infinity or NaN has the scale NaN: what is computed from it is NaN.
+ *   codes  int8 [M][groups][2][32], groups = ceil(N / 32): Gate's codes of a group,
+ *          then Up's; codes of columns past N are 0
+ *   scales bf16 [groups][M][2]: Gate's, Up's
+ *
+ * swiglu_train_forward_int8: Y [M,N] and codes and scales; workspace as for
+ *   swiglu_train_forward (swiglu_train_forward_workspace_bytes).
+ * swiglu_train_backward_int8, swiglu_mlp_train_backward_int8: as the calls without
+ *   _int8, from codes and scales.
+ * swiglu_train_workspace_bytes_int8: workspace of the backward calls at (M,K,N)
+ *   ([dG | dU], Y and sums of splits); enough for the forward call too.  0 for an
+ *   invalid shape and for M == 0.
+ * swiglu_dequantize_kept_int8: G and U [M,N], code s rounded to bf16.
+ * All: as the calls above; codes and scales 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+size_t swiglu_train_workspace_bytes_int8(int64_t M, int64_t K, int64_t N);
+swiglu_status swiglu_train_forward_int8(const swiglu_bf16 *A,
+                                        const swiglu_bf16 *W1,
+                                        const swiglu_bf16 *W2, swiglu_bf16 *Y,
+                                        int8_t *codes, swiglu_bf16 *scales,
+                                        int64_t M, int64_t K, int64_t N,
+                                        void *workspace, size_t workspace_bytes,
+                                        void *stream);
+swiglu_status swiglu_dequantize_kept_int8(const int8_t *codes,
+                                          const swiglu_bf16 *scales,
+                                          swiglu_bf16 *G, swiglu_bf16 *U,
+                                          int64_t M, int64_t N, void *stream);
+swiglu_status swiglu_train_backward_int8(
+    const swiglu_bf16 *dY, const swiglu_bf16 *A, const swiglu_bf16 *W1,
+    const swiglu_bf16 *W2, const int8_t *codes, const swiglu_bf16 *scales,
+    swiglu_bf16 *dA, swiglu_bf16 *dW1, swiglu_bf16 *dW2, int64_t M, int64_t K,
+    int64_t N, void *workspace, size_t workspace_bytes, void *stream);
+swiglu_status swiglu_mlp_train_backward_int8(
+    const swiglu_bf16 *dZ, const swiglu_bf16 *A, const swiglu_bf16 *W1,
+    const swiglu_bf16 *W2, const swiglu_bf16 *W3, const int8_t *codes,
+    const swiglu_bf16 *scales, swiglu_bf16 *dA, swiglu_bf16 *dW1,
+    swiglu_bf16 *dW2, swiglu_bf16 *dW3, int64_t M, int64_t K, int64_t N,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Low-rank adapters of many requests beside the packed products.  Row m of a
  * batch has adapter i = ids[m]; ids outside 0 .. adapters - 1 (-1 by
  * convention) have none.  An adapter adds a rank-`rank` product to a projection:

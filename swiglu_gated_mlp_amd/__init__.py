@@ -72,6 +72,11 @@ SIGNATURES = {
     "swiglu_train_forward": ([_P] * 6 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "swiglu_train_backward": ([_P] * 9 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "swiglu_mlp_train_backward": ([_P] * 12 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_train_workspace_bytes_int8": ([_I64, _I64, _I64], ctypes.c_size_t),
+    "swiglu_train_forward_int8": ([_P] * 6 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_dequantize_kept_int8": ([_P] * 4 + [_I64, _I64, _P], ctypes.c_int),
+    "swiglu_train_backward_int8": ([_P] * 9 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "swiglu_mlp_train_backward_int8": ([_P] * 11 + [_I64, _I64, _I64, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "swiglu_lora_packed_bytes": ([_I64] * 4, ctypes.c_size_t),
     "swiglu_gemm_lora_packed_bytes": ([_I64] * 4, ctypes.c_size_t),
     "swiglu_lora_pack": ([_P] * 5 + [_I64] * 4 + [_P], ctypes.c_int),
@@ -727,8 +732,10 @@ def swiglu_probe_train_plan(launch: str, M: int, K: int, N: int) -> list:
 
 
 # training (gradients and differentiable forms of the product and the block)
-from .train import (swiglu, swiglu_mlp, swiglu_mlp_train_backward, swiglu_train_backward,  # noqa: E402,F401
-                    swiglu_train_forward, swiglu_train_forward_workspace_bytes, swiglu_train_workspace_bytes)
+from .train import (swiglu, swiglu_dequantize_kept_int8, swiglu_mlp, swiglu_mlp_train_backward,  # noqa: E402,F401
+                    swiglu_mlp_train_backward_int8, swiglu_train_backward, swiglu_train_backward_int8,
+                    swiglu_train_forward, swiglu_train_forward_int8, swiglu_train_forward_workspace_bytes,
+                    swiglu_train_workspace_bytes, swiglu_train_workspace_bytes_int8)
 
 # low-rank adapters of many requests beside the packed products
 from .lora import (swiglu_fused_packed_lora, swiglu_gemm_lora_pack, swiglu_gemm_lora_packed_bytes,  # noqa: E402,F401

@@ -57,6 +57,15 @@ __device__ __forceinline__ unsigned pack2(float lo, float hi) {
     return __builtin_bit_cast(unsigned, h);
 }
 
+// The low bytes of four words as one word.
+__device__ __forceinline__ unsigned low_bytes(unsigned a, unsigned b, unsigned c, unsigned d) {
+    const unsigned ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), cd = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
+    return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+}
+// 1.5 * 2^23: added to a number below 2^22, it leaves the nearest whole number
+// (ties to even) in the low bits.
+constexpr float ROUND_BITS = 12582912.0f;
+
 // Map the hardware workgroup id to a logical id such that XCD x (which gets
 // ids x, x+8, x+16, ...) owns one contiguous range of logical ids.
 __device__ __forceinline__ int xcd_remap(int bid, int total) {

@@ -45,20 +45,14 @@ __device__ __forceinline__ Scale scale_of(unsigned top_bits) {
     return Scale{top / 127.0f, 127.0f / top};
 }
 
-// Two bf16 to codes in the low bytes of a and b: 1.5 * 2^23 added to a product
-// below 2^22 leaves its nearest whole number (ties to even) in the low bits.  The
-// product is rounded first (the definition's two steps), so no fma here.
+// Two bf16 to codes in the low bytes of a and b.  The product is rounded before
+// its nearest whole number is taken (the definition's two steps): no fma here.
 __device__ __forceinline__ void code2(unsigned w, float inv, unsigned& a, unsigned& b) {
 #pragma clang fp contract(off)
     const float x = __builtin_bit_cast(float, w << 16) * inv;
     const float y = __builtin_bit_cast(float, w & 0xFFFF0000u) * inv;
-    a = __builtin_bit_cast(unsigned, x + 12582912.0f);
-    b = __builtin_bit_cast(unsigned, y + 12582912.0f);
-}
-// low bytes of four words to one
-__device__ __forceinline__ unsigned low_bytes(unsigned a, unsigned b, unsigned c, unsigned d) {
-    const unsigned ab = __builtin_amdgcn_perm(b, a, 0x0c0c0400u), cd = __builtin_amdgcn_perm(d, c, 0x0c0c0400u);
-    return __builtin_amdgcn_perm(cd, ab, 0x05040100u);
+    a = __builtin_bit_cast(unsigned, x + ROUND_BITS);
+    b = __builtin_bit_cast(unsigned, y + ROUND_BITS);
 }
 __device__ __forceinline__ u32x2 codes8(u32x4 v, Scale s) {
     unsigned b[8];

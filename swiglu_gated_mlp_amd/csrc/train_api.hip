@@ -36,6 +36,11 @@ struct Buffers {
     int n = 0;
     void in(const void* p, int64_t elems) { item[n++] = Item{p, elems * 2, false}; }
     void out(const void* p, int64_t elems) { item[n++] = Item{p, elems * 2, true}; }
+    void kept(const void* codes, const void* scales, int64_t M, int64_t N, bool out) {
+        const int64_t groups = ceil_div(N, swt::GROUP);
+        item[n++] = Item{codes, M * groups * 2 * swt::GROUP, out};
+        item[n++] = Item{scales, M * groups * 4, out};
+    }
     swiglu_status check() const {
         for (int i = 0; i < n; ++i)
             if (!item[i].p) return SWIGLU_ERR_NULL_POINTER;
@@ -55,7 +60,8 @@ struct Buffers {
 // ---------------------------------------------------------------------------
 // F_: the forward product; then the products of a backward pass in its two phases,
 // D (recomputed, or from dZ; with dW3 beside it), then dA and dW1 | dW2.
-enum Kind { F_KEEP, D_DUAL, D_DY, G_DA, G_DW, G_DW3 };
+// F_KEEP8, D_DY8: with Gate and Up kept as int8.
+enum Kind { F_KEEP, D_DUAL, D_DY, G_DA, G_DW, G_DW3, F_KEEP8, D_DY8 };
 
 struct Shape {
     int64_t rows, cols, kb;   // output (dual: columns of each half), contraction blocks
@@ -66,9 +72,9 @@ Shape shape_of(Kind p, int64_t M, int64_t K, int64_t N) {
     switch (p) {
         case G_DA: return {M, K, 2 * ceil_div(N, 64), false, false};
         case G_DW: return {K, 2 * N, ceil_div(M, 64), false, true};
-        case D_DY: return {M, N, ceil_div(K, 64), false, false};
+        case D_DY: case D_DY8: return {M, N, ceil_div(K, 64), false, false};
         case G_DW3: return {N, K, ceil_div(M, 64), false, true};
-        default: return {M, N, ceil_div(K, 64), true, false};   // F_KEEP, D_DUAL
+        default: return {M, N, ceil_div(K, 64), true, false};   // F_KEEP, F_KEEP8, D_DUAL
     }
 }
 
@@ -273,6 +279,7 @@ Launch plan_launch(int jobs, const Kind* kind, int64_t M, int64_t K, int64_t N, 
 
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 int64_t d_bytes(int64_t M, int64_t N) { return align256(M * 2 * N * 2); }
+int64_t y_bytes(int64_t M, int64_t N) { return align256(M * N * 2); }
 
 // The launches of a backward pass: D, then the gradients.
 struct Passes {
@@ -284,11 +291,11 @@ struct Passes {
         return b;
     }
 };
-// d: D_DUAL, D_DY, or -1 (kept Gate and Up: an element-wise kernel)
+// d: D_DUAL, D_DY, D_DY8, or -1 (kept Gate and Up: an element-wise kernel)
 Passes plan_backward(int d, bool da, bool dw, int64_t M, int64_t K, int64_t N, int cus) {
     Passes p;
-    if (d == D_DY && dw) {
-        const Kind k[2] = {D_DY, G_DW3};
+    if ((d == D_DY || d == D_DY8) && dw) {
+        const Kind k[2] = {(Kind)d, G_DW3};
         p.l[p.n++] = plan_launch(2, k, M, K, N, cus);
     } else if (d >= 0) {
         const Kind k[1] = {(Kind)d};
@@ -340,7 +347,7 @@ hipError_t launch_pair(const Launch& l, swt::GemmArgs a, swt::GemmArgs b, hipStr
 template <class A>
 hipError_t launch_with(const Launch& l, const swt::GemmArgs& a, const swt::GemmArgs& b, hipStream_t s) {
     if (l.jobs == 1) return launch_pair<A, swt::NoProduct>(l, a, b, s);
-    if constexpr (A::EPI == swt::EP_STORE || A::EPI == swt::EP_DY_D) {
+    if constexpr (A::EPI == swt::EP_STORE || A::EPI == swt::EP_DY_D || A::EPI == swt::EP_DY_D8) {
         if constexpr (A::BM == 256) return launch_pair<A, PGrad<256>>(l, a, b, s);
         else return l.t[1].bm == 256 ? launch_pair<A, PGrad<256>>(l, a, b, s) : launch_pair<A, PGrad<128>>(l, a, b, s);
     }
@@ -374,6 +381,8 @@ hipError_t run_launch(const Launch& l, swt::GemmArgs a, swt::GemmArgs b, float* 
         case F_KEEP: return launch_rows<PDual, swt::EP_KEEP>(l, a, b, s);
         case D_DUAL: return launch_rows<PDual, swt::EP_DUAL_D>(l, a, b, s);
         case D_DY: return launch_rows<PRows, swt::EP_DY_D>(l, a, b, s);
+        case F_KEEP8: return launch_rows<PDual, swt::EP_KEEP8>(l, a, b, s);
+        case D_DY8: return launch_rows<PRows, swt::EP_DY_D8>(l, a, b, s);
         case G_DA: return launch_rows<PRows, swt::EP_STORE>(l, a, b, s);
         default:
             return l.t[0].bm == 256 ? launch_pair<PGrad<256>, swt::NoProduct>(l, a, b, s)
@@ -444,6 +453,17 @@ hipError_t run_dgate(const Call& c, const uint16_t* dY, const uint16_t* G, const
     void* kargs[] = {(void*)&dY, (void*)&G, (void*)&U, (void*)&D, &N, &groups};
     return hipLaunchKernel(reinterpret_cast<const void*>(&swt::dgate_kernel),
                            dim3((unsigned)std::min<int64_t>(ceil_div(groups, 256), 16384)), dim3(256), kargs, 0, c.s);
+}
+
+// Elements from Gate and Up kept as int8 (swt::KeptUse).
+template <int USE>
+hipError_t run_kept(const int8_t* codes, const swiglu_bf16* scales, const uint16_t* dY, uint16_t* C0, uint16_t* C1,
+                    int64_t M, int64_t N, hipStream_t s) {
+    long long units = ceil_div(M, 4) * 2 * ceil_div(N, swt::GROUP);
+    int Mi = (int)M, Ni = (int)N;
+    void* kargs[] = {(void*)&codes, (void*)&scales, (void*)&dY, (void*)&C0, (void*)&C1, &Mi, &Ni, &units};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::kept_kernel<USE>),
+                           dim3((unsigned)std::min<int64_t>(ceil_div(units, 256), 16384)), dim3(256), kargs, 0, s);
 }
 
 // the weight gradients of an empty batch are zero
@@ -568,6 +588,116 @@ swiglu_status swiglu_mlp_train_backward(const swiglu_bf16* dZ, const swiglu_bf16
     a.C0 = c.D; a.E0 = G; a.E1 = U;
     const swt::GemmArgs dw3 = dw_args(c, Y, N, dZ, K, K, dW3, dW3);
     hipError_t e = run_launch(p.l[0], a, dw3, c.part, c.s);
+    if (e == hipSuccess && (dA || dW1)) e = run_gradients(c, p.l[p.n - 1], A, W1, W2, dA, dW1, dW2);
+    return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+size_t swiglu_train_workspace_bytes_int8(int64_t M, int64_t K, int64_t N) {
+    if (check_train_shape(M, K, N) != SWIGLU_OK || M == 0) return 0;
+    return (size_t)(train_workspace(M, K, N, cu_count_now()) + y_bytes(M, N));
+}
+
+swiglu_status swiglu_train_forward_int8(const swiglu_bf16* A, const swiglu_bf16* W1, const swiglu_bf16* W2,
+                                        swiglu_bf16* Y, int8_t* codes, swiglu_bf16* scales, int64_t M, int64_t K,
+                                        int64_t N, void* workspace, size_t workspace_bytes, void* stream) {
+    swiglu_status st = check_train_shape(M, K, N);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return SWIGLU_OK;
+    Buffers b;
+    b.in(A, M * K); b.in(W1, K * N); b.in(W2, K * N);
+    b.out(Y, M * N); b.kept(codes, scales, M, N, true);
+    if (workspace) b.out(workspace, (int64_t)(workspace_bytes / 2));
+    if ((st = b.check()) != SWIGLU_OK) return st;
+    const Kind f[1] = {F_KEEP8};
+    const Launch l = plan_launch(1, f, M, K, N, cu_count_now());
+    if (!workspace) workspace_bytes = 0;
+    if (workspace_bytes < (size_t)l.part_bytes()) return SWIGLU_ERR_WORKSPACE;
+    const Call c{M, K, N, (hipStream_t)stream, nullptr, (float*)workspace};
+    swt::GemmArgs a = dual_args(c, A, W1, W2);
+    a.C0 = Y; a.C1 = (uint16_t*)codes; a.C2 = scales;
+    const hipError_t e = run_launch(l, a, a, c.part, c.s);
+    return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+swiglu_status swiglu_dequantize_kept_int8(const int8_t* codes, const swiglu_bf16* scales, swiglu_bf16* G,
+                                          swiglu_bf16* U, int64_t M, int64_t N, void* stream) {
+    swiglu_status st = check_train_shape(M, 8, N);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return SWIGLU_OK;
+    Buffers b;
+    b.kept(codes, scales, M, N, false);
+    b.out(G, M * N); b.out(U, M * N);
+    if ((st = b.check()) != SWIGLU_OK) return st;
+    const hipError_t e = run_kept<swt::KEPT_GU>(codes, scales, nullptr, G, U, M, N, (hipStream_t)stream);
+    return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+swiglu_status swiglu_train_backward_int8(const swiglu_bf16* dY, const swiglu_bf16* A, const swiglu_bf16* W1,
+                                         const swiglu_bf16* W2, const int8_t* codes, const swiglu_bf16* scales,
+                                         swiglu_bf16* dA, swiglu_bf16* dW1, swiglu_bf16* dW2, int64_t M, int64_t K,
+                                         int64_t N, void* workspace, size_t workspace_bytes, void* stream) {
+    swiglu_status st = check_train_shape(M, K, N);
+    if (st != SWIGLU_OK) return st;
+    if (!dW1 != !dW2) return SWIGLU_ERR_NULL_POINTER;   // both weight gradients, or none
+    if (M == 0) {
+        uint16_t* dW[2] = {dW1, dW2};
+        const int64_t elems[2] = {K * N, K * N};
+        if (dW1 && overlap(range_of(dW1, 2 * K * N), range_of(dW2, 2 * K * N))) return SWIGLU_ERR_ALIASING;
+        return empty_batch(dW, elems, 2, (hipStream_t)stream);
+    }
+    Buffers b;
+    b.in(dY, M * N); b.in(A, M * K); b.in(W1, K * N); b.in(W2, K * N);
+    b.kept(codes, scales, M, N, false);
+    if (dA) b.out(dA, M * K);
+    if (dW1) { b.out(dW1, K * N); b.out(dW2, K * N); }
+    if (workspace) b.out(workspace, (int64_t)(workspace_bytes / 2));
+    if ((st = b.check()) != SWIGLU_OK) return st;
+    const Passes p = plan_backward(-1, dA, dW1, M, K, N, cu_count_now());
+    if (!workspace || workspace_bytes < (size_t)(d_bytes(M, N) + p.part_bytes())) return SWIGLU_ERR_WORKSPACE;
+    const Call c{M, K, N, (hipStream_t)stream, (uint16_t*)workspace, (float*)((char*)workspace + d_bytes(M, N))};
+    hipError_t e = run_kept<swt::KEPT_D>(codes, scales, dY, c.D, nullptr, M, N, c.s);
+    if (e == hipSuccess && (dA || dW1)) e = run_gradients(c, p.l[p.n - 1], A, W1, W2, dA, dW1, dW2);
+    return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+swiglu_status swiglu_mlp_train_backward_int8(const swiglu_bf16* dZ, const swiglu_bf16* A, const swiglu_bf16* W1,
+                                             const swiglu_bf16* W2, const swiglu_bf16* W3, const int8_t* codes,
+                                             const swiglu_bf16* scales, swiglu_bf16* dA, swiglu_bf16* dW1,
+                                             swiglu_bf16* dW2, swiglu_bf16* dW3, int64_t M, int64_t K, int64_t N,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    swiglu_status st = check_train_shape(M, K, N);
+    if (st != SWIGLU_OK) return st;
+    if (!dW1 != !dW2 || !dW1 != !dW3) return SWIGLU_ERR_NULL_POINTER;   // the three weight gradients, or none
+    if (M == 0) {
+        uint16_t* dW[3] = {dW1, dW2, dW3};
+        const int64_t elems[3] = {K * N, K * N, K * N};
+        for (int i = 0; dW1 && i < 3; ++i)
+            for (int j = 0; j < i; ++j)
+                if (overlap(range_of(dW[i], 2 * K * N), range_of(dW[j], 2 * K * N))) return SWIGLU_ERR_ALIASING;
+        return empty_batch(dW, elems, 3, (hipStream_t)stream);
+    }
+    Buffers b;
+    b.in(dZ, M * K); b.in(A, M * K); b.in(W1, K * N); b.in(W2, K * N); b.in(W3, K * N);
+    b.kept(codes, scales, M, N, false);
+    if (dA) b.out(dA, M * K);
+    if (dW1) { b.out(dW1, K * N); b.out(dW2, K * N); b.out(dW3, K * N); }
+    if (workspace) b.out(workspace, (int64_t)(workspace_bytes / 2));
+    if ((st = b.check()) != SWIGLU_OK) return st;
+    const Passes p = plan_backward(D_DY8, dA, dW1, M, K, N, cu_count_now());
+    const int64_t before = d_bytes(M, N) + (dW1 ? y_bytes(M, N) : 0);
+    if (!workspace || workspace_bytes < (size_t)(before + p.part_bytes())) return SWIGLU_ERR_WORKSPACE;
+    const Call c{M, K, N, (hipStream_t)stream, (uint16_t*)workspace, (float*)((char*)workspace + before)};
+    uint16_t* const Y = (uint16_t*)((char*)workspace + d_bytes(M, N));
+    swt::GemmArgs a{};
+    a.A0 = dZ; a.lda = K;
+    a.B0 = W3; a.ldb = K;
+    a.rows = (int)M; a.cols = (int)N;
+    a.kseg = (int)K; a.segs = 1;
+    a.C0 = c.D; a.E0 = (const uint16_t*)codes; a.E1 = scales;
+    const swt::GemmArgs dw3 = dw_args(c, Y, N, dZ, K, K, dW3, dW3);
+    // dW3's operand, before the launch that it shares with dY
+    hipError_t e = dW1 ? run_kept<swt::KEPT_Y>(codes, scales, nullptr, Y, nullptr, M, N, c.s) : hipSuccess;
+    if (e == hipSuccess) e = run_launch(p.l[0], a, dw3, c.part, c.s);
     if (e == hipSuccess && (dA || dW1)) e = run_gradients(c, p.l[p.n - 1], A, W1, W2, dA, dW1, dW2);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
 }

@@ -46,7 +46,9 @@ enum Epilogue : int {
     EP_STORE = 0,   // C0 (columns < n0_cols) or C1, bf16
     EP_KEEP = 1,    // dual: Y = SiLU(x) y, G = x, U = y
     EP_DUAL_D = 2,  // dual: D from dY and the recomputed G = x, U = y
-    EP_DY_D = 3     // x = dY: D from it and the kept G and U
+    EP_DY_D = 3,    // x = dY: D from it and the kept G and U
+    EP_KEEP8 = 4,   // dual: Y = SiLU(x) y, G = x and U = y kept as int8
+    EP_DY_D8 = 5    // x = dY: D from it and G and U kept as int8
 };
 
 struct GemmArgs {
@@ -66,10 +68,10 @@ struct GemmArgs {
     float* part;           // the parts' sums, [split][rest tile]
     // epilogue operands
     uint16_t* C0;          // STORE: columns below n0_cols (row length ldc); KEEP: Y; D kinds: D
-    uint16_t* C1;          // STORE: the other columns; KEEP: G
-    uint16_t* C2;          // KEEP: U
-    const uint16_t* E0;    // DUAL_D: dY; DY_D: G
-    const uint16_t* E1;    // DY_D: U
+    uint16_t* C1;          // STORE: the other columns; KEEP: G; KEEP8: codes
+    uint16_t* C2;          // KEEP: U; KEEP8: scales
+    const uint16_t* E0;    // DUAL_D: dY; DY_D: G; DY_D8: codes
+    const uint16_t* E1;    // DY_D: U; DY_D8: scales
     int n0_cols, ldc;
 };
 
@@ -224,6 +226,110 @@ __device__ __forceinline__ void block_load(const BlockAt& b, Rsrc c, long long l
     rows_to_block(in, v);
 }
 
+// ---------------------------------------------------------------------------
+// Gate and Up kept as int8, a bf16 scale for 32 columns of a row (one MFMA block's
+// row: the two lanes that hold it find its largest magnitude with one exchange).
+//   codes  [rows][groups][2][32]: a group's Gate codes, then its Up codes, so that
+//          a block's row is 64 bytes in one place; groups = ceil(cols / 32), columns
+//          past the last are 0
+//   scales [groups][rows][2]: a word holds Gate's (low) and Up's, and 32 rows of a
+//          block 128 bytes
+// s = max |x| / 127 rounded up to bf16 (so that no code passes 127), at least 2^-126;
+// code = round(x / s).  In bf16 a scale costs a coarser step by at most 2^-7 of it and
+// saves 1/16 byte an element.  A group that holds an infinity or NaN has the scale NaN,
+// and what is computed from it is NaN.
+// ---------------------------------------------------------------------------
+constexpr int GROUP = 32;
+// the larger magnitude as bits: infinities above all numbers, NaN above them
+__device__ __forceinline__ unsigned max_abs(unsigned m, float x) {
+    return max(m, __builtin_bit_cast(unsigned, x) & 0x7FFFFFFFu);
+}
+__device__ __forceinline__ unsigned max_halves(unsigned m) {
+    const auto r = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return max((unsigned)r[0], (unsigned)r[1]);
+}
+// the scale's bf16 bits from the largest magnitude's fp32 bits
+__device__ __forceinline__ unsigned kept_scale(unsigned top) {
+    const float t = __builtin_bit_cast(float, top) / 127.0f;
+    const unsigned up = (__builtin_bit_cast(unsigned, t) + 0xFFFFu) >> 16;
+    return top >= 0x7F800000u ? 0x7FC0u : max(up, 0x0080u);
+}
+// 16 values of a block's row (layout of its sums) to codes and their scale; q8: whether
+// the columns 8q .. 8q + 7 exist.  x / s as x times v_rcp_f32 of s: a code differs from
+// the exact quotient's only within 2^-16 of a tie.
+__device__ __forceinline__ unsigned block_codes(float (&x)[16], const bool (&q8)[4], unsigned (&d)[4]) {
+    unsigned top = 0u;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        if (!q8[r >> 2]) x[r] = 0.0f;
+        top = max_abs(top, x[r]);
+    }
+    const unsigned s = kept_scale(max_halves(top));
+    const float inv = __builtin_amdgcn_rcpf(__builtin_bit_cast(float, s << 16));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        unsigned b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = __builtin_bit_cast(unsigned, x[4 * q + e] * inv + ROUND_BITS);
+        d[q] = s == 0x7FC0u ? 0u : low_bytes(b[0], b[1], b[2], b[3]);
+    }
+    return s;
+}
+// Codes of columns 8q + 4 (l >> 5) + 0 .. 3 in word q to 16 adjacent columns from
+// 16 (l >> 5) on, and back (in the order of out's words).
+__device__ __forceinline__ u32x4 codes_to_row(unsigned (&d)[4]) {
+    swap32(d[0], d[2]);
+    swap32(d[1], d[3]);
+    return u32x4{d[0], d[2], d[1], d[3]};
+}
+__device__ __forceinline__ void row_to_codes(u32x4 v, unsigned (&d)[4]) {
+    d[0] = v[0];
+    d[2] = v[1];
+    d[1] = v[2];
+    d[3] = v[3];
+    swap32(d[0], d[2]);
+    swap32(d[1], d[3]);
+}
+// four codes times their scale: bytes as 0 .. 255 and one exact fma
+__device__ __forceinline__ void code_values(unsigned d, float s, float* v) {
+    const unsigned u = d ^ 0x80808080u;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = fmaf((float)((u >> (8 * e)) & 255u), s, -128.0f * s);
+}
+// A block of kept Gate and Up seen from its group's codes and scales of the tile's first
+// row: byte offsets of the lane's Gate codes, Up codes and scales of row r0 + (l & 31),
+// past the end where it has none (selected, never summed: a sum would wrap around).
+struct KeptAt {
+    Rsrc codes, scales;
+    uint32_t gate, up, scale;
+};
+__device__ __forceinline__ KeptAt kept_at(const GemmArgs& p, const uint16_t* codes, const uint16_t* scales, int m0,
+                                          int n0, int r0, int c0, int lane) {
+    const int groups = (p.cols + GROUP - 1) / GROUP;
+    const int g = (n0 + c0) / GROUP, r = r0 + (lane & 31);
+    const bool in = g < groups && m0 + r < p.rows;
+    KeptAt k;
+    k.codes = corner(codes, 32 * (long long)groups, m0, 32 * g);
+    k.scales = corner(scales, 2 * (long long)p.rows, g, 2 * m0);
+    const uint32_t at = (uint32_t)(r * groups * 64 + 16 * (lane >> 5));
+    k.gate = in ? at : OFF_NONE;
+    k.up = in ? at + 32 : OFF_NONE;
+    k.scale = in ? (uint32_t)r * 4 : OFF_NONE;
+    return k;
+}
+__device__ __forceinline__ void kept_load(const KeptAt& k, float (&g)[16], float (&u)[16]) {
+    const u32x4 cg = __builtin_amdgcn_raw_buffer_load_b128(k.codes, k.gate, 0, 0);
+    const u32x4 cu = __builtin_amdgcn_raw_buffer_load_b128(k.codes, k.up, 0, 0);
+    const unsigned s = __builtin_amdgcn_raw_buffer_load_b32(k.scales, k.scale, 0, 0);
+    unsigned d[4];
+    row_to_codes(cg, d);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) code_values(d[q], __builtin_bit_cast(float, s << 16), g + 4 * q);
+    row_to_codes(cu, d);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) code_values(d[q], __builtin_bit_cast(float, s & 0xFFFF0000u), u + 4 * q);
+}
+
 // The epilogue of the block at row r0, column c0 of the tile at (m0, n0) (x;
 // dual: and y).
 template <int EPI>
@@ -259,14 +365,33 @@ __device__ __forceinline__ void finish_block(const GemmArgs& p, int m0, int n0, 
 #pragma unroll
         for (int r = 0; r < 16; ++r) v[r] = y[r];
         block_store(b, corner(p.C2, p.cols, m0, n0), p.cols, v);
+    } else if constexpr (EPI == EP_KEEP8) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = silu_f(x[r]) * y[r];
+        block_store(b, corner(p.C0, p.cols, m0, n0), p.cols, v);
+        const KeptAt k = kept_at(p, p.C1, p.C2, m0, n0, r0, c0, lane);
+        bool q8[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) q8[q] = n0 + c0 + 8 * q < p.cols;
+        unsigned d[4];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = x[r];
+        unsigned s = block_codes(v, q8, d);
+        __builtin_amdgcn_raw_buffer_store_b128(codes_to_row(d), k.codes, k.gate, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) v[r] = y[r];
+        s |= block_codes(v, q8, d) << 16;
+        __builtin_amdgcn_raw_buffer_store_b128(codes_to_row(d), k.codes, k.up, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(s, k.scales, lane < 32 ? k.scale : OFF_NONE, 0, 0);
     } else {
         float dg[16], du[16];
-        block_load(b, corner(p.E0, p.cols, m0, n0), p.cols, v);
+        if constexpr (EPI == EP_DY_D8) kept_load(kept_at(p, p.E0, p.E1, m0, n0, r0, c0, lane), v, w);
+        else block_load(b, corner(p.E0, p.cols, m0, n0), p.cols, v);
         if constexpr (EPI == EP_DUAL_D) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) silu_grad(v[r], x[r], y[r], dg[r], du[r]);
         } else {
-            block_load(b, corner(p.E1, p.cols, m0, n0), p.cols, w);
+            if constexpr (EPI == EP_DY_D) block_load(b, corner(p.E1, p.cols, m0, n0), p.cols, w);
 #pragma unroll
             for (int r = 0; r < 16; ++r) silu_grad(x[r], v[r], w[r], dg[r], du[r]);
         }
@@ -757,6 +882,72 @@ __global__ __launch_bounds__(256) void dgate_kernel(const uint16_t* __restrict__
         uint16_t* d = D + (size_t)m * 2 * N + n;
         st16(d, pack8(dg));
         st16(d + N, pack8(du));
+    }
+}
+
+// What is computed from Gate and Up kept as int8, element by element: D = [dG | dU]
+// from dY, Y = SiLU(G) U, or G and U themselves.  A thread has half a group (16
+// columns) of four rows: their scales lie in one 16-byte piece, and the rows' loads go
+// out together.  Bound by HBM.
+enum KeptUse : int { KEPT_D = 0, KEPT_Y = 1, KEPT_GU = 2 };
+template <int USE>
+__global__ __launch_bounds__(256) void kept_kernel(const uint8_t* __restrict__ codes,
+                                                   const uint32_t* __restrict__ scales,
+                                                   const uint16_t* __restrict__ dY, uint16_t* __restrict__ C0,
+                                                   uint16_t* __restrict__ C1, int M, int N, long long units) {
+    constexpr int ROWS = 4;
+    const int groups = (N + GROUP - 1) / GROUP, halves = 2 * groups;
+    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < units; t += (long long)gridDim.x * 256) {
+        const int m0 = (int)(t / halves) * ROWS, hg = (int)(t % halves);
+        const int g = hg >> 1, n = hg * 16;
+        if (n >= N) continue;
+        const bool second = n + 8 < N;   // the half group's columns 8 .. 15
+        u32x4 cg[ROWS], cu[ROWS], dy[ROWS][2];
+        unsigned s[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int m = min(m0 + r, M - 1);
+            const uint8_t* c = codes + ((size_t)m * groups + g) * 64 + 16 * (hg & 1);
+            cg[r] = *reinterpret_cast<const u32x4*>(c);
+            cu[r] = *reinterpret_cast<const u32x4*>(c + 32);
+            s[r] = scales[(size_t)g * M + m];
+            if constexpr (USE == KEPT_D) {
+                const uint16_t* d = dY + (size_t)m * N + n;
+                dy[r][0] = ld16(d);
+                dy[r][1] = second ? ld16(d + 8) : u32x4{0u, 0u, 0u, 0u};
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int m = m0 + r;
+            if (m >= M) break;
+            const float sg = __builtin_bit_cast(float, s[r] << 16), su = __builtin_bit_cast(float, s[r] & 0xFFFF0000u);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float gv[8], uv[8], x[8], y[8];
+                code_values(cg[r][2 * h], sg, gv);
+                code_values(cg[r][2 * h + 1], sg, gv + 4);
+                code_values(cu[r][2 * h], su, uv);
+                code_values(cu[r][2 * h + 1], su, uv + 4);
+                if constexpr (USE == KEPT_D) {
+                    float d[8];
+                    unpack8(dy[r][h], d);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) silu_grad(d[e], gv[e], uv[e], x[e], y[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = USE == KEPT_Y ? silu_f(gv[e]) * uv[e] : gv[e];
+                        y[e] = uv[e];
+                    }
+                }
+                if (h == 1 && !second) continue;
+                const size_t at = (size_t)m * (USE == KEPT_D ? 2 * (size_t)N : (size_t)N) + n + 8 * h;
+                st16(C0 + at, pack8(x));
+                if constexpr (USE == KEPT_D) st16(C0 + at + N, pack8(y));
+                if constexpr (USE == KEPT_GU) st16(C1 + at, pack8(y));
+            }
+        }
     }
 }
 

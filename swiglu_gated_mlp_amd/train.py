@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (_check, _dev_bf16, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
+from . import (_check, _dev_bf16, _empty, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
                swiglu_gemm_bf16)
 
 _need: dict = {}
@@ -135,6 +135,113 @@ def swiglu_mlp_train_backward(dZ: torch.Tensor, A: torch.Tensor, W1: torch.Tenso
 
 
 # ---------------------------------------------------------------------------
+# Gate and Up kept as int8
+# ---------------------------------------------------------------------------
+def swiglu_train_workspace_bytes_int8(M: int, K: int, N: int) -> int:
+    return int(lib().swiglu_train_workspace_bytes_int8(M, K, N))
+
+
+def _dev_int8(t, name: str) -> int:
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.int8 and t.is_contiguous():
+        return t.data_ptr()
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8:
+        raise TypeError("%s must be an int8 tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _kept_shapes(codes, scales, M: int, N: int):
+    groups = (N + 31) // 32
+    _shape(codes, (M, groups, 2, 32), "codes")
+    _shape(scales, (groups, M, 2), "scales")
+    return groups
+
+
+def swiglu_train_forward_int8(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, Y: torch.Tensor | None = None,
+                              codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, workspace=None,
+                              stream=None):
+    """swiglu_train_forward with G and U kept as int8: returns (Y, codes, scales), Y
+    bf16 [M,N], codes int8 [M, groups, 2, 32] (a group of 32 columns' Gate, then its
+    Up), scales bf16 [groups, M, 2], groups = ceil(N / 32)."""
+    M, K, N = _weights(A, W1, W2)
+    _shape(Y, (M, N), "Y")
+    groups = _kept_shapes(codes, scales, M, N)
+    a, w1, w2 = _dev_bf16(A, "A"), _dev_bf16(W1, "W1"), _dev_bf16(W2, "W2")
+    s = _stream(stream)
+    Y = _new((M, N), A.device, s, stream) if Y is None else Y
+    if codes is None:
+        codes = _empty((M, groups, 2, 32), torch.int8, A.device, s)
+    scales = _new((groups, M, 2), A.device, s, stream) if scales is None else scales
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, A.device), A.device, s)
+    st = lib().swiglu_train_forward_int8(a, w1, w2, _dev_bf16(Y, "Y"), _dev_int8(codes, "codes"),
+                                         _dev_bf16(scales, "scales"), M, K, N, _ptr(ws), ws_bytes, s)
+    _check("swiglu_train_forward_int8", st)
+    return Y, codes, scales
+
+
+def swiglu_dequantize_kept_int8(codes: torch.Tensor, scales: torch.Tensor, N: int, G: torch.Tensor | None = None,
+                                U: torch.Tensor | None = None, stream=None):
+    """(G, U) bf16 [M,N] of what swiglu_train_forward_int8 kept."""
+    M = codes.shape[0]
+    _kept_shapes(codes, scales, M, N)
+    for t, name in ((G, "G"), (U, "U")):
+        _shape(t, (M, N), name)
+    c, sc = _dev_int8(codes, "codes"), _dev_bf16(scales, "scales")
+    s = _stream(stream)
+    G = _new((M, N), codes.device, s, stream) if G is None else G
+    U = _new((M, N), codes.device, s, stream) if U is None else U
+    st = lib().swiglu_dequantize_kept_int8(c, sc, _dev_bf16(G, "G"), _dev_bf16(U, "U"), M, N, s)
+    _check("swiglu_dequantize_kept_int8", st)
+    return G, U
+
+
+def swiglu_train_backward_int8(dY: torch.Tensor, A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
+                               codes: torch.Tensor, scales: torch.Tensor, dA: torch.Tensor | None = None,
+                               dW1: torch.Tensor | None = None, dW2: torch.Tensor | None = None, need_dA: bool = True,
+                               need_dW: bool = True, workspace=None, stream=None):
+    """swiglu_train_backward from codes and scales of swiglu_train_forward_int8."""
+    M, K, N = _weights(A, W1, W2)
+    _shape(dY, (M, N), "dY")
+    _kept_shapes(codes, scales, M, N)
+    ins = [_dev_bf16(t, n) for t, n in ((dY, "dY"), (A, "A"), (W1, "W1"), (W2, "W2"))]
+    ins += [_dev_int8(codes, "codes"), _dev_bf16(scales, "scales")]
+    s = _stream(stream)
+    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
+    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, A.device), A.device, s)
+    outs = [0 if t is None else _dev_bf16(t, n) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
+    st = lib().swiglu_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
+    _check("swiglu_train_backward_int8", st)
+    return dA, dW1, dW2
+
+
+def swiglu_mlp_train_backward_int8(dZ: torch.Tensor, A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor,
+                                   W3: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                                   dA: torch.Tensor | None = None, dW1: torch.Tensor | None = None,
+                                   dW2: torch.Tensor | None = None, dW3: torch.Tensor | None = None,
+                                   need_dA: bool = True, need_dW: bool = True, workspace=None, stream=None):
+    """swiglu_mlp_train_backward from codes and scales of swiglu_train_forward_int8 (Y
+    is computed from them)."""
+    M, K, N = _weights(A, W1, W2)
+    _shape(dZ, (M, K), "dZ")
+    _shape(W3, (N, K), "W3")
+    _kept_shapes(codes, scales, M, N)
+    ins = [_dev_bf16(t, n) for t, n in ((dZ, "dZ"), (A, "A"), (W1, "W1"), (W2, "W2"), (W3, "W3"))]
+    ins += [_dev_int8(codes, "codes"), _dev_bf16(scales, "scales")]
+    s = _stream(stream)
+    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
+    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
+    dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), A.device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes_int8, M, K, N, A.device), A.device, s)
+    outs = [0 if t is None else _dev_bf16(t, n)
+            for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"), (dW3, "dW3"))]
+    st = lib().swiglu_mlp_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
+    _check("swiglu_mlp_train_backward_int8", st)
+    return dA, dW1, dW2, dW3
+
+
+# ---------------------------------------------------------------------------
 # autograd
 # ---------------------------------------------------------------------------
 def _rows(t: torch.Tensor) -> torch.Tensor:
@@ -143,13 +250,13 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
 
 class _Swiglu(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, A, W1, W2, recompute):
+    def forward(ctx, A, W1, W2, recompute, keep):
         rows = _rows(A)
         if recompute:
             Y, kept = swiglu_fused(rows, W1, W2), ()
         else:
-            Y, *kept = swiglu_train_forward(rows, W1, W2)
-        ctx.shape = A.shape
+            Y, *kept = (swiglu_train_forward_int8 if keep == "int8" else swiglu_train_forward)(rows, W1, W2)
+        ctx.shape, ctx.keep = A.shape, keep
         ctx.save_for_backward(rows, W1, W2, *kept)
         return Y.view(*A.shape[:-1], W1.shape[1])
 
@@ -158,41 +265,59 @@ class _Swiglu(torch.autograd.Function):
     def backward(ctx, dY):
         rows, W1, W2, *kept = ctx.saved_tensors
         need_a, need_1, need_2 = ctx.needs_input_grad[:3]
-        dA, dW1, dW2 = swiglu_train_backward(_rows(dY), rows, W1, W2, *kept, need_dA=need_a,
-                                             need_dW=need_1 or need_2)
-        return (dA.view(ctx.shape) if need_a else None, dW1 if need_1 else None, dW2 if need_2 else None, None)
+        call = swiglu_train_backward_int8 if ctx.keep == "int8" else swiglu_train_backward
+        dA, dW1, dW2 = call(_rows(dY), rows, W1, W2, *kept, need_dA=need_a, need_dW=need_1 or need_2)
+        return (dA.view(ctx.shape) if need_a else None, dW1 if need_1 else None, dW2 if need_2 else None, None, None)
 
 
 class _SwigluMlp(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, A, W1, W2, W3):
+    def forward(ctx, A, W1, W2, W3, keep):
         rows = _rows(A)
-        Y, G, U = swiglu_train_forward(rows, W1, W2)
+        if keep == "int8":
+            Y, *kept = swiglu_train_forward_int8(rows, W1, W2)
+        else:
+            Y, G, U = swiglu_train_forward(rows, W1, W2)
+            kept = (G, U, Y)
         Z = swiglu_gemm_bf16(Y, W3)
-        ctx.shape = A.shape
-        ctx.save_for_backward(rows, W1, W2, W3, G, U, Y)
+        ctx.shape, ctx.keep = A.shape, keep
+        ctx.save_for_backward(rows, W1, W2, W3, *kept)
         return Z.view(*A.shape[:-1], W3.shape[1])
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dZ):
-        need = ctx.needs_input_grad
-        grads = swiglu_mlp_train_backward(_rows(dZ), *ctx.saved_tensors, need_dA=need[0], need_dW=any(need[1:]))
+        need = ctx.needs_input_grad[:4]
+        call = swiglu_mlp_train_backward_int8 if ctx.keep == "int8" else swiglu_mlp_train_backward
+        grads = call(_rows(dZ), *ctx.saved_tensors, need_dA=need[0], need_dW=any(need[1:]))
         dA = grads[0].view(ctx.shape) if need[0] else None
-        return (dA,) + tuple(g if n else None for g, n in zip(grads[1:], need[1:]))
+        return (dA,) + tuple(g if n else None for g, n in zip(grads[1:], need[1:])) + (None,)
 
 
-def swiglu(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, recompute: bool = False) -> torch.Tensor:
-    """Differentiable Y = SiLU(A @ W1) * (A @ W2), A [..., K].  Keeps Gate and Up
-    (4 M N bytes) for the backward pass, or (recompute) computes them again in
+def _keep(keep: str) -> str:
+    if keep not in ("bf16", "int8"):
+        raise ValueError("keep must be \"bf16\" or \"int8\" (got %r)" % (keep,))
+    return keep
+
+
+def swiglu(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, recompute: bool = False,
+           keep: str = "bf16") -> torch.Tensor:
+    """Differentiable Y = SiLU(A @ W1) * (A @ W2), A [..., K].  Keeps Gate and Up for
+    the backward pass, as they are (4 M N bytes) or (keep "int8") in 8 bits with a
+    scale for 32 columns of a row (2.125 M N), or (recompute) computes them again in
     it for 4 M K N more operations.  Without recompute they are written in every
     call, also where no gradient is wanted (swiglu_fused writes Y alone)."""
-    return _Swiglu.apply(A, W1, W2, recompute)
+    if _keep(keep) == "int8" and recompute:
+        raise ValueError("recompute keeps nothing: keep is \"bf16\" with it")
+    return _Swiglu.apply(A, W1, W2, recompute, keep)
 
 
-def swiglu_mlp(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, W3: torch.Tensor) -> torch.Tensor:
+def swiglu_mlp(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, W3: torch.Tensor,
+               keep: str = "bf16") -> torch.Tensor:
     """Differentiable gated MLP block Z = (SiLU(A @ W1) * (A @ W2)) @ W3, A [..., K],
-    W3 [N,K] (any [N, ...] where no gradient is wanted)."""
+    W3 [N,K] (any [N, ...] where no gradient is wanted).  Keeps Gate, Up and Y for the
+    backward pass (6 M N bytes), or (keep "int8") Gate and Up in 8 bits (2.125 M N)."""
+    _keep(keep)
     if torch.is_grad_enabled() and any(t.requires_grad for t in (A, W1, W2, W3)):
         _shape(W3, (W1.shape[1], A.shape[-1]), "W3")
-    return _SwigluMlp.apply(A, W1, W2, W3)
+    return _SwigluMlp.apply(A, W1, W2, W3, keep)
