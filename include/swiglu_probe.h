@@ -51,6 +51,13 @@ typedef enum {
 } swiglu_train_launch;
 int swiglu_probe_train_plan(int launch, int64_t M, int64_t K, int64_t N, int32_t plan[12]);
 
+/* How an int8 product is run at (M,K,N) on the current device (host call; gemm: 0 the
+ * fused product, 1 one weight): plan receives the kernel (0 decode, 1 few rows, 2 many
+ * rows), a tile's rows, its packed weight rows and the parts that K is split into.
+ * Returns 1, or 0 for a shape that the calls refuse, M == 0 or plan NULL. */
+int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N,
+                           int32_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

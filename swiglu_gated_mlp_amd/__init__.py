@@ -100,6 +100,7 @@ SIGNATURES = {
     # include/swiglu_probe.h (diagnostic ceilings)
     "swiglu_probe_mfma": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_read": ([_P, ctypes.c_size_t, _P, ctypes.c_int, _P], ctypes.c_int),
+    "swiglu_probe_int8_plan": ([ctypes.c_int, _I64, _I64, _I64, _P], ctypes.c_int),
     "swiglu_probe_train_plan": ([ctypes.c_int, _I64, _I64, _I64, _P], ctypes.c_int),
 }
 
@@ -729,6 +730,16 @@ def swiglu_probe_train_plan(launch: str, M: int, K: int, N: int) -> list:
         raise ValueError("invalid shape M=%d K=%d N=%d" % (M, K, N))
     keys = ("rows", "cols", "whole", "rest", "splits", "blocks")
     return [dict(zip(keys, out[6 * i:6 * i + 6])) for i in range(n)]
+
+
+def swiglu_probe_int8_plan(gemm: bool, M: int, K: int, N: int) -> dict:
+    """How an int8 product (gemm: of one weight) is run at (M,K,N): the kernel
+    ("decode", "narrow", "stream"), a tile's rows and packed weight rows, the parts
+    that K is split into."""
+    out = (ctypes.c_int32 * 4)()
+    if lib().swiglu_probe_int8_plan(int(bool(gemm)), M, K, N, out) == 0:
+        raise ValueError("invalid shape M=%d K=%d N=%d" % (M, K, N))
+    return dict(kernel=("decode", "narrow", "stream")[out[0]], rows=out[1], cols=out[2], splits=out[3])
 
 
 # training (gradients and differentiable forms of the product and the block)

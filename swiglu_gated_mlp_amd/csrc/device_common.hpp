@@ -100,6 +100,50 @@ __device__ __forceinline__ s16x4 ds_read_tr16(const uint16_t* lds) {
         (lds_s16x4_ptr)((__attribute__((address_space(3))) uint16_t*)(lds)));
 }
 
+// ---------------------------------------------------------------------------
+// The epilogue of one 32 x 32 MFMA block without LDS.  A lane holds 16 sums of
+// row l & 31: v[4q + e] is column 8q + 4 (l >> 5) + e.  Two exchanges between
+// lanes (v_permlane32_swap, v_permlane16_swap) turn the block, packed to bf16,
+// into 16 bytes a lane with four lanes on 64 adjacent bytes of a row:
+//   out[h]: row 16h + (l & 15), columns 8c .. 8c + 7, c = 2 ((l >> 4) & 1) + (l >> 5).
+// They are their own inverse.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(unsigned& a, unsigned& b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+
+// d[q][w]: packed columns 8q + 4 (l >> 5) + 2w, + 1
+__device__ __forceinline__ void block_to_rows(unsigned (&d)[4][2], u32x4 (&out)[2]) {
+#pragma unroll
+    for (int q = 0; q < 4; q += 2)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) swap32(d[q][w], d[q + 1][w]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) swap16(d[q][w], d[q + 2][w]);
+    out[0] = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
+    out[1] = u32x4{d[2][0], d[2][1], d[3][0], d[3][1]};
+}
+constexpr int RSRC_END = 0x7FFFFFF0;          // every offset of a valid lane is below
+constexpr uint32_t OFF_NONE = 0xFFFFFFF0u;    // past every descriptor's end
+// A matrix seen from a tile's corner, for the block epilogue: accesses of lanes
+// past its rows or columns have offsets past the descriptor's end, where loads
+// give 0 and stores are dropped, so the epilogue has no branches (with branches
+// the compiler moved all sums of a wave out of the accumulation registers at
+// once and spilled).
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc corner(const uint16_t* c, long long ld, int m0, int n0) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(c + (size_t)m0 * ld + n0), 0, RSRC_END, 0x00020000);
+}
+
 // s_waitcnt immediate: vector-memory count vm, LDS/scalar count lgkm (no
 // export wait)
 constexpr int waitcnt_imm(int vm, int lgkm) {

@@ -140,8 +140,8 @@ __device__ __forceinline__ float scaled(int sum, float col, float row) { return 
 // columns of one token per 32x32 accumulator block, so it writes 16 bytes of
 // Gate and 16 bytes of Up per block.  Rows >= M and columns >= N are skipped.
 // ---------------------------------------------------------------------------
-template <int TM, int TN, class Acc>
-__device__ __forceinline__ void store_partials(const Acc (&acc)[2][TM][TN], float* part, int split,
+template <int TM, int TN>
+__device__ __forceinline__ void store_partials(const f32x16 (&acc)[2][TM][TN], float* part, int split,
                                                int M, int N, int row0, int col0, int lane) {
     float* base = part + (size_t)split * M * (2 * (size_t)N);
 #pragma unroll
@@ -158,10 +158,8 @@ __device__ __forceinline__ void store_partials(const Acc (&acc)[2][TM][TN], floa
                 f32x4 g, u;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    // int32 sums keep their bits
-                    const auto gs = acc[0][i][j][4 * q + e], us = acc[1][i][j][4 * q + e];
-                    g[e] = __builtin_bit_cast(float, gs);
-                    u[e] = __builtin_bit_cast(float, us);
+                    g[e] = acc[0][i][j][4 * q + e];
+                    u[e] = acc[1][i][j][4 * q + e];
                 }
                 *reinterpret_cast<f32x4*>(prow + n) = g;
                 *reinterpret_cast<f32x4*>(prow + N + n) = u;
@@ -909,7 +907,8 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
                                                      int total, const LoraArgs* la = nullptr) {
     static_assert(!(LORA != 0 && (SPLIT || IL || F8 || SEQ)), "adapters: bf16 per-tile or single-weight pack, whole K");
     static_assert(!(GEMM && (IL || F8 || SEQ)), "plain GEMM: single-weight pack");
-    static_assert(!(I8 && (IL || F8 || SEQ || LORA != 0)), "int8 operands: per-tile or single-weight pack");
+    static_assert(!(I8 && (SPLIT || IL || F8 || SEQ || LORA != 0 || (PANELS && GEMM))),
+                  "int8 operands: whole K; the fused product also on panels");
     static_assert(!(IL && SPLIT), "the interleaved layout has no split-K schedule");
     static_assert(!(F8 && (IL || SPLIT)), "FP8 operands: per-tile layout, data-parallel only");
     static_assert(!(SEQ && (SPLIT || PANELS || IL || F8)), "sequential order: bf16 per-tile tiles only");
@@ -1364,9 +1363,8 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
             asm volatile("" : "+v"(sl));
 #pragma unroll
             for (int g = 0; g < WT; ++g) {
-                const int u = cur.n0 / 32 + wave;
-                const int tc = GH ? (u >> 1) * 32 : u * 32;   // (tiled) column of the wave's first
-                const int n = GEMM ? (tc >> 7) * PACK_ROWS + PACK_BN * (GH ? (u & 1) : g) + (tc & (PACK_BN - 1)) : tc;
+                const int tc = cur.n0 + wave * 32;   // (tiled) column of the wave's first
+                const int n = GEMM ? (tc >> 7) * PACK_ROWS + PACK_BN * g + (tc & (PACK_BN - 1)) : tc;
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     cs[g][q] = scales4(GEMM || g == 0 ? p.s1 : p.s2, n + 8 * q + 4 * (sl >> 5), N);
@@ -1682,11 +1680,12 @@ struct DecodeArgs {
 // I8: int8 operands (see Acc16; K and KB count pairs of int8).
 // Lora: LoraArgs, or nothing.  With it, each row's low-rank adapter is added to
 // the summed Gate and Up (or plain) values before the epilogue.
+// WAVES: 8 halves the steps of a long contraction to few columns, where the grid
+// leaves a workgroup a CU.
 template <int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false, bool I8 = false,
-          class... Lora>
-__global__ __launch_bounds__(256) void decode_kernel(DecodeArgs p, Lora... lora) {
+          int WAVES = 4, class... Lora>
+__global__ __launch_bounds__(64 * WAVES) void decode_kernel(DecodeArgs p, Lora... lora) {
     static_assert(GEMM || !HALF, "HALF splits the single-weight product only");
-    constexpr int WAVES = 4;
     constexpr int NH = HALF ? 1 : 2;    // weight halves per workgroup
     constexpr int AROWS = 16 * MT;      // activation rows per K block
     static_assert(!I8 || sizeof...(Lora) == 0, "adapters: bf16 operands");

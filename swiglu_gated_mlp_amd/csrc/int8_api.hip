@@ -1,9 +1,13 @@
 // Host side of the int8 products (swiglu_*_int8; include/swiglu.h): argument
 // checks, plans and launches.  Every check runs before the first HIP call.
 #include "swiglu.h"
+#include "swiglu_probe.h"
 
 #include "int8_kernels.hpp"
+#include "int8_narrow.hpp"
 #include "launch.hpp"
+
+#include <cmath>
 
 using namespace swh;
 using namespace swl;
@@ -51,20 +55,127 @@ struct Buffers {
     }
 };
 
-// The packs are those of bf16 weights of K / 2 rows, and so are the plans.
+// The packs are those of bf16 weights of K / 2 rows, and so are the streaming plans.
 int64_t packed_bytes_int8(int64_t K, int64_t N) { return 2 * packed_elems(K / 2, N); }
 int64_t gemm_packed_bytes_int8(int64_t K, int64_t N) { return 2 * gemm_packed_elems(K / 2, N); }
 
 // Products whose activations reach 2 GiB run as row chunks, data-parallel.
 bool in_chunks(int64_t M, int64_t K) { return M > stream_rows_limit(K, 1); }
 
-Plan fused_plan_int8(int64_t M, int64_t K, int64_t N) {
-    return make_plan(M, K / 2, N, in_chunks(M, K) ? SWIGLU_VARIANT_DATA_PARALLEL : SWIGLU_VARIANT_AUTO,
-                     cu_count_now());
+// ---------------------------------------------------------------------------
+// Plans.  The weight-streaming decode kernel (up to 64 rows), the tiles and parts of
+// narrow_kernel, or the streaming kernel of many rows, whichever an estimate says is
+// fastest.
+//   The estimates are microseconds of a launch on an idle device with the weights in
+// HBM and the caches full of something else's outputs, and only their order matters.
+// Fitted to this chip over 126 shapes (33 .. 4096 rows, K 896 .. 29568, N 896 .. 29568)
+// with every tile and up to 16 parts: off by 8 % in the root mean square, and the
+// choice costs 2 % over the best on average.
+// ---------------------------------------------------------------------------
+struct Plan8 {
+    enum How { DECODE, NARROW, STREAM } how;
+    int cus;
+    Plan stream;            // STREAM: 256-row tiles, or (panels > 0) one row of them on panels
+    int tile;               // NARROW: index into kNarrow
+    int units, tiles_m, groups, splits, kb_per_split;
+    size_t part_bytes;
+};
+
+// rows and 32-row weight blocks of a workgroup, microseconds outside the stages, and a
+// stage (128 k) on a CU that has one workgroup.
+struct NarrowTile {
+    int bm, blocks;
+    double once, stage;
+};
+constexpr NarrowTile kNarrow[3] = {{128, 8, 9.3, 0.69}, {128, 4, 8.4, 0.48}, {64, 4, 8.6, 0.39}};
+
+// A CU's stages, the weights from HBM and the matrix cores overlap in part.
+double overlapped(double cu, double hbm, double mfma) { return std::sqrt(cu * cu + hbm * hbm + mfma * mfma); }
+
+// work items on the CUs: in rounds, evened out from two on
+double rounds_of(int64_t items, int cus) {
+    return items > 2 * (int64_t)cus ? (double)items / cus : (double)ceil_div(items, cus);
 }
-Plan gemm_plan_int8(int64_t M, int64_t K, int64_t N) {
-    return in_chunks(M, K) ? make_plan(M, K / 2, gemm_tiled_cols(N), SWIGLU_VARIANT_DATA_PARALLEL, cu_count_now())
-                           : gemm_plan(M, K / 2, N);
+
+double narrow_us(const Plan8& p, int64_t K, int64_t M) {
+    const NarrowTile& t = kNarrow[p.tile];
+    const int64_t items = (int64_t)p.tiles_m * p.groups * p.splits;
+    const double rows = (double)p.groups * t.blocks * 32;   // packed
+    return t.once +
+           overlapped(rounds_of(items, p.cus) * p.kb_per_split * t.stage, (rows + M) * K / 7.6e6,
+                      2.0 * p.tiles_m * t.bm * rows * K / 2.95e9) +
+           (p.splits > 1 ? 2.0 + p.part_bytes / 3.1e6 : 0.0);
+}
+
+double stream_us(const Plan& p, int64_t M, int64_t K) {
+    const double rows = p.tiles_n * 256.0;
+    // panels: four to a column tile, a wave each
+    if (p.panels > 0)
+        return 13.0 + overlapped(ceil_div(p.panels, p.cus) * p.KB * 0.42, (rows + M) * K / 12.0e6, 0.0);
+    const int rest = p.tiles % p.cus;
+    const double rounds = p.tiles / p.cus + (rest == 0 ? 0.0 : p.tail_ntiles ? (double)rest / p.cus + 0.25 : 1.0);
+    return 4.3 + overlapped(rounds * (p.KB * 0.93 + 12.7), (rows + M) * K / 6.0e6,
+                            2.0 * p.tiles_m * 256 * rows * K / 3.3e9);
+}
+
+// 33 to 64 rows on the decode kernel (see run_decode)
+double decode_us(bool gemm, int64_t KB, int64_t nt, int cus) {
+    return gemm ? 5.0 + 0.16 * KB * ceil_div(2 * ceil_div(nt, 16), cus) : 5.4 + 0.49 * KB * ceil_div(ceil_div(nt, 32), cus);
+}
+
+// The streaming kernel at any M, without a workspace.
+Plan8 stream_plan(bool gemm, int64_t M, int64_t K, int64_t N) {
+    Plan8 p{};
+    p.how = Plan8::STREAM;
+    p.cus = cu_count_now();
+    if (p.cus <= 0) p.cus = 256;
+    Plan& s = p.stream;
+    s.t = TileCfg{256, 128};
+    s.cus = p.cus;
+    s.KB = (int)ceil_div(K, 128);
+    s.tiles_m = (int)ceil_div(M, 256);
+    s.tiles_n = (int)ceil_div(gemm ? gemm_tiled_cols(N) : N, swk::PACK_BN);
+    s.tiles = s.tiles_m * s.tiles_n;
+    s.tail_ntiles = tail_tiles(s.tiles_m, s.tiles_n, p.cus);
+    s.splits = 1;
+    s.kb_per_split = s.KB;
+    // one row of tiles that leaves CUs idle on a wide product: its panels over all CUs
+    if (!gemm && s.tiles_m == 1 && s.tiles_n < p.cus && 2 * s.tiles_n >= p.cus) s.panels = 4 * s.tiles_n;
+    return p;
+}
+
+Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
+    Plan8 best = stream_plan(gemm, M, K, N);
+    if (in_chunks(M, K)) return best;
+    const int64_t KB = ceil_div(K, 128);
+    double best_us = stream_us(best.stream, M, K);
+    if (M <= 64) {
+        best.how = Plan8::DECODE;
+        if (M <= 32) return best;
+        best_us = decode_us(gemm, KB, gemm ? gemm_tiled_cols(N) : N, best.cus);
+    }
+    static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 16};
+    for (int i = 0; i < 3; ++i) {
+        Plan8 p = best;
+        p.how = Plan8::NARROW;
+        p.tile = i;
+        p.units = (int)(gemm && i == 0 ? 4 * ceil_div(N, swk::PACK_ROWS) : ceil_div(N, 32));
+        p.tiles_m = (int)ceil_div(M, kNarrow[i].bm);
+        p.groups = (int)ceil_div(p.units, gemm || i == 0 ? 4 : 2);
+        for (int s : kSplits) {
+            if (s > 1 && 3 * s > KB) break;
+            p.kb_per_split = (int)ceil_div(KB, s);
+            p.splits = (int)ceil_div(KB, p.kb_per_split);
+            p.part_bytes = p.splits > 1 ? (size_t)p.splits * p.groups * p.tiles_m * kNarrow[i].blocks * kNarrow[i].bm * 128
+                                        : 0;
+            const double us = narrow_us(p, K, M);
+            if (us < best_us) {
+                best_us = us;
+                best = p;
+            }
+        }
+    }
+    return best;
 }
 
 // One product on the packed kernels; GEMM: N columns of one weight, else of a pair.
@@ -78,54 +189,132 @@ struct Product8 {
     void* part;
 };
 
+template <int MT, int CG, int UNROLL, bool GEMM, bool HALF, bool LDSA, int WAVES>
+hipError_t launch_decode8(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t s) {
+    void (*fn)(swk::DecodeArgs) = &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA, true, WAVES>;
+    swk::DecodeArgs args = a;
+    void* kargs[] = {&args};
+    return hipLaunchKernel(reinterpret_cast<const void*>(fn),
+                           dim3((unsigned)(ceil_div(n_tiled, 16 * CG) * (HALF ? 2 : 1))), dim3(64 * WAVES), kargs, 0, s);
+}
+
+// The decode kernel's configuration (MT 16-row tiles, CG groups of 16 columns a
+// workgroup, UNROLL blocks in flight a wave, L: activations through LDS, waves), as
+// measured (us, inputs rotated past the last-level cache).  Fused:
+//   K=3584 N=18944  M=1 / 8: <1,1,8> 23.3 / 23.4, <1,8,2> 25.4, <1,2,4> 24.2
+//                   M=16: <1,1,4,L,8 waves> 24.2, <1,1,8> 25.2, <1,1,8,L> 25.5
+//                   M=32: <2,1,4,L> 27.4, <2,8,1> 28.1, <2,2,2> 28.5
+//   K=8192 N=29568  M=1 / 16 / 32: <2,8,1> 71.8 / 71.3 / 72.4, <1,1,8> 83.0 / 83.5, <2,1,4,L> 88.3
+//   K=896 N=4864    M=1 / 16 / 32: <1,1,8> 4.1 / 4.6, <1,1,4,L,8 waves> 4.4 (16), <2,1,4,L> 5.0 (32)
+// wide groups where they still give most CUs a workgroup, else narrow ones, with
+// activations through LDS from 9 rows on.  One weight, each half of a tile's columns a
+// workgroup of its own (8 waves: the contraction is long, the columns few):
+//   K=18944 N=3584  M=1: <1,1,4> 12.8, <1,1,4,L> 13.3, 4 waves <1,1,14> 13.7
+//                   M=16: <1,1,4,L> 15.0, <1,1,4> 17.2, 4 waves <1,1,8,L> 15.9
+//                   M=32: <2,1,2,L> 18.6, 4 waves <2,2,2> 29.4
+//   K=29568 N=8192  M=1 / 16: <1,2,4> 38.4 / 40.3, <1,1,4> 37.3 / 49.2, <1,1,4,L> 38.7 / 42.9
+//                   M=32: 4 waves <2,2,2> 49.0, <2,1,2,L> 55.2
+//   K=4864 N=896    M=1 / 16 / 32: <1,1,4> 4.3, <1,1,4,L> 5.2 (16), <2,1,2,L> 6.5 (32)
+// 33 to 64 rows, on products that are too small for narrow_kernel to fill the CUs:
+//   K=896 N=4864    M=64: <4,2,1,L> 6.1, 8 waves <4,1,1,L> 7.3 (narrow_kernel 7.4)
+//   K=4864 N=896    M=64: 8 waves <4,1,1,L> 7.9, 4 waves 10.4 (narrow_kernel 9.5)
 template <bool GEMM>
-hipError_t run_rows(const Product8& q, const Plan& p, hipStream_t s) {
-    const int64_t nt = GEMM ? gemm_tiled_cols(q.N) : q.N;
-    if (p.variant == SWIGLU_VARIANT_DECODE) {
-        swk::DecodeArgs d{};
-        d.A = reinterpret_cast<const uint16_t*>(q.A);
-        d.Wp = reinterpret_cast<const uint16_t*>(q.W);
-        d.Y = q.Y;
-        d.M = (int)q.M; d.K = (int)(q.K / 2); d.N = (int)q.N; d.KB = p.KB;
-        d.sa = q.sa; d.s1 = q.s1; d.s2 = q.s2;
-        if constexpr (GEMM) return launch_decode_gemm<true>(d, nt, p, s);
-        else return launch_decode_cfg<true>(d, nt, p, s);
+hipError_t run_decode(const swk::DecodeArgs& d, int64_t nt, int cus, hipStream_t s) {
+    if constexpr (GEMM) {
+        if (d.M > 32) return launch_decode8<4, 1, 1, true, true, true, 8>(d, nt, s);
+        const bool wide = ceil_div(nt, 16) >= cus;   // two workgroups of one group a CU
+        if (d.M <= 16) {
+            if (wide && d.M > 8) return launch_decode8<1, 2, 4, true, true, false, 8>(d, nt, s);
+            return d.M > 4 ? launch_decode8<1, 1, 4, true, true, true, 8>(d, nt, s)
+                           : launch_decode8<1, 1, 4, true, true, false, 8>(d, nt, s);
+        }
+        return wide ? launch_decode8<2, 2, 2, true, true, false, 4>(d, nt, s)
+                    : launch_decode8<2, 1, 2, true, true, true, 8>(d, nt, s);
+    } else {
+        if (d.M > 32) return launch_decode8<4, 2, 1, false, false, true, 4>(d, nt, s);
+        if (4 * ceil_div(nt, 128) >= 3 * (int64_t)cus) return launch_decode8<2, 8, 1, false, false, false, 4>(d, nt, s);
+        if (d.M <= 8) return launch_decode8<1, 1, 8, false, false, false, 4>(d, nt, s);
+        return d.M <= 16 ? launch_decode8<1, 1, 4, false, false, true, 8>(d, nt, s)
+                         : launch_decode8<2, 1, 4, false, false, true, 4>(d, nt, s);
     }
-    swk::FusedArgs a{};
-    a.A = reinterpret_cast<const uint16_t*>(q.A);
-    a.W1 = reinterpret_cast<const uint16_t*>(q.W);
-    a.Y = q.Y;
-    a.M = (int)q.M; a.K = (int)(q.K / 2); a.N = (int)q.N;
-    a.tiles_m = p.tiles_m; a.tiles_n = p.tiles_n;
-    a.splits = p.splits; a.kb_per_split = p.kb_per_split; a.KB = p.KB;
-    a.sa = q.sa; a.s1 = q.s1; a.s2 = q.s2;
-    if (p.splits <= 1) return launch_stream_dp<false, false, false, GEMM, true>(a, p, s);
-    a.part = reinterpret_cast<float*>(q.part);
-    const int grid = p.tiles * p.splits;
-    const hipError_t e = launch_stream<128, true, false, false, false, false, GEMM, true>(a, grid, grid, s);
-    if (e != hipSuccess) return e;
-    const long long groups = (long long)q.M * (nt / 4);
-    const int rgrid = (int)std::max<long long>(1, std::min<long long>(ceil_div(groups, 256), (long long)p.cus * 8));
-    const int* part = reinterpret_cast<const int*>(q.part);
-    int M = (int)q.M, N = (int)q.N, NT = (int)nt, S = p.splits;
-    void* args[] = {(void*)&part, (void*)&q.Y, (void*)&q.sa, (void*)&q.s1, (void*)&q.s2, &M, &N, &NT, &S};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swq::splitk_reduce_int8_kernel<GEMM>), dim3(rgrid),
-                           dim3(256), args, 0, s);
+}
+
+template <int BM, int WT, bool GEMM, bool ONCE>
+hipError_t launch_narrow_as(const swq::NarrowArgs& a, hipStream_t s) {
+    using P = swq::Narrow<BM, 4, WT, 4, GEMM, ONCE>;
+    if (a.splits > 1 && !a.part) return hipErrorInvalidValue;
+    swq::NarrowArgs args = a;
+    void* kargs[] = {&args};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_kernel<P>),
+                                         dim3((unsigned)(a.tiles_m * a.groups * a.splits)), dim3(64 * P::WAVES), kargs, 0,
+                                         s);
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t jobs = (int64_t)a.tiles_m * a.groups * P::UNITS * (P::GEMM ? P::WT : 1) * P::TM;
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_reduce_kernel<P>),
+                           dim3((unsigned)ceil_div(jobs, 4)), dim3(256), kargs, 0, s);
+}
+
+template <int BM, int WT, bool GEMM>
+hipError_t launch_narrow(const swq::NarrowArgs& a, hipStream_t s) {
+    // weights that fit the last-level cache beside others stay there; see Narrow::ONCE
+    const int64_t bytes = (int64_t)a.groups * 4 * WT * 32 * a.KB * 128;
+    const bool once = bytes > ((int64_t)32 << 20) && a.tiles_m <= (BM == 64 ? 2 : 4);
+    return once ? launch_narrow_as<BM, WT, GEMM, true>(a, s) : launch_narrow_as<BM, WT, GEMM, false>(a, s);
 }
 
 template <bool GEMM>
-hipError_t run_product(const Product8& q, const Plan& p, hipStream_t s) {
+hipError_t run_rows(const Product8& q, const Plan8& p, hipStream_t s) {
+    if (p.how == Plan8::NARROW) {
+        swq::NarrowArgs a{};
+        a.A = q.A; a.W = q.W; a.Y = q.Y;
+        a.sa = q.sa; a.s1 = q.s1; a.s2 = q.s2;
+        a.part = reinterpret_cast<int*>(q.part);
+        a.M = (int)q.M; a.K = (int)q.K; a.N = (int)q.N; a.KB = (int)ceil_div(q.K, 128);
+        a.units = p.units; a.tiles_m = p.tiles_m; a.groups = p.groups;
+        a.splits = p.splits; a.kb_per_split = p.kb_per_split;
+        switch (p.tile) {
+            case 0: return launch_narrow<128, 2, GEMM>(a, s);
+            case 1: return launch_narrow<128, 1, GEMM>(a, s);
+            default: return launch_narrow<64, 1, GEMM>(a, s);
+        }
+    }
+    const uint16_t* A = reinterpret_cast<const uint16_t*>(q.A);
+    const uint16_t* W = reinterpret_cast<const uint16_t*>(q.W);
+    if (p.how == Plan8::DECODE) {
+        swk::DecodeArgs d{};
+        d.A = A; d.Wp = W; d.Y = q.Y;
+        d.M = (int)q.M; d.K = (int)(q.K / 2); d.N = (int)q.N; d.KB = (int)ceil_div(q.K, 128);
+        d.sa = q.sa; d.s1 = q.s1; d.s2 = q.s2;
+        return run_decode<GEMM>(d, GEMM ? gemm_tiled_cols(q.N) : q.N, p.cus, s);
+    }
+    swk::FusedArgs a{};
+    a.A = A; a.W1 = W; a.Y = q.Y;
+    a.M = (int)q.M; a.K = (int)(q.K / 2); a.N = (int)q.N;
+    a.tiles_m = p.stream.tiles_m; a.tiles_n = p.stream.tiles_n;
+    a.splits = 1; a.kb_per_split = a.KB = p.stream.KB;
+    a.sa = q.sa; a.s1 = q.s1; a.s2 = q.s2;
+    if constexpr (!GEMM) {
+        if (p.stream.panels > 0) {
+            a.panels = p.stream.panels;
+            const int g = std::min(a.panels, p.cus);
+            return launch_stream<256, false, true, false, false, false, false, true>(a, g, g, s);
+        }
+    }
+    return launch_stream_dp<false, false, false, GEMM, true>(a, p.stream, s);
+}
+
+template <bool GEMM>
+hipError_t run_product(const Product8& q, const Plan8& p, hipStream_t s) {
     if (!in_chunks(q.M, q.K)) return run_rows<GEMM>(q, p, s);
     const int64_t rows = balanced_chunk(q.M, stream_rows_limit(q.K, 1));
-    const int64_t nt = GEMM ? gemm_tiled_cols(q.N) : q.N;
     for (int64_t m0 = 0; m0 < q.M; m0 += rows) {
         Product8 c = q;
         c.M = std::min(rows, q.M - m0);
         c.A += m0 * q.K;
         c.sa += m0;
         c.Y += m0 * q.N;
-        const Plan cp = make_plan(c.M, q.K / 2, nt, SWIGLU_VARIANT_DATA_PARALLEL, p.cus);
-        const hipError_t e = run_rows<GEMM>(c, cp, s);
+        // not plan_int8: the call's workspace holds no sums of a chunk's parts
+        const hipError_t e = run_rows<GEMM>(c, stream_plan(GEMM, c.M, q.K, q.N), s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -167,13 +356,13 @@ int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 struct MlpSpace {
     int64_t a8, sa, y8, sy, part, bytes;
 };
-MlpSpace mlp_space(int64_t M, int64_t K, int64_t N, const Plan& up, const Plan& down) {
+MlpSpace mlp_space(int64_t M, int64_t K, int64_t N, const Plan8& up, const Plan8& down) {
     MlpSpace w{};
     w.sa = align256(M * K);
     w.y8 = w.sa + align256(4 * M);
     w.sy = w.y8 + align256(M * N);
     w.part = w.sy + align256(4 * M);
-    w.bytes = w.part + (int64_t)std::max(split_workspace_bytes(up, M, N), gemm_split_bytes(down, M, K));
+    w.bytes = w.part + (int64_t)std::max(up.part_bytes, down.part_bytes);
     return w;
 }
 
@@ -249,17 +438,17 @@ swiglu_status swiglu_gemm_pack_weight_int8(const int8_t* W, int8_t* Wg, int64_t 
 
 size_t swiglu_workspace_bytes_int8(int64_t M, int64_t K, int64_t N) {
     if (check_shape_int8(M, K, N) != SWIGLU_OK || M == 0) return 0;
-    return split_workspace_bytes(fused_plan_int8(M, K, N), M, N);
+    return plan_int8(false, M, K, N).part_bytes;
 }
 
 size_t swiglu_gemm_workspace_bytes_int8(int64_t M, int64_t K, int64_t N) {
     if (check_shape_int8(M, K, N) != SWIGLU_OK || M == 0) return 0;
-    return gemm_split_bytes(gemm_plan_int8(M, K, N), M, N);
+    return plan_int8(true, M, K, N).part_bytes;
 }
 
 size_t swiglu_mlp_workspace_bytes_int8(int64_t M, int64_t K, int64_t N) {
     if (check_mlp_int8(M, K, N) != SWIGLU_OK || M == 0) return 0;
-    return (size_t)mlp_space(M, K, N, fused_plan_int8(M, K, N), gemm_plan_int8(M, N, K)).bytes;
+    return (size_t)mlp_space(M, K, N, plan_int8(false, M, K, N), plan_int8(true, M, N, K)).bytes;
 }
 
 swiglu_status swiglu_fused_packed_int8(const int8_t* A, const float* sa, const int8_t* Wp, const float* s1,
@@ -274,8 +463,8 @@ swiglu_status swiglu_fused_packed_int8(const int8_t* A, const float* sa, const i
     b.out(Y, 2 * M * N);
     if (workspace) b.out(workspace, (int64_t)workspace_bytes);
     if ((st = b.check()) != SWIGLU_OK) return st;
-    const Plan p = fused_plan_int8(M, K, N);
-    if (workspace_bytes < split_workspace_bytes(p, M, N)) return SWIGLU_ERR_WORKSPACE;
+    const Plan8 p = plan_int8(false, M, K, N);
+    if (workspace_bytes < p.part_bytes) return SWIGLU_ERR_WORKSPACE;
     const Product8 q{(const uint8_t*)A, sa, (const uint8_t*)Wp, s1, s2, Y, M, K, N, workspace};
     const hipError_t e = run_product<false>(q, p, (hipStream_t)stream);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
@@ -293,8 +482,8 @@ swiglu_status swiglu_gemm_packed_int8(const int8_t* A, const float* sa, const in
     b.out(C, 2 * M * N);
     if (workspace) b.out(workspace, (int64_t)workspace_bytes);
     if ((st = b.check()) != SWIGLU_OK) return st;
-    const Plan p = gemm_plan_int8(M, K, N);
-    if (workspace_bytes < gemm_split_bytes(p, M, N)) return SWIGLU_ERR_WORKSPACE;
+    const Plan8 p = plan_int8(true, M, K, N);
+    if (workspace_bytes < p.part_bytes) return SWIGLU_ERR_WORKSPACE;
     const Product8 q{(const uint8_t*)A, sa, (const uint8_t*)Wg, sw, sw, C, M, K, N, workspace};
     const hipError_t e = run_product<true>(q, p, (hipStream_t)stream);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
@@ -313,7 +502,7 @@ swiglu_status swiglu_mlp_packed_int8(const swiglu_bf16* A, const int8_t* Wp, con
     b.out(Y, 2 * M * N); b.out(Z, 2 * M * K);
     if (workspace) b.out(workspace, (int64_t)workspace_bytes);
     if ((st = b.check()) != SWIGLU_OK) return st;
-    const Plan up = fused_plan_int8(M, K, N), down = gemm_plan_int8(M, N, K);
+    const Plan8 up = plan_int8(false, M, K, N), down = plan_int8(true, M, N, K);
     const MlpSpace w = mlp_space(M, K, N, up, down);
     if (workspace_bytes < (size_t)w.bytes) return SWIGLU_ERR_WORKSPACE;
     char* const base = (char*)workspace;
@@ -329,6 +518,17 @@ swiglu_status swiglu_mlp_packed_int8(const swiglu_bf16* A, const int8_t* Wp, con
     if (e == hipSuccess)
         e = run_product<true>(Product8{y8, sy, (const uint8_t*)W3g, s3, s3, Z, M, N, K, base + w.part}, down, s);
     return e == hipSuccess ? SWIGLU_OK : hip_fail(e);
+}
+
+int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N, int32_t* plan) {
+    if (check_shape_int8(M, K, N) != SWIGLU_OK || M == 0 || !plan) return 0;
+    const Plan8 p = plan_int8(gemm != 0, M, K, N);
+    const bool narrow = p.how == Plan8::NARROW;
+    const int rows = p.how == Plan8::DECODE ? (M <= 16 ? 16 : M <= 32 ? 32 : 64) : narrow ? kNarrow[p.tile].bm : 256;
+    const int cols = narrow ? 32 * kNarrow[p.tile].blocks : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
+    const int32_t v[4] = {p.how, rows, cols, narrow ? p.splits : 1};
+    std::copy(v, v + 4, plan);
+    return 1;
 }
 
 }  // extern "C"

@@ -195,45 +195,4 @@ __global__ __launch_bounds__(256) void pack_int8_kernel(const uint8_t* __restric
     }
 }
 
-// ---------------------------------------------------------------------------
-// The splits' int32 sums, added, scaled and finished: the fused product (NT = N:
-// Gate of column n at n, Up at N + n) or, GEMM, the single pack's tiled columns
-// (n: output column (n / 128) 256 + n % 128, and that + 128 at NT + n).
-// ---------------------------------------------------------------------------
-template <bool GEMM>
-__global__ __launch_bounds__(256) void splitk_reduce_int8_kernel(const int* __restrict__ part,
-                                                                 uint16_t* __restrict__ Y,
-                                                                 const float* __restrict__ sa,
-                                                                 const float* __restrict__ s1,
-                                                                 const float* __restrict__ s2, int M, int N, int NT,
-                                                                 int S) {
-    const long long groups = (long long)M * (NT / 4);
-    const size_t stride = (size_t)M * 2 * (size_t)NT;
-    for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < groups; t += (long long)gridDim.x * 256) {
-        const int m = (int)(t / (NT / 4));
-        const int n = (int)(t % (NT / 4)) * 4;
-        const int* src = part + (size_t)m * 2 * (size_t)NT + n;
-        i32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
-#pragma unroll 4
-        for (int s = 0; s < S; ++s) {
-            g += *reinterpret_cast<const i32x4*>(src + s * stride);
-            u += *reinterpret_cast<const i32x4*>(src + s * stride + NT);
-        }
-        const int col = GEMM ? (n / PACK_BN) * PACK_ROWS + n % PACK_BN : n;
-        const f32x4 c1 = scales4(s1, col, N), c2 = GEMM ? scales4(s1, col + PACK_BN, N) : scales4(s2, col, N);
-        const float row = sa[m];
-        float x[4], y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] = scaled(g[e], c1[e], row);
-            y[e] = scaled(u[e], c2[e], row);
-            if constexpr (!GEMM) x[e] = silu_f(x[e]) * y[e];
-        }
-        uint16_t* out = Y + (size_t)m * N + col;
-        if (col < N) *reinterpret_cast<u32x2*>(out) = u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
-        if (GEMM && col + PACK_BN < N)
-            *reinterpret_cast<u32x2*>(out + PACK_BN) = u32x2{pack2(y[0], y[1]), pack2(y[2], y[3])};
-    }
-}
-
 }  // namespace swq

@@ -102,6 +102,17 @@ struct Plan {
 constexpr int kDecodeMaxM = 64;
 inline bool variant_known(int v) { return v >= SWIGLU_VARIANT_AUTO && v <= SWIGLU_VARIANT_SEQUENTIAL; }
 
+// Wave quantisation of the 256 x 128 schedule: when the last round of
+// tiles would leave most CUs idle, the column tiles that make up that round
+// run afterwards as 128 x 128 tiles (twice as many, half the work each).
+inline int tail_tiles(int tiles_m, int tiles_n, int cus) {
+    const int tiles = tiles_m * tiles_n;
+    const int rem = tiles > cus ? tiles % cus : 0;
+    if (rem == 0 || rem * 10 > cus * 6) return 0;
+    const int nt = (int)ceil_div(rem, tiles_m);
+    return nt < tiles_n ? nt : 0;
+}
+
 inline Plan make_plan(int64_t M, int64_t K, int64_t N, int variant, int cus) {
     Plan p{};
     if (cus <= 0) cus = 256;
@@ -141,17 +152,7 @@ inline Plan make_plan(int64_t M, int64_t K, int64_t N, int variant, int cus) {
     p.tiles_m = (int)ceil_div(M, p.t.BM);
     p.tiles_n = (int)ceil_div(N, p.t.BN);
     p.tiles = p.tiles_m * p.tiles_n;
-    // Wave quantisation of the 256 x 128 schedule: when the last round of
-    // tiles would leave most CUs idle, the column tiles that make up that round
-    // run afterwards as 128 x 128 tiles (twice as many, half the work each).
-    p.tail_ntiles = 0;
-    if (dp_tiles && p.t.BM == 256 && p.tiles > cus) {
-        const int rem = p.tiles % cus;
-        if (rem > 0 && rem * 10 <= cus * 6) {
-            const int nt = (int)ceil_div(rem, p.tiles_m);
-            if (nt < p.tiles_n) p.tail_ntiles = nt;
-        }
-    }
+    p.tail_ntiles = dp_tiles && p.t.BM == 256 ? tail_tiles(p.tiles_m, p.tiles_n, cus) : 0;
     // One row of 128-row tiles that leaves CUs idle: the 32-column weight
     // panels (four per tile) are spread evenly over the CUs instead, so every
     // CU streams weights.
@@ -176,42 +177,6 @@ inline Plan make_plan(int64_t M, int64_t K, int64_t N, int variant, int cus) {
 inline size_t split_workspace_bytes(const Plan& p, int64_t M, int64_t N) {
     if (p.variant != SWIGLU_VARIANT_SPLIT_K || p.splits <= 1) return 0;
     return (size_t)p.splits * (size_t)M * 2 * (size_t)N * sizeof(float);
-}
-
-template <int BM, int BN, int WM, int WN, bool DUAL, bool PACKED, bool SPLIT>
-hipError_t launch_tile(const swk::FusedArgs& a, int grid, hipStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&swk::fused_tile_kernel<BM, BN, WM, WN, DUAL, PACKED, SPLIT>);
-    swk::FusedArgs args = a;
-    void* kargs[] = {&args};
-    return hipLaunchKernel(fn, dim3(grid), dim3(64 * WM * WN), kargs, 0, s);
-}
-
-// n_tiled: the packed weights' output columns (N for the fused product; 128
-// per packed tile for the single-weight GEMM).  HALF: one workgroup per
-// (column groups, weight half), twice the grid.
-// la: low-rank adapters (NULL: none).
-template <bool I8, int MT, int CG, int UNROLL, bool GEMM = false, bool HALF = false, bool LDSA = false>
-hipError_t launch_decode(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t s, const swk::LoraArgs* la) {
-    void (*plain)(swk::DecodeArgs) = &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA, I8>;
-    const void* fn = reinterpret_cast<const void*>(plain);
-    if constexpr (!I8) {
-        void (*adapted)(swk::DecodeArgs, swk::LoraArgs) =
-            &swk::decode_kernel<MT, CG, UNROLL, GEMM, HALF, LDSA, false, swk::LoraArgs>;
-        if (la) fn = reinterpret_cast<const void*>(adapted);
-    }
-    swk::DecodeArgs args = a;
-    swk::LoraArgs lora = la ? *la : swk::LoraArgs{};
-    void* kargs[] = {&args, &lora};
-    return hipLaunchKernel(fn, dim3((unsigned)(ceil_div(n_tiled, 16 * CG) * (HALF ? 2 : 1))), dim3(256), kargs, 0,
-                           s);
-}
-
-template <int BM, int BN, int WM, int WN, bool SPLIT, int WSRC = swk::W_PACKED>
-hipError_t launch_prefill(const swk::FusedArgs& a, int grid, hipStream_t s) {
-    const void* fn = reinterpret_cast<const void*>(&swk::fused_prefill_kernel<BM, BN, WM, WN, SPLIT, WSRC>);
-    swk::FusedArgs args = a;
-    void* kargs[] = {&args};
-    return hipLaunchKernel(fn, dim3(grid), dim3(64 * WM * WN), kargs, 0, s);
 }
 
 // `total` work items (tiles, or tile x K split) on `grid` <= total workgroups;
@@ -253,7 +218,7 @@ template <bool IL, bool F8 = false, bool SEQ = false, bool GEMM = false, bool I8
 hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t s,
                             const swk::LoraArgs* la = nullptr) {
     const int grid = p.tiles;
-    if (p.t.BM == 128) {
+    if constexpr (!I8) if (p.t.BM == 128) {   // int8: 256-row tiles only
         if constexpr (SEQ) return launch_stream<128, false, false, false, false, true>(a, grid, grid, s);
         if constexpr (!GEMM && !IL) {
             // two rows of 128-row tiles that leave CUs idle on a wide product:
@@ -268,7 +233,7 @@ hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t 
                 pa.tiles_m = 1;
                 pa.panels = 4 * p.tiles_n;
                 const int g = std::min(pa.panels, p.cus);
-                return launch_stream<256, false, true, IL, F8, false, false, I8>(pa, g, g, s, la);
+                return launch_stream<256, false, true, IL, F8, false, false>(pa, g, g, s, la);
             }
         }
         if (p.panels > 0) {
@@ -278,10 +243,10 @@ hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t 
             pa.panels = GEMM ? 2 * p.panels : p.panels;
             if (pa.panels <= 4 * p.cus) {
                 const int g = std::min(pa.panels, p.cus);
-                return launch_stream<128, false, true, IL, F8, false, GEMM, I8>(pa, g, g, s, la);
+                return launch_stream<128, false, true, IL, F8, false, GEMM>(pa, g, g, s, la);
             }
         }
-        return launch_stream<128, false, false, IL, F8, false, GEMM, I8>(a, grid, grid, s, la);
+        return launch_stream<128, false, false, IL, F8, false, GEMM>(a, grid, grid, s, la);
     }
     // one workgroup per CU works through the 256-row tiles
     if (p.tail_ntiles == 0)
@@ -316,111 +281,6 @@ hipError_t launch_stream_dp(const swk::FusedArgs& a, const Plan& p, hipStream_t 
 // The data-parallel streaming plan (any M).
 inline Plan stream_dp_plan(int64_t M, int64_t K, int64_t N, int cus) {
     return make_plan(M, K, N, SWIGLU_VARIANT_DATA_PARALLEL, cus);
-}
-
-// The decode kernel's configuration for a plan: column groups per workgroup
-// (CG) and K blocks in flight per wave (UNROLL), measured on this chip: wider
-// groups read each activation fragment for more weight bytes and stream
-// longer contiguous runs of the packed blocks; they pay off for long K (>= 96
-// blocks), or from 17 tokens on, as long as the grid still gives about one
-// workgroup per CU.  Measured (us, one call, inputs rotated past the
-// last-level cache):
-//   K=3584 N=18944 M=1 / 16: <1,1,8> 42.9 / 45.8, <1,1,4> 43.0 / 46.3, <1,2,4> 46.1 / 47.5
-//   K=8192 N=29568 M=1 / 16: <1,8,2> 138.4 / 138.0, the same with L 142.3 / 142.0
-//   K=8192 N=29568 M=32: <2,8,1> 140.2, <2,4,1> 147.3, <2,2,2> 170.4
-//   K=3584 N=18944 M=32: <2,8,1> 52.2, <2,2,2> 54.7, <2,4,1> 61.8
-//   K=896 N=4864 M=64: <4,2,1> 9.9, <4,2,2> 10.5, <4,1,1> 11.8
-// With the activations staged through LDS (L = LDSA: one full-line load
-// per 8 rows instead of a half-line per row and fragment), which pays once
-// there are more than 8 distinct rows and the group is narrow:
-//   K=3584 N=18944 M=16: <1,1,8,L> 44.1-44.4 against 45.9-46.3; M=1 / 4 / 8: no gain
-//   K=896 N=4864 M=64: <4,2,1,L> 9.33-9.38 against 9.82-9.90; M=32 with 8 groups: 55.6 against 52.0
-// n_tiled: the packed weights' output columns.
-template <bool I8 = false>
-hipError_t launch_decode_cfg(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s,
-                             const swk::LoraArgs* la = nullptr) {
-    const bool long_k = p.KB >= 96;
-    const int64_t wg64 = ceil_div(n_tiled, 64), wg128 = ceil_div(n_tiled, 128);
-    switch (p.decode_mt) {
-        case 1:
-            if (long_k && 4 * wg128 >= 3 * p.cus) return launch_decode<I8, 1, 8, 2>(d, n_tiled, s, la);
-            return d.M > 8 ? launch_decode<I8, 1, 1, 8, false, false, true>(d, n_tiled, s, la)
-                           : launch_decode<I8, 1, 1, 8>(d, n_tiled, s, la);
-        case 2:
-            if (2 * wg128 >= p.cus) return launch_decode<I8, 2, 8, 1>(d, n_tiled, s, la);
-            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<I8, 2, 4, 1>(d, n_tiled, s, la)
-                                                    : launch_decode<I8, 2, 2, 2>(d, n_tiled, s, la);
-        default:
-            return (long_k && 4 * wg64 >= 3 * p.cus) ? launch_decode<I8, 4, 4, 1>(d, n_tiled, s, la)
-                                                    : launch_decode<I8, 4, 2, 1, false, false, true>(d, n_tiled, s, la);
-    }
-}
-
-// The same for the single-weight GEMM (n_tiled = 128 per 256-column packed
-// tile), where a workgroup may take one weight half (HALF): half the bytes per
-// workgroup and twice the grid.  Measured on this chip (us, one call, inputs
-// rotated past the last-level cache):
-//   K=3584 N=18944 M=1: <1,1,14,H> 22.6, <1,1,8,H> 23.2, <1,1,8> 23.9
-//   K=3584 N=18944 M=16: <1,1,8> 26.7, <1,1,8,H> 29.7
-//   K=8192 N=29568 M=1 / 16: <1,4,4,H> 79.5 / 78.6, <1,1,8> 93.7 / 99.0
-//   K=18944 N=3584 M=1 / 16: <1,1,14,H> 23.3 / 31.3, <1,1,8,H> 23.6 / 30.8, <1,1,8> 30.6 / 42.6
-//   K=8192 N=29568 M=32: <2,8,1,H> 73.3, <2,4,1> 76.1, <2,2,2,H> 113.4
-//   K=29568 N=8192 M=32: <2,2,2,H> 92.8, <2,2,2> 129.3, <2,4,1,H> 123.9
-//   K=896 N=4864 M=64: <4,2,1,H> 8.0, <4,2,1> 9.5
-//   K=4864 N=896 M=64: <4,1,1,H> 21.8, <4,2,1,H> 24.4, <4,2,1> 31.8
-// and with the activations staged through LDS (L, as for the fused product):
-//   K=3584 N=18944 M=16: <1,1,8,H,L> 25.2, <1,1,8,L> 26.3, <1,1,8> 27.0
-//   K=18944 N=3584 M=16: <1,1,8,H,L> 27.4, <1,1,8,H> 30.9; K=4864 N=896 M=16: 7.9 against 9.5
-//   K=8192 N=29568 M=16: <1,4,4,H> 77.7, <1,4,4,H,L> 79.5
-//   K=896 N=4864 M=64: <4,1,1,H,L> 6.8, <4,2,1,H,L> 7.1, <4,2,1,H> 8.0
-//   K=4864 N=896 M=64: <4,1,1,H,L> 17.6, <4,1,1,H> 21.8
-// i.e. halves whenever the whole-pair grid leaves CUs short of work, the
-// deepest per-wave prefetch the registers allow at one or two tokens' rows,
-// and staged activations for narrow groups from 9 rows on.
-template <bool I8 = false>
-hipError_t launch_decode_gemm(const swk::DecodeArgs& d, int64_t n_tiled, const Plan& p, hipStream_t s,
-                             const swk::LoraArgs* la = nullptr) {
-    const bool long_k = p.KB >= 96;
-    const int64_t wg64 = ceil_div(n_tiled, 64);
-    switch (p.decode_mt) {
-        case 1:
-            if (long_k && 2 * wg64 >= p.cus) return launch_decode<I8, 1, 4, 4, true, true>(d, n_tiled, s, la);
-            if (d.M <= 8) return launch_decode<I8, 1, 1, 14, true, true>(d, n_tiled, s, la);
-            return launch_decode<I8, 1, 1, 8, true, true, true>(d, n_tiled, s, la);
-        case 2:
-            if (long_k) {
-                return 4 * wg64 >= 3 * p.cus ? launch_decode<I8, 2, 8, 1, true, true>(d, n_tiled, s, la)
-                                             : launch_decode<I8, 2, 2, 2, true, true>(d, n_tiled, s, la);
-            }
-            return 2 * ceil_div(n_tiled, 128) >= p.cus ? launch_decode<I8, 2, 8, 1, true>(d, n_tiled, s, la)
-                                                       : launch_decode<I8, 2, 2, 2, true>(d, n_tiled, s, la);
-        default:
-            if (long_k && 4 * wg64 >= 3 * p.cus) return launch_decode<I8, 4, 4, 1, true>(d, n_tiled, s, la);
-            return launch_decode<I8, 4, 1, 1, true, true, true>(d, n_tiled, s, la);
-    }
-}
-
-// The single-weight GEMM's plan: the fused product's AUTO rule on the pack's
-// tiled width (128 columns per packed tile), whose split-K needs fp32
-// partials over those tiled columns.  One addition: a compute-bound product
-// (from 1024 rows on) whose data-parallel tiles leave over half the CUs idle
-// -- a narrow output, like the MLP's down projection back to a small model
-// width -- splits K as well: there the idle matrix cores cost more than the
-// partial sums' traffic (measured: 0.5B-width down projection, M=4096
-// K=4864 N=896, 86.6 us data-parallel on 64 tiles, 70 us in 4 splits).
-inline Plan gemm_plan(int64_t M, int64_t K, int64_t N) {
-    const int cus = cu_count_now();
-    const int64_t nt = gemm_tiled_cols(N);
-    Plan p = make_plan(M, K, nt, SWIGLU_VARIANT_AUTO, cus);
-    if (p.variant == SWIGLU_VARIANT_DATA_PARALLEL && M >= 1024 && 2 * (int64_t)p.tiles < p.cus) {
-        const Plan q = make_plan(M, K, nt, SWIGLU_VARIANT_SPLIT_K, cus);
-        if (q.splits > 1) p = q;
-    }
-    return p;
-}
-
-inline size_t gemm_split_bytes(const Plan& p, int64_t M, int64_t N) {
-    return split_workspace_bytes(p, M, gemm_tiled_cols(N));
 }
 
 }  // namespace swl

@@ -114,8 +114,6 @@ __device__ __forceinline__ void st16(uint16_t* p, u32x4 v) { *reinterpret_cast<u
 // a load.  (Its warning for a reserved register is off here: it says that the value in m0
 // is not kept over the statement, which is what is meant.)
 // ---------------------------------------------------------------------------
-constexpr int RSRC_END = 0x7FFFFFF0;          // every offset of a valid lane is below
-constexpr uint32_t OFF_NONE = 0xFFFFFFF0u;    // past every descriptor's end
 __device__ __forceinline__ i32x4 stage_rsrc(const uint16_t* base, bool valid) {
     const uint64_t p = (uint64_t)base;
     return i32x4{(int)(uint32_t)p, (int)(uint32_t)(p >> 32) & 0xFFFF, valid ? RSRC_END : 0, 0x00020000};
@@ -129,39 +127,8 @@ __device__ __forceinline__ void dma16_buffer(i32x4 rsrc, uint32_t off, uint32_t 
 }
 #pragma clang diagnostic pop
 
-// ---------------------------------------------------------------------------
-// The epilogue of one 32 x 32 MFMA block without LDS.  A lane holds 16 sums of
-// row l & 31: v[4q + e] is column 8q + 4 (l >> 5) + e.  Two exchanges between
-// lanes (v_permlane32_swap, v_permlane16_swap) turn the block, packed to bf16,
-// into 16 bytes a lane with four lanes on 64 adjacent bytes of a row:
-//   out[h]: row 16h + (l & 15), columns 8c .. 8c + 7, c = 2 ((l >> 4) & 1) + (l >> 5).
-// They are their own inverse, so operands of the epilogue (dY, G, U) are loaded
-// that way too and brought into the lanes that hold the matching sums.
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void swap32(unsigned& a, unsigned& b) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-__device__ __forceinline__ void swap16(unsigned& a, unsigned& b) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = r[0];
-    b = r[1];
-}
-
-// d[q][w]: packed columns 8q + 4 (l >> 5) + 2w, + 1
-__device__ __forceinline__ void block_to_rows(unsigned (&d)[4][2], u32x4 (&out)[2]) {
-#pragma unroll
-    for (int q = 0; q < 4; q += 2)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) swap32(d[q][w], d[q + 1][w]);
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) swap16(d[q][w], d[q + 2][w]);
-    out[0] = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
-    out[1] = u32x4{d[2][0], d[2][1], d[3][0], d[3][1]};
-}
+// The inverse of block_to_rows: operands of the epilogue (dY, G, U) are loaded along
+// rows too, and brought into the lanes that hold the matching sums.
 __device__ __forceinline__ void rows_to_block(const u32x4 (&in)[2], float (&v)[16]) {
     unsigned d[4][2] = {{in[0][0], in[0][1]}, {in[0][2], in[0][3]}, {in[1][0], in[1][1]}, {in[1][2], in[1][3]}};
 #pragma unroll
@@ -181,15 +148,6 @@ __device__ __forceinline__ void rows_to_block(const u32x4 (&in)[2], float (&v)[1
         }
 }
 
-// A matrix seen from a tile's corner, for the block epilogue: accesses of lanes
-// past its rows or columns have offsets past the descriptor's end, where loads
-// give 0 and stores are dropped, so the epilogue has no branches (with branches
-// the compiler moved all sums of a wave out of the accumulation registers at
-// once and spilled).
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-__device__ __forceinline__ Rsrc corner(const uint16_t* c, long long ld, int m0, int n0) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(c + (size_t)m0 * ld + n0), 0, RSRC_END, 0x00020000);
-}
 // The lane's two 16-byte pieces of a block: rows r, r + 16 and column n of the
 // tile at (m0, n0); inside: whether they lie in the matrix.
 struct BlockAt {

@@ -178,13 +178,20 @@ def test_pack_layout(dev):
                 assert torch.equal(got, want)
 
 
-# every schedule: one to 64 rows (decode: each count of 16-row tiles, wide and narrow groups), panels, 128-row tiles,
-# persistent 256-row tiles with and without a tail, splits; ragged K and N
-SHAPES = [(1, 16, 8), (1, 896, 4864), (7, 144, 136), (8, 896, 512), (9, 912, 520), (16, 13312, 264), (17, 1024, 1040),
-          (30, 8192, 24584), (32, 2064, 19000), (33, 896, 4864), (48, 13312, 16392), (64, 912, 4872), (50, 2048, 18944),
-          (65, 896, 4864), (100, 4096, 18952), (128, 3584, 8200), (129, 912, 1032), (180, 1040, 19000), (256, 896, 4864),
-          (300, 4112, 1032), (400, 912, 33000), (512, 896, 4864), (513, 1040, 904), (1100, 2000, 4872),
-          (2100, 1024, 9000), (100, 16000, 520), (200, 16000, 1000), (1030, 4112, 1000)]
+# every kernel: one to 64 rows (each count of 16-row tiles, wide and narrow groups), few rows (each tile, whole and in
+# parts), many rows (panels, persistent 256-row tiles with and without a tail); ragged K and N
+SHAPES = [(1, 16, 8), (1, 896, 4864), (4, 1040, 520), (5, 2064, 520), (7, 144, 136), (8, 896, 512), (9, 912, 520),
+          (1, 1040, 25000), (16, 1040, 25000), (16, 13312, 264), (17, 1024, 1040), (30, 8192, 24584), (32, 2064, 19000),
+          (12, 2064, 65544), (31, 2064, 65544), (33, 896, 4864), (34, 128, 64), (48, 912, 1032), (64, 4880, 904),
+          (37, 1760, 64), (48, 13312, 16392), (64, 912, 4872), (50, 2048, 18944), (65, 896, 4864), (65, 272, 72),
+          (66, 9120, 5872), (70, 400, 8312), (70, 7216, 8280), (70, 7504, 16624), (71, 2960, 2712), (74, 656, 64),
+          (76, 576, 18744), (69, 7664, 5872), (82, 416, 16768), (100, 4096, 18952), (128, 3584, 8200), (129, 912, 1032),
+          (149, 1744, 23056), (180, 1040, 19000), (200, 8192, 29568), (220, 400, 19688), (256, 896, 4864),
+          (300, 4112, 1032), (300, 9008, 20008), (414, 16064, 1368), (400, 912, 33000), (512, 896, 4864),
+          (513, 1040, 904), (655, 144, 19880), (656, 2544, 10192), (972, 144, 29584), (1100, 2000, 4872),
+          (1159, 1600, 10816), (1196, 2576, 12472), (1300, 3600, 18952), (1816, 2576, 264), (1800, 3600, 18952),
+          (2100, 1024, 9000), (2706, 7216, 72), (2729, 14912, 400), (100, 16000, 520), (200, 16000, 1000),
+          (1030, 4112, 1000)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -196,11 +203,21 @@ def test_products(dev, M, K, N):
     check_gemm(C, A, sa, W1, s1, "gemm")
 
 
-def test_splits_are_met(dev):
-    """The last shapes above are split over K."""
-    assert sw.swiglu_workspace_bytes_int8(100, 16000, 520) > 0
-    assert sw.swiglu_gemm_workspace_bytes_int8(200, 16000, 1000) > 0
-    assert sw.swiglu_gemm_workspace_bytes_int8(1030, 4112, 1000) > 0
+def test_every_kernel_is_met(dev):
+    """The shapes above, as they are planned on this device."""
+    met = set()
+    for gemm in (False, True):
+        for shape in SHAPES:
+            p = sw.swiglu_probe_int8_plan(gemm, *shape)
+            met.add((gemm, p["kernel"], p["rows"], p["cols"], p["splits"] > 1))
+    for gemm in (False, True):
+        for tile in ((64, 128), (128, 128), (128, 256)):
+            for parts in (False, True):
+                assert (gemm, "narrow") + tile + (parts,) in met, (gemm, tile, parts)
+        for rows in (16, 32, 64):
+            assert (gemm, "decode", rows, 256, False) in met
+        assert (gemm, "stream", 256, 256, False) in met
+    assert (False, "stream", 256, 64, False) in met
 
 
 @pytest.mark.parametrize("M", [1, 40, 100, 300])

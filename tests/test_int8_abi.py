@@ -150,3 +150,17 @@ def test_binding_refusals():
         sw.swiglu_quantize_rows_int8(a, scales=v)
     with pytest.raises(ValueError, match="invalid int8 weight shape"):
         sw.swiglu_mlp_packed_int8(a, wp, v, v, wp, torch.zeros(64))
+
+
+def test_plan_probe():
+    for gemm in (False, True):
+        for shape, kernel in (((1, 64, 72), "decode"), ((32, 3584, 18944), "decode"), ((33, 3584, 18944), None),
+                              ((8192, 3584, 18944), "stream")):
+            p = sw.swiglu_probe_int8_plan(gemm, *shape)
+            assert kernel in (None, p["kernel"]) and p["rows"] > 0 and p["cols"] > 0 and p["splits"] >= 1
+            need = (sw.swiglu_gemm_workspace_bytes_int8 if gemm else sw.swiglu_workspace_bytes_int8)(*shape)
+            assert (need > 0) == (p["splits"] > 1)
+        for bad in ((0, 64, 72), (4, 72, 64), (4, 64, 60)):
+            with pytest.raises(ValueError, match="invalid shape"):
+                sw.swiglu_probe_int8_plan(gemm, *bad)
+    assert sw.lib().swiglu_probe_int8_plan(0, 4, 64, 72, None) == 0
