@@ -455,15 +455,22 @@ hipError_t run_dgate(const Call& c, const uint16_t* dY, const uint16_t* G, const
                            dim3((unsigned)std::min<int64_t>(ceil_div(groups, 256), 16384)), dim3(256), kargs, 0, c.s);
 }
 
-// Elements from Gate and Up kept as int8 (swt::KeptUse).
+// Elements from Gate and Up kept as int8 (swt::KeptUse): four rows a thread once that
+// leaves every CU its threads, one row before.
+template <int USE, int ROWS>
+hipError_t run_kept_rows(const int8_t* codes, const swiglu_bf16* scales, const uint16_t* dY, uint16_t* C0, uint16_t* C1,
+                         int64_t M, int64_t N, hipStream_t s) {
+    long long units = ceil_div(M, ROWS) * (N / 8);
+    int Mi = (int)M, Ni = (int)N;
+    void* kargs[] = {(void*)&codes, (void*)&scales, (void*)&dY, (void*)&C0, (void*)&C1, &Mi, &Ni, &units};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::kept_kernel<USE, ROWS>),
+                           dim3((unsigned)std::min<int64_t>(ceil_div(units, 256), 65536)), dim3(256), kargs, 0, s);
+}
 template <int USE>
 hipError_t run_kept(const int8_t* codes, const swiglu_bf16* scales, const uint16_t* dY, uint16_t* C0, uint16_t* C1,
                     int64_t M, int64_t N, hipStream_t s) {
-    long long units = ceil_div(M, 4) * 2 * ceil_div(N, swt::GROUP);
-    int Mi = (int)M, Ni = (int)N;
-    void* kargs[] = {(void*)&codes, (void*)&scales, (void*)&dY, (void*)&C0, (void*)&C1, &Mi, &Ni, &units};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swt::kept_kernel<USE>),
-                           dim3((unsigned)std::min<int64_t>(ceil_div(units, 256), 16384)), dim3(256), kargs, 0, s);
+    return M * N >= (int64_t)1 << 24 ? run_kept_rows<USE, 4>(codes, scales, dY, C0, C1, M, N, s)
+                                     : run_kept_rows<USE, 1>(codes, scales, dY, C0, C1, M, N, s);
 }
 
 // the weight gradients of an empty batch are zero

@@ -844,67 +844,58 @@ __global__ __launch_bounds__(256) void dgate_kernel(const uint16_t* __restrict__
 }
 
 // What is computed from Gate and Up kept as int8, element by element: D = [dG | dU]
-// from dY, Y = SiLU(G) U, or G and U themselves.  A thread has half a group (16
-// columns) of four rows: their scales lie in one 16-byte piece, and the rows' loads go
+// from dY, Y = SiLU(G) U, or G and U themselves.  A thread has 8 columns of ROWS rows
+// (adjacent threads adjacent columns, so that stores are whole runs), whose loads go
 // out together.  Bound by HBM.
 enum KeptUse : int { KEPT_D = 0, KEPT_Y = 1, KEPT_GU = 2 };
-template <int USE>
+template <int USE, int ROWS>
 __global__ __launch_bounds__(256) void kept_kernel(const uint8_t* __restrict__ codes,
                                                    const uint32_t* __restrict__ scales,
                                                    const uint16_t* __restrict__ dY, uint16_t* __restrict__ C0,
                                                    uint16_t* __restrict__ C1, int M, int N, long long units) {
-    constexpr int ROWS = 4;
-    const int groups = (N + GROUP - 1) / GROUP, halves = 2 * groups;
+    const int groups = (N + GROUP - 1) / GROUP, per_row = N / 8;
     for (long long t = (long long)blockIdx.x * 256 + threadIdx.x; t < units; t += (long long)gridDim.x * 256) {
-        const int m0 = (int)(t / halves) * ROWS, hg = (int)(t % halves);
-        const int g = hg >> 1, n = hg * 16;
-        if (n >= N) continue;
-        const bool second = n + 8 < N;   // the half group's columns 8 .. 15
-        u32x4 cg[ROWS], cu[ROWS], dy[ROWS][2];
+        const int m0 = (int)(t / per_row) * ROWS, c = (int)(t % per_row);
+        const int g = c >> 2, n = c * 8;
+        u32x2 cg[ROWS], cu[ROWS];
+        u32x4 dy[ROWS];
         unsigned s[ROWS];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int m = min(m0 + r, M - 1);
-            const uint8_t* c = codes + ((size_t)m * groups + g) * 64 + 16 * (hg & 1);
-            cg[r] = *reinterpret_cast<const u32x4*>(c);
-            cu[r] = *reinterpret_cast<const u32x4*>(c + 32);
+            const uint8_t* q = codes + ((size_t)m * groups + g) * 64 + 8 * (c & 3);
+            cg[r] = *reinterpret_cast<const u32x2*>(q);
+            cu[r] = *reinterpret_cast<const u32x2*>(q + 32);
             s[r] = scales[(size_t)g * M + m];
-            if constexpr (USE == KEPT_D) {
-                const uint16_t* d = dY + (size_t)m * N + n;
-                dy[r][0] = ld16(d);
-                dy[r][1] = second ? ld16(d + 8) : u32x4{0u, 0u, 0u, 0u};
-            }
+            if constexpr (USE == KEPT_D) dy[r] = ld16(dY + (size_t)m * N + n);
         }
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
             const int m = m0 + r;
             if (m >= M) break;
             const float sg = __builtin_bit_cast(float, s[r] << 16), su = __builtin_bit_cast(float, s[r] & 0xFFFF0000u);
+            float gv[8], uv[8], x[8], y[8];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float gv[8], uv[8], x[8], y[8];
-                code_values(cg[r][2 * h], sg, gv);
-                code_values(cg[r][2 * h + 1], sg, gv + 4);
-                code_values(cu[r][2 * h], su, uv);
-                code_values(cu[r][2 * h + 1], su, uv + 4);
-                if constexpr (USE == KEPT_D) {
-                    float d[8];
-                    unpack8(dy[r][h], d);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) silu_grad(d[e], gv[e], uv[e], x[e], y[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = USE == KEPT_Y ? silu_f(gv[e]) * uv[e] : gv[e];
-                        y[e] = uv[e];
-                    }
-                }
-                if (h == 1 && !second) continue;
-                const size_t at = (size_t)m * (USE == KEPT_D ? 2 * (size_t)N : (size_t)N) + n + 8 * h;
-                st16(C0 + at, pack8(x));
-                if constexpr (USE == KEPT_D) st16(C0 + at + N, pack8(y));
-                if constexpr (USE == KEPT_GU) st16(C1 + at, pack8(y));
+                code_values(cg[r][h], sg, gv + 4 * h);
+                code_values(cu[r][h], su, uv + 4 * h);
             }
+            if constexpr (USE == KEPT_D) {
+                float d[8];
+                unpack8(dy[r], d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) silu_grad(d[e], gv[e], uv[e], x[e], y[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = USE == KEPT_Y ? silu_f(gv[e]) * uv[e] : gv[e];
+                    y[e] = uv[e];
+                }
+            }
+            const size_t at = (size_t)m * (USE == KEPT_D ? 2 * (size_t)N : (size_t)N) + n;
+            st16(C0 + at, pack8(x));
+            if constexpr (USE == KEPT_D) st16(C0 + at + N, pack8(y));
+            if constexpr (USE == KEPT_GU) st16(C1 + at, pack8(y));
         }
     }
 }
