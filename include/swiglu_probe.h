@@ -53,10 +53,11 @@ int swiglu_probe_train_plan(int launch, int64_t M, int64_t K, int64_t N, int32_t
 
 /* How an int8 product is run at (M,K,N) on the current device (host call; gemm: 0 the
  * fused product, 1 one weight): plan receives the kernel (0 decode, 1 few rows, 2 many
- * rows), a tile's rows, its packed weight rows and the parts that K is split into.
- * Returns 1, or 0 for a shape that the calls refuse, M == 0 or plan NULL. */
+ * rows), a tile's rows, its packed weight rows, the parts that K is split into and
+ * whether its weights are loaded non-temporally.  Returns 1, or 0 for a shape that the
+ * calls refuse, M == 0 or plan NULL. */
 int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N,
-                           int32_t *plan);
+                           int32_t plan[5]);
 
 #ifdef __cplusplus
 }

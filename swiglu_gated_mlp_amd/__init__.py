@@ -735,11 +735,12 @@ def swiglu_probe_train_plan(launch: str, M: int, K: int, N: int) -> list:
 def swiglu_probe_int8_plan(gemm: bool, M: int, K: int, N: int) -> dict:
     """How an int8 product (gemm: of one weight) is run at (M,K,N): the kernel
     ("decode", "narrow", "stream"), a tile's rows and packed weight rows, the parts
-    that K is split into."""
-    out = (ctypes.c_int32 * 4)()
+    that K is split into, whether the weights are loaded non-temporally."""
+    out = (ctypes.c_int32 * 5)()
     if lib().swiglu_probe_int8_plan(int(bool(gemm)), M, K, N, out) == 0:
         raise ValueError("invalid shape M=%d K=%d N=%d" % (M, K, N))
-    return dict(kernel=("decode", "narrow", "stream")[out[0]], rows=out[1], cols=out[2], splits=out[3])
+    return dict(kernel=("decode", "narrow", "stream")[out[0]], rows=out[1], cols=out[2], splits=out[3],
+                once=bool(out[4]))
 
 
 # training (gradients and differentiable forms of the product and the block)

@@ -68,43 +68,53 @@ bool in_chunks(int64_t M, int64_t K) { return M > stream_rows_limit(K, 1); }
 // fastest.
 //   The estimates are microseconds of a launch on an idle device with the weights in
 // HBM and the caches full of something else's outputs, and only their order matters.
-// Fitted to this chip over 126 shapes (33 .. 4096 rows, K 896 .. 29568, N 896 .. 29568)
-// with every tile and up to 16 parts: off by 8 % in the root mean square, and the
-// choice costs 2 % over the best on average.
+// Fitted to this chip over 126 shapes (33 .. 2048 rows, K 896 .. 29568, N 896 .. 29568)
+// with every tile and up to 16 parts, and to the same launches one after another: off
+// by 10 % in the root mean square, and the choice costs 2 to 3 % over the best on
+// average.
 // ---------------------------------------------------------------------------
 struct Plan8 {
     enum How { DECODE, NARROW, STREAM } how;
     int cus;
     Plan stream;            // STREAM: 256-row tiles, or (panels > 0) one row of them on panels
     int tile;               // NARROW: index into kNarrow
+    bool once;              // weights loaded non-temporally
     int units, tiles_m, groups, splits, kb_per_split;
     size_t part_bytes;
 };
 
-// rows and 32-row weight blocks of a workgroup, microseconds outside the stages, and a
-// stage (128 k) on a CU that has one workgroup.
+// Tiles: rows, waves and 32-row weight blocks a wave.  Counts of waves that divide no
+// power of two fill the CUs where the others leave a round nearly empty: 7B width, 128
+// rows, fused <128,4,2> 33, <128,6,1> 30, 64 rows <64,4,1> 30, <64,5,1> 25 us.  Without
+// the fused product's 6 and 5 the choice costs 4 % over the best on average, with one
+// tile of each height 9 %.  One weight gains nothing from them.
 struct NarrowTile {
-    int bm, blocks;
-    double once, stage;
+    int bm, waves, wt;
+    bool gemm;
+    int blocks() const { return waves * wt; }
+    // microseconds outside the stages, and a stage (128 k) on a CU that has one workgroup
+    double once() const { return bm == 128 ? 8.9 : 8.2; }
+    double stage() const { return bm == 128 ? 0.2 + 0.052 * blocks() : 0.07 + 0.063 * blocks(); }
 };
-constexpr NarrowTile kNarrow[3] = {{128, 8, 9.3, 0.69}, {128, 4, 8.4, 0.48}, {64, 4, 8.6, 0.39}};
+constexpr NarrowTile kNarrow[] = {{128, 4, 2, true}, {128, 3, 1, true}, {128, 6, 1, false},
+                                  {64, 4, 1, true},  {64, 3, 1, true},  {64, 5, 1, false}};
 
 // A CU's stages, the weights from HBM and the matrix cores overlap in part.
 double overlapped(double cu, double hbm, double mfma) { return std::sqrt(cu * cu + hbm * hbm + mfma * mfma); }
 
-// work items on the CUs: in rounds, evened out from two on
+// work items on the CUs: in rounds, which run into each other from three on
 double rounds_of(int64_t items, int cus) {
-    return items > 2 * (int64_t)cus ? (double)items / cus : (double)ceil_div(items, cus);
+    return items > 3 * (int64_t)cus ? (double)items / cus + 0.3 : (double)ceil_div(items, cus);
 }
 
 double narrow_us(const Plan8& p, int64_t K, int64_t M) {
     const NarrowTile& t = kNarrow[p.tile];
     const int64_t items = (int64_t)p.tiles_m * p.groups * p.splits;
-    const double rows = (double)p.groups * t.blocks * 32;   // packed
-    return t.once +
-           overlapped(rounds_of(items, p.cus) * p.kb_per_split * t.stage, (rows + M) * K / 7.6e6,
-                      2.0 * p.tiles_m * t.bm * rows * K / 2.95e9) +
-           (p.splits > 1 ? 2.0 + p.part_bytes / 3.1e6 : 0.0);
+    const double rows = (double)p.groups * t.blocks() * 32;   // packed
+    return t.once() +
+           overlapped(rounds_of(items, p.cus) * p.kb_per_split * t.stage(), (rows + M) * K / 7.9e6,
+                      2.0 * p.tiles_m * t.bm * rows * K / 2.28e9) +
+           (p.splits > 1 ? 2.5 + p.part_bytes / 3.6e6 : 0.0);
 }
 
 double stream_us(const Plan& p, int64_t M, int64_t K) {
@@ -155,18 +165,22 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
         best_us = decode_us(gemm, KB, gemm ? gemm_tiled_cols(N) : N, best.cus);
     }
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 16};
-    for (int i = 0; i < 3; ++i) {
+    for (const NarrowTile& t : kNarrow) {
+        if (gemm && !t.gemm) continue;
         Plan8 p = best;
         p.how = Plan8::NARROW;
-        p.tile = i;
-        p.units = (int)(gemm && i == 0 ? 4 * ceil_div(N, swk::PACK_ROWS) : ceil_div(N, 32));
-        p.tiles_m = (int)ceil_div(M, kNarrow[i].bm);
-        p.groups = (int)ceil_div(p.units, gemm || i == 0 ? 4 : 2);
+        p.tile = (int)(&t - kNarrow);
+        // a wave's share of the columns (see Narrow)
+        p.units = (int)(gemm && t.wt == 2 ? 4 * ceil_div(N, swk::PACK_ROWS) : ceil_div(N, gemm || t.wt == 2 ? 32 : 16));
+        p.tiles_m = (int)ceil_div(M, t.bm);
+        p.groups = (int)ceil_div(p.units, t.waves);
+        // weights that fit the last-level cache beside others stay there; see Narrow::ONCE
+        p.once = (int64_t)p.groups * t.blocks() * 32 * KB * 128 > ((int64_t)32 << 20) && p.tiles_m <= (t.bm == 64 ? 2 : 4);
         for (int s : kSplits) {
             if (s > 1 && 3 * s > KB) break;
             p.kb_per_split = (int)ceil_div(KB, s);
             p.splits = (int)ceil_div(KB, p.kb_per_split);
-            p.part_bytes = p.splits > 1 ? (size_t)p.splits * p.groups * p.tiles_m * kNarrow[i].blocks * kNarrow[i].bm * 128
+            p.part_bytes = p.splits > 1 ? (size_t)p.splits * p.groups * p.tiles_m * t.blocks() * t.bm * 128
                                         : 0;
             const double us = narrow_us(p, K, M);
             if (us < best_us) {
@@ -239,27 +253,23 @@ hipError_t run_decode(const swk::DecodeArgs& d, int64_t nt, int cus, hipStream_t
     }
 }
 
-template <int BM, int WT, bool GEMM, bool ONCE>
+template <int BM, int WAVES, int WT, bool GEMM, bool ONCE>
 hipError_t launch_narrow_as(const swq::NarrowArgs& a, hipStream_t s) {
-    using P = swq::Narrow<BM, 4, WT, 4, GEMM, ONCE>;
+    using P = swq::Narrow<BM, WAVES, WT, 4, GEMM, ONCE>;
     if (a.splits > 1 && !a.part) return hipErrorInvalidValue;
     swq::NarrowArgs args = a;
     void* kargs[] = {&args};
     const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_kernel<P>),
-                                         dim3((unsigned)(a.tiles_m * a.groups * a.splits)), dim3(64 * P::WAVES), kargs, 0,
-                                         s);
+                                         dim3((unsigned)(a.tiles_m * a.groups * a.splits)), dim3(64 * WAVES), kargs, 0, s);
     if (e != hipSuccess || a.splits == 1) return e;
-    const int64_t jobs = (int64_t)a.tiles_m * a.groups * P::UNITS * (P::GEMM ? P::WT : 1) * P::TM;
+    const int64_t jobs = (int64_t)a.tiles_m * a.groups * WAVES * (GEMM ? WT : 1) * P::TM;
     return hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_reduce_kernel<P>),
                            dim3((unsigned)ceil_div(jobs, 4)), dim3(256), kargs, 0, s);
 }
 
-template <int BM, int WT, bool GEMM>
-hipError_t launch_narrow(const swq::NarrowArgs& a, hipStream_t s) {
-    // weights that fit the last-level cache beside others stay there; see Narrow::ONCE
-    const int64_t bytes = (int64_t)a.groups * 4 * WT * 32 * a.KB * 128;
-    const bool once = bytes > ((int64_t)32 << 20) && a.tiles_m <= (BM == 64 ? 2 : 4);
-    return once ? launch_narrow_as<BM, WT, GEMM, true>(a, s) : launch_narrow_as<BM, WT, GEMM, false>(a, s);
+template <int BM, int WAVES, int WT, bool GEMM>
+hipError_t launch_narrow(const swq::NarrowArgs& a, bool once, hipStream_t s) {
+    return once ? launch_narrow_as<BM, WAVES, WT, GEMM, true>(a, s) : launch_narrow_as<BM, WAVES, WT, GEMM, false>(a, s);
 }
 
 template <bool GEMM>
@@ -272,11 +282,17 @@ hipError_t run_rows(const Product8& q, const Plan8& p, hipStream_t s) {
         a.M = (int)q.M; a.K = (int)q.K; a.N = (int)q.N; a.KB = (int)ceil_div(q.K, 128);
         a.units = p.units; a.tiles_m = p.tiles_m; a.groups = p.groups;
         a.splits = p.splits; a.kb_per_split = p.kb_per_split;
-        switch (p.tile) {
-            case 0: return launch_narrow<128, 2, GEMM>(a, s);
-            case 1: return launch_narrow<128, 1, GEMM>(a, s);
-            default: return launch_narrow<64, 1, GEMM>(a, s);
+        const NarrowTile& t = kNarrow[p.tile];
+        if (t.bm == 128) {
+            if (t.wt == 2) return launch_narrow<128, 4, 2, GEMM>(a, p.once, s);
+            if (t.waves == 3) return launch_narrow<128, 3, 1, GEMM>(a, p.once, s);
+            if constexpr (!GEMM) return launch_narrow<128, 6, 1, false>(a, p.once, s);
+        } else {
+            if (t.waves == 4) return launch_narrow<64, 4, 1, GEMM>(a, p.once, s);
+            if (t.waves == 3) return launch_narrow<64, 3, 1, GEMM>(a, p.once, s);
+            if constexpr (!GEMM) return launch_narrow<64, 5, 1, false>(a, p.once, s);
         }
+        return hipErrorInvalidValue;
     }
     const uint16_t* A = reinterpret_cast<const uint16_t*>(q.A);
     const uint16_t* W = reinterpret_cast<const uint16_t*>(q.W);
@@ -525,9 +541,9 @@ int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N, int32_t* p
     const Plan8 p = plan_int8(gemm != 0, M, K, N);
     const bool narrow = p.how == Plan8::NARROW;
     const int rows = p.how == Plan8::DECODE ? (M <= 16 ? 16 : M <= 32 ? 32 : 64) : narrow ? kNarrow[p.tile].bm : 256;
-    const int cols = narrow ? 32 * kNarrow[p.tile].blocks : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
-    const int32_t v[4] = {p.how, rows, cols, narrow ? p.splits : 1};
-    std::copy(v, v + 4, plan);
+    const int cols = narrow ? 32 * kNarrow[p.tile].blocks() : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
+    const int32_t v[5] = {p.how, rows, cols, narrow ? p.splits : 1, narrow && p.once};
+    std::copy(v, v + 5, plan);
     return 1;
 }
 

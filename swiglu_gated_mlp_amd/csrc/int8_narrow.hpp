@@ -5,22 +5,22 @@
 // against 35 GOP, which the matrix cores do in a third of the time), and a CU reaches
 // its share of HBM's rate only with some 50 KB in flight.  So
 //  - a workgroup takes BM rows and WAVES x WT blocks of 32 packed weight rows, and a
-//    part of the contraction such that all CUs have one or two workgroups;
+//    part of the contraction, such that all CUs have about as much to do;
 //  - the activations go through a ring of NBUF stages (128 k) in LDS, the weights
 //    straight to registers (each is needed by one wave), both NBUF - 1 stages ahead;
 //  - parts leave their int32 sums in the lanes' own order (1 KiB runs), and a second
 //    launch adds them: whole numbers, so in any order the same.
 // WT 2: a wave has the Gate and the Up block of the same 32 columns (or, GEMM, columns
-// 128 apart of one weight).  WT 1: one block; the fused product's first half of the
-// waves have Gate blocks, the other half the Up blocks of the same columns, and they
-// exchange sums through LDS at the end, each finishing half of the rows.
+// 128 apart of one weight).  WT 1: one block; the fused product's holds the Gate and Up
+// rows of 16 columns, so that a lane has both sums of a column.
 // ONCE: weights that no or few other row tiles read are loaded non-temporally: they
 // then displace nothing from the caches, and where these hold another kernel's outputs
-// nothing waits for those to be written back.  us at 7B width after 1 GB was written /
-// after the same kernel on other weights: fused 33 rows 51 -> 32 / 30 -> 30, 128 rows
-// 54 -> 42 / 35 -> 34, one weight, 512 rows in four tiles 56 -> 49 / 46 -> 45; but three
-// tiles of 64 rows (K=4096 N=11008) 45 -> 53 / 37 -> 48, and a product whose 9 MB of
-// weights stay in the last-level cache (0.5B width, 256 rows) 13 -> 12 / 8.1 -> 9.5.
+// nothing waits for those to be written back.  us after 1 GB was written / after the
+// same kernel on other weights: fused at 7B width 33 rows 49 -> 27 / 27 -> 24, 128 rows
+// 52 -> 35 / 31 -> 30, at 72B width 131 -> 81 / 93 -> 79, one weight of 7B width, 512
+// rows in four tiles 56 -> 50 / 44 -> 44; but five tiles of 64 rows (one weight, K=4096
+// N=11008) 37 -> 34 / 28 -> 30, and a product whose 9 MB of weights stay in the
+// last-level cache (0.5B width, 256 rows) 12.0 -> 11.7 / 6.9 -> 8.4.
 #pragma once
 
 #include "fused_kernels.hpp"
@@ -39,8 +39,8 @@ struct NarrowArgs {
     int* part;             // splits > 1: the parts' sums, [split][tile][block][quad][lane][4]
     int M, K, N;
     int KB;                // ceil(K / 128)
-    int units;             // GEMM: of WT blocks; fused: of a Gate and an Up block
-    int tiles_m, groups;   // row tiles, groups of P::UNITS units
+    int units;             // waves' shares of the columns: 32, WT 2 GEMM 2 x 32, PAIR 16
+    int tiles_m, groups;   // row tiles, groups of WAVES units
     int splits, kb_per_split;
 };
 
@@ -50,10 +50,7 @@ struct Narrow {
     static constexpr bool GEMM = GEMM_, ONCE = ONCE_;
     static constexpr int TM = BM / 32;
     static constexpr int BLOCKS = WAVES * WT * TM;   // 32 x 32 blocks of a tile
-    static constexpr bool EXCHANGE = !GEMM && WT == 1;
-    static constexpr int UNITS = EXCHANGE ? WAVES / 2 : WAVES;   // of a workgroup
-    // finishing an exchanged tile: the rows' blocks a wave keeps
-    static constexpr int HALF = EXCHANGE ? (TM + 1) / 2 : TM;
+    static constexpr bool PAIR = !GEMM && WT == 1;   // Gate and Up rows of 16 columns in a block
 };
 
 template <int... Q, class F>
@@ -67,13 +64,19 @@ using Upto = std::make_integer_sequence<int, N>;
 template <class P>
 __device__ __forceinline__ int narrow_column(int u, int t) {
     if constexpr (P::GEMM && P::WT == 2) return (u >> 2) * PACK_ROWS + (u & 3) * 32 + PACK_BN * t;
-    else return 32 * u;
+    else return (P::PAIR ? 16 : 32) * u;
 }
 
-// The columns' scales of a block, as its sums lie in the lanes.
-__device__ __forceinline__ void narrow_scales(const float* s, int n, int N, int lane, f32x4 (&c)[4]) {
+// The columns' scales of a block, as its sums lie in the lanes (PAIR: of W1 for q = 0,
+// 1, of W2 for 2, 3).
+template <class P>
+__device__ __forceinline__ void narrow_scales(const NarrowArgs& p, int u, int t, int lane, f32x4 (&c)[4]) {
+    const int n = narrow_column<P>(u, t) + 4 * (lane >> 5);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) c[q] = scales4(s, n + 8 * q + 4 * (lane >> 5), N);
+    for (int q = 0; q < 4; ++q) {
+        if constexpr (P::PAIR) c[q] = scales4(q < 2 ? p.s1 : p.s2, n + 8 * (q & 1), p.N);
+        else c[q] = scales4(P::GEMM || t == 0 ? p.s1 : p.s2, n + 8 * q, p.N);
+    }
 }
 
 // Block at rows m0 + .., columns n + .. : scaled, finished, stored.
@@ -96,6 +99,28 @@ template <class P>
 __device__ __forceinline__ void narrow_finish(const NarrowArgs& p, int u, int t, int m0, int lane, const i32x16& x,
                                               const i32x16& y, const f32x4 (&cx)[4], const f32x4 (&cy)[4],
                                               float row) {
+    if constexpr (P::PAIR) {
+        unsigned d[2][2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                float v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 4 * q + 2 * w + e;
+                    v[e] = silu_f(scaled(x[i], cx[q][2 * w + e], row)) * scaled(x[i + 8], cx[q + 2][2 * w + e], row);
+                }
+                d[q][w] = pack2(v[0], v[1]);
+            }
+        // columns 4 (l >> 5) + 0 .. 3 and the same + 8 to 8 (l >> 5) + 0 .. 7
+        swap32(d[0][0], d[1][0]);
+        swap32(d[0][1], d[1][1]);
+        const int m = m0 + (lane & 31), n = narrow_column<P>(u, 0) + 8 * (lane >> 5);
+        if (m < p.M && n < p.N)
+            *reinterpret_cast<u32x4*>(p.Y + (size_t)m * p.N + n) = u32x4{d[0][0], d[0][1], d[1][0], d[1][1]};
+        return;
+    }
     float v[16];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -110,16 +135,17 @@ __device__ __forceinline__ void narrow_finish(const NarrowArgs& p, int u, int t,
 template <class P>
 __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
     constexpr int BM = P::BM, WAVES = P::WAVES, WT = P::WT, NBUF = P::NBUF, TM = P::TM;
-    constexpr int A_INS = BM / 8 / WAVES;          // 1 KiB loads of activations per wave and stage
+    constexpr int A_ALL = BM / 8;                  // 1 KiB loads of activations a stage,
+    constexpr int A_INS = (A_ALL + WAVES - 1) / WAVES;   // of them a wave's (past the last: into a spare slot)
     constexpr int LOADS = A_INS + 4 * WT;          // loads per wave and stage
     constexpr int LPS = (LOADS + 3) / 4;           // of them per sub-step
     constexpr int LATE = LOADS < 3 * LPS ? LOADS : 3 * LPS;   // in the first three sub-steps
     constexpr int ASTAGE = BM * 128;               // bytes
-    static_assert(A_INS >= 1 && BM % (8 * WAVES) == 0, "tile");
+    constexpr bool SPARE = A_ALL % WAVES != 0;
+    static_assert(BM % 32 == 0, "tile");
     static_assert(NBUF >= 3 && NBUF * ASTAGE <= 163840, "LDS");
     static_assert((NBUF - 3) * LOADS + LATE <= 63 && (NBUF - 2) * LOADS <= 63, "vmcnt range");
-    constexpr int EXBYTES = P::EXCHANGE ? WAVES * P::HALF * 4096 : 0;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[NBUF * ASTAGE > EXBYTES ? NBUF * ASTAGE : EXBYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NBUF * ASTAGE + (SPARE ? 1024 : 0)];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -131,8 +157,7 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
     const int m0 = tm * BM;
     const int kb0 = split * p.kb_per_split;
     const int ns = min(p.KB, kb0 + p.kb_per_split) - kb0;
-    const bool up = P::EXCHANGE && wave >= P::UNITS;
-    const int u_own = grp * P::UNITS + (up ? wave - P::UNITS : wave);
+    const int u_own = grp * WAVES + wave;
     const int u = min(u_own, p.units - 1);         // a wave without a unit repeats the last one
 
     // lane l of activation load i: row (wave A_INS + i) 8 + l / 8, 16-byte chunk
@@ -141,16 +166,17 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
     int a_k[A_INS];
 #pragma unroll
     for (int i = 0; i < A_INS; ++i) {
-        const int r = (wave * A_INS + i) * 8 + (lane >> 3);
+        const int r = min(wave * A_INS + i, A_ALL - 1) * 8 + (lane >> 3);
         a_k[i] = 16 * ((lane & 7) ^ swz(r));
         a_off[i] = (uint32_t)((size_t)min(m0 + r, p.M - 1) * p.K);
     }
     // weights: fragment (t, kk) of a block of 128 k; see packed_off
-    const uint32_t w_lane = (uint32_t)(((lane >> 4) & 1) * 2048 + (lane >> 5) * 256 + (lane & 15) * 16);
-    constexpr bool EIGHT = P::GEMM && WT == 1;     // units of a packed tile: 8, or 4
-    const char* w_base = reinterpret_cast<const char*>(p.W) +
-                         ((size_t)(EIGHT ? u >> 3 : u >> 2) * p.KB + kb0) * 32768 +
-                         (EIGHT ? (u & 7) : (u & 3) + (up ? 4 : 0)) * 4096;
+    // (two adjacent groups of 16 packed rows a block; PAIR: a Gate group and its Up group)
+    const uint32_t w_lane =
+        (uint32_t)(((lane >> 4) & 1) * (P::PAIR ? 16384 : 2048) + (lane >> 5) * 256 + (lane & 15) * 16);
+    constexpr int EACH = WT == 1 ? 8 : 4;          // units of a packed tile
+    const char* w_base = reinterpret_cast<const char*>(p.W) + ((size_t)(u / EACH) * p.KB + kb0) * 32768 +
+                         (u % EACH) * (P::PAIR ? 2048 : 4096);
 
     bf16x8 wf[NBUF][WT][4];
 #pragma unroll
@@ -177,8 +203,9 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
             // k past the end: any byte will do, its weights are zero
             const char* b = valid ? reinterpret_cast<const char*>(p.A) : zero;
             const uint32_t k = (uint32_t)min((kb0 + ls) * 128 + a_k[i], p.K - 16);
+            const int to = SPARE && wave * A_INS + i >= A_ALL ? NBUF * ASTAGE : SET * ASTAGE + (wave * A_INS + i) * 1024;
             dma16(reinterpret_cast<const uint16_t*>(b + ((a_off[i] + k) & mask)),
-                  reinterpret_cast<uint16_t*>(smem + SET * ASTAGE + (wave * A_INS + i) * 1024));
+                  reinterpret_cast<uint16_t*>(smem + to));
         }
     };
     // fragment reads: row 32 i + (l & 31), chunk 2 kk + (l >> 5), swizzled
@@ -234,11 +261,10 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
     };
 
     // the scales, first of all loads (parts need none)
-    constexpr int NC = P::GEMM ? WT : 2;
-    f32x4 cs[NC][4];
+    f32x4 cs[WT][4];
     float rs[TM];
 #pragma unroll
-    for (int t = 0; t < NC; ++t) narrow_scales(P::GEMM || t == 0 ? p.s1 : p.s2, narrow_column<P>(u, t), p.N, lane, cs[t]);
+    for (int t = 0; t < WT; ++t) narrow_scales<P>(p, u, t, lane, cs[t]);
 #pragma unroll
     for (int i = 0; i < TM; ++i) rs[i] = p.sa[min(m0 + 32 * i + (lane & 31), p.M - 1)];
     each(Upto<NBUF - 1>{}, [&](auto qc) __attribute__((always_inline)) {
@@ -248,7 +274,7 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((NBUF - 2) * LOADS, 0));
     __builtin_amdgcn_s_barrier();
 #pragma unroll
-    for (int t = 0; t < NC; ++t)
+    for (int t = 0; t < WT; ++t)
 #pragma unroll
         for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(cs[t][q]));
 #pragma unroll
@@ -285,38 +311,6 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
                         i32x4{acc[t][i][4 * q], acc[t][i][4 * q + 1], acc[t][i][4 * q + 2], acc[t][i][4 * q + 3]};
         return;
     }
-    if constexpr (P::EXCHANGE) {
-        // Gate waves keep the first HALF row blocks and take their Up sums, Up waves the
-        // others and their Gate sums
-        __builtin_amdgcn_s_barrier();   // every wave's loads to LDS have landed, its reads are done
-        auto at = [&](int w, int i) { return reinterpret_cast<int*>(smem) + (w * P::HALF + i) * 1024 + lane * 4; };
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            if (up != (i < P::HALF)) continue;
-            int* d = at(wave, i < P::HALF ? i : i - P::HALF);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<i32x4*>(d + q * 256) =
-                    i32x4{acc[0][i][4 * q], acc[0][i][4 * q + 1], acc[0][i][4 * q + 2], acc[0][i][4 * q + 3]};
-        }
-        __syncthreads();
-        if (u_own >= p.units) return;
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            if (up == (i < P::HALF)) continue;
-            const int* d = at(up ? wave - P::UNITS : wave + P::UNITS, i < P::HALF ? i : i - P::HALF);
-            i32x16 o;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const i32x4 v = *reinterpret_cast<const i32x4*>(d + q * 256);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[4 * q + e] = v[e];
-            }
-            if (up) narrow_finish<P>(p, u, 0, m0 + 32 * i, lane, o, acc[0][i], cs[0], cs[NC - 1], rs[i]);
-            else narrow_finish<P>(p, u, 0, m0 + 32 * i, lane, acc[0][i], o, cs[0], cs[NC - 1], rs[i]);
-        }
-        return;
-    }
     if (u_own >= p.units) return;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -334,9 +328,8 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
 template <class P>
 __global__ __launch_bounds__(256) void narrow_reduce_kernel(NarrowArgs p) {
     constexpr int TM = P::TM, JB = P::GEMM ? P::WT : 1;
-    constexpr int JOBS = P::UNITS * JB * TM;       // of a tile
-    // from a Gate block to its Up block
-    constexpr int TO_UP = (P::EXCHANGE ? P::UNITS : 1) * TM * 1024;
+    constexpr int JOBS = P::WAVES * JB * TM;       // of a tile
+    constexpr bool TWO = !P::GEMM && P::WT == 2;   // a Gate block, and its Up block behind the unit's others
     const int lane = threadIdx.x & 63;
     const int id = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tile = id / JOBS, job = id - tile * JOBS;
@@ -344,12 +337,11 @@ __global__ __launch_bounds__(256) void narrow_reduce_kernel(NarrowArgs p) {
     if (tile >= tiles) return;
     const int grp = tile / p.tiles_m, tm = tile - grp * p.tiles_m;
     const int wave = job / (JB * TM), t = job / TM % JB, i = job % TM;
-    const int u = grp * P::UNITS + wave, m0 = tm * P::BM + 32 * i;
+    const int u = grp * P::WAVES + wave, m0 = tm * P::BM + 32 * i;
     if (u >= p.units || m0 >= p.M) return;
-    const int n = narrow_column<P>(u, t);
     f32x4 cx[4], cy[4];
-    narrow_scales(p.s1, n, p.N, lane, cx);
-    if constexpr (!P::GEMM) narrow_scales(p.s2, n, p.N, lane, cy);
+    narrow_scales<P>(p, u, t, lane, cx);
+    if constexpr (TWO) narrow_scales<P>(p, u, 1, lane, cy);
     const float row = p.sa[min(m0 + (lane & 31), p.M - 1)];
     i32x16 x, y;
 #pragma unroll
@@ -363,14 +355,14 @@ __global__ __launch_bounds__(256) void narrow_reduce_kernel(NarrowArgs p) {
             const i32x4 v = *reinterpret_cast<const i32x4*>(src + q * 256);
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[4 * q + e] += v[e];
-            if constexpr (!P::GEMM) {
-                const i32x4 w = *reinterpret_cast<const i32x4*>(src + TO_UP + q * 256);
+            if constexpr (TWO) {
+                const i32x4 w = *reinterpret_cast<const i32x4*>(src + TM * 1024 + q * 256);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[4 * q + e] += w[e];
             }
         }
     }
-    narrow_finish<P>(p, u, t, m0, lane, x, y, cx, P::GEMM ? cx : cy, row);
+    narrow_finish<P>(p, u, t, m0, lane, x, y, cx, TWO ? cy : cx, row);
 }
 
 }  // namespace swq

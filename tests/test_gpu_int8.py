@@ -191,7 +191,10 @@ SHAPES = [(1, 16, 8), (1, 896, 4864), (4, 1040, 520), (5, 2064, 520), (7, 144, 1
           (513, 1040, 904), (655, 144, 19880), (656, 2544, 10192), (972, 144, 29584), (1100, 2000, 4872),
           (1159, 1600, 10816), (1196, 2576, 12472), (1300, 3600, 18952), (1816, 2576, 264), (1800, 3600, 18952),
           (2100, 1024, 9000), (2706, 7216, 72), (2729, 14912, 400), (100, 16000, 520), (200, 16000, 1000),
-          (1030, 4112, 1000)]
+          (1030, 4112, 1000), (33, 18416, 1056), (174, 16, 5160), (33, 1232, 14568), (259, 6368, 56), (36, 7408, 4128),
+          (65, 23584, 1040), (73, 13408, 1624), (334, 10736, 1432), (70, 11952, 4144), (1513, 15248, 256),
+          (69, 19024, 6264), (70, 2576, 12960), (35, 5984, 8320), (66, 10032, 4360), (1359, 14736, 488),
+          (65, 15200, 8368)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -209,15 +212,16 @@ def test_every_kernel_is_met(dev):
     for gemm in (False, True):
         for shape in SHAPES:
             p = sw.swiglu_probe_int8_plan(gemm, *shape)
-            met.add((gemm, p["kernel"], p["rows"], p["cols"], p["splits"] > 1))
+            met.add((gemm, p["kernel"], p["rows"], p["cols"], p["splits"] > 1, p["once"]))
     for gemm in (False, True):
-        for tile in ((64, 128), (128, 128), (128, 256)):
+        for tile in ((64, 96), (64, 128), (128, 96), (128, 256)) + (() if gemm else ((64, 160), (128, 192))):
             for parts in (False, True):
-                assert (gemm, "narrow") + tile + (parts,) in met, (gemm, tile, parts)
+                for once in (False, True):
+                    assert (gemm, "narrow") + tile + (parts, once) in met, (gemm, tile, parts, once)
         for rows in (16, 32, 64):
-            assert (gemm, "decode", rows, 256, False) in met
-        assert (gemm, "stream", 256, 256, False) in met
-    assert (False, "stream", 256, 64, False) in met
+            assert (gemm, "decode", rows, 256, False, False) in met
+        assert (gemm, "stream", 256, 256, False, False) in met
+    assert (False, "stream", 256, 64, False, False) in met
 
 
 @pytest.mark.parametrize("M", [1, 40, 100, 300])
