@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _dev_bf16, _empty, _new, _ptr, _scratch, _shape, _stream, lib
+from . import _check, _empty, _new, _ptr, _scratch, _shape, _stream, lib
 
 _need: dict = {}
 
@@ -40,17 +40,35 @@ def swiglu_mlp_workspace_bytes_int8(M: int, K: int, N: int) -> int:
     return int(lib().swiglu_mlp_workspace_bytes_int8(M, K, N))
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _dev(t, dtype, name: str) -> int:
-    """A contiguous GPU tensor of dtype."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.is_contiguous():
-        return t.data_ptr()
+    """A contiguous tensor of dtype on the current GPU (plans, streams and launches are
+    that device's)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous():
+        device = t.get_device()
+        if device >= 0 and device == _current_device():
+            return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.device.type != "cuda":
         raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s (got %s)" % (name, str(dtype)[6:], t.dtype))
-    raise ValueError("%s must be contiguous" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s is on %s, the current device is %d" % (name, t.device, _current_device()))
+
+
+def _dev_bf16(t, name: str) -> int:
+    return _dev(t, torch.bfloat16, name)
+
+
+def _vector(t, n: int, name: str) -> int:
+    if t.shape != (n,):
+        _shape(t, (n,), name)
+    return _dev(t, torch.float32, name)
 
 
 def _matrix(t, name: str):
@@ -119,15 +137,8 @@ def _weight_at_least(W, sizer, K: int, N: int, name: str) -> None:
     need = _cached(sizer, K, N)
     if need == 0:
         raise ValueError("invalid int8 weight shape [%d,%d]" % (K, N))
-    if W.numel() * W.element_size() < need:
-        raise ValueError("%s holds %d bytes; a packed int8 [%d,%d] weight needs %d"
-                         % (name, W.numel() * W.element_size(), K, N, need))
-
-
-def _vectors(pairs, n: int):
-    for t, name in pairs:
-        _shape(t, (n,), name)
-    return [_dev(t, torch.float32, name) for t, name in pairs]
+    if W.numel() < need:
+        raise ValueError("%s holds %d codes; a packed int8 [%d,%d] weight needs %d" % (name, W.numel(), K, N, need))
 
 
 def _product(fn: str, sizer, need_fn, A, sa, W, wname, scales, out, oname, workspace, stream):
@@ -135,8 +146,8 @@ def _product(fn: str, sizer, need_fn, A, sa, W, wname, scales, out, oname, works
     N = scales[0][0].shape[0]
     _weight_at_least(W, sizer, K, N, wname)
     _shape(out, (M, N), oname)
-    a, (r,) = _dev(A, torch.int8, "A"), _vectors([(sa, "sa")], M)
-    w, cols = _dev(W, torch.int8, wname), _vectors(scales, N)
+    a, r, w = _dev(A, torch.int8, "A"), _vector(sa, M, "sa"), _dev(W, torch.int8, wname)
+    cols = [_vector(t, N, name) for t, name in scales]
     s = _stream(stream)
     out = _new((M, N), A.device, s, stream) if out is None else out
     ws, ws_bytes = _scratch(workspace, _cached(need_fn, M, K, N, device=A.device), A.device, s)
@@ -169,11 +180,10 @@ def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, 
     N = s1.shape[0]
     _weight_at_least(Wp, swiglu_packed_bytes_int8, K, N, "Wp")
     _weight_at_least(W3g, swiglu_gemm_packed_bytes_int8, N, K, "W3g")
-    for t, shape, name in ((Y, (M, N), "Y"), (Z, (M, K), "Z")):
-        _shape(t, shape, name)
+    _shape(Y, (M, N), "Y")
+    _shape(Z, (M, K), "Z")
     a, wp, w3 = _dev_bf16(A, "A"), _dev(Wp, torch.int8, "Wp"), _dev(W3g, torch.int8, "W3g")
-    p1, p2 = _vectors([(s1, "s1"), (s2, "s2")], N)
-    p3, = _vectors([(s3, "s3")], K)
+    p1, p2, p3 = _vector(s1, N, "s1"), _vector(s2, N, "s2"), _vector(s3, K, "s3")
     s = _stream(stream)
     Y = _new((M, N), A.device, s, stream) if Y is None else Y
     Z = _new((M, K), A.device, s, stream) if Z is None else Z

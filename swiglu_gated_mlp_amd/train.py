@@ -17,6 +17,7 @@ import torch
 
 from . import (_check, _dev_bf16, _empty, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
                swiglu_gemm_bf16)
+from .int8 import _dev, _dev_bf16 as _here
 
 _need: dict = {}
 
@@ -141,16 +142,6 @@ def swiglu_train_workspace_bytes_int8(M: int, K: int, N: int) -> int:
     return int(lib().swiglu_train_workspace_bytes_int8(M, K, N))
 
 
-def _dev_int8(t, name: str) -> int:
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.int8 and t.is_contiguous():
-        return t.data_ptr()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int8:
-        raise TypeError("%s must be an int8 tensor" % name)
-    if t.device.type != "cuda":
-        raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
-    raise ValueError("%s must be contiguous" % name)
-
-
 def _kept_shapes(codes, scales, M: int, N: int):
     groups = (N + 31) // 32
     _shape(codes, (M, groups, 2, 32), "codes")
@@ -167,15 +158,15 @@ def swiglu_train_forward_int8(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tenso
     M, K, N = _weights(A, W1, W2)
     _shape(Y, (M, N), "Y")
     groups = _kept_shapes(codes, scales, M, N)
-    a, w1, w2 = _dev_bf16(A, "A"), _dev_bf16(W1, "W1"), _dev_bf16(W2, "W2")
+    a, w1, w2 = _here(A, "A"), _here(W1, "W1"), _here(W2, "W2")
     s = _stream(stream)
     Y = _new((M, N), A.device, s, stream) if Y is None else Y
     if codes is None:
         codes = _empty((M, groups, 2, 32), torch.int8, A.device, s)
     scales = _new((groups, M, 2), A.device, s, stream) if scales is None else scales
     ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, A.device), A.device, s)
-    st = lib().swiglu_train_forward_int8(a, w1, w2, _dev_bf16(Y, "Y"), _dev_int8(codes, "codes"),
-                                         _dev_bf16(scales, "scales"), M, K, N, _ptr(ws), ws_bytes, s)
+    st = lib().swiglu_train_forward_int8(a, w1, w2, _here(Y, "Y"), _dev(codes, torch.int8, "codes"),
+                                         _here(scales, "scales"), M, K, N, _ptr(ws), ws_bytes, s)
     _check("swiglu_train_forward_int8", st)
     return Y, codes, scales
 
@@ -187,11 +178,11 @@ def swiglu_dequantize_kept_int8(codes: torch.Tensor, scales: torch.Tensor, N: in
     _kept_shapes(codes, scales, M, N)
     for t, name in ((G, "G"), (U, "U")):
         _shape(t, (M, N), name)
-    c, sc = _dev_int8(codes, "codes"), _dev_bf16(scales, "scales")
+    c, sc = _dev(codes, torch.int8, "codes"), _here(scales, "scales")
     s = _stream(stream)
     G = _new((M, N), codes.device, s, stream) if G is None else G
     U = _new((M, N), codes.device, s, stream) if U is None else U
-    st = lib().swiglu_dequantize_kept_int8(c, sc, _dev_bf16(G, "G"), _dev_bf16(U, "U"), M, N, s)
+    st = lib().swiglu_dequantize_kept_int8(c, sc, _here(G, "G"), _here(U, "U"), M, N, s)
     _check("swiglu_dequantize_kept_int8", st)
     return G, U
 
@@ -204,13 +195,13 @@ def swiglu_train_backward_int8(dY: torch.Tensor, A: torch.Tensor, W1: torch.Tens
     M, K, N = _weights(A, W1, W2)
     _shape(dY, (M, N), "dY")
     _kept_shapes(codes, scales, M, N)
-    ins = [_dev_bf16(t, n) for t, n in ((dY, "dY"), (A, "A"), (W1, "W1"), (W2, "W2"))]
-    ins += [_dev_int8(codes, "codes"), _dev_bf16(scales, "scales")]
+    ins = [_here(t, n) for t, n in ((dY, "dY"), (A, "A"), (W1, "W1"), (W2, "W2"))]
+    ins += [_dev(codes, torch.int8, "codes"), _here(scales, "scales")]
     s = _stream(stream)
     dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
     dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
     ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, A.device), A.device, s)
-    outs = [0 if t is None else _dev_bf16(t, n) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
+    outs = [0 if t is None else _here(t, n) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
     st = lib().swiglu_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
     _check("swiglu_train_backward_int8", st)
     return dA, dW1, dW2
@@ -227,14 +218,14 @@ def swiglu_mlp_train_backward_int8(dZ: torch.Tensor, A: torch.Tensor, W1: torch.
     _shape(dZ, (M, K), "dZ")
     _shape(W3, (N, K), "W3")
     _kept_shapes(codes, scales, M, N)
-    ins = [_dev_bf16(t, n) for t, n in ((dZ, "dZ"), (A, "A"), (W1, "W1"), (W2, "W2"), (W3, "W3"))]
-    ins += [_dev_int8(codes, "codes"), _dev_bf16(scales, "scales")]
+    ins = [_here(t, n) for t, n in ((dZ, "dZ"), (A, "A"), (W1, "W1"), (W2, "W2"), (W3, "W3"))]
+    ins += [_dev(codes, torch.int8, "codes"), _here(scales, "scales")]
     s = _stream(stream)
     dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
     dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
     dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), A.device, s, stream)
     ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes_int8, M, K, N, A.device), A.device, s)
-    outs = [0 if t is None else _dev_bf16(t, n)
+    outs = [0 if t is None else _here(t, n)
             for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"), (dW3, "dW3"))]
     st = lib().swiglu_mlp_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
     _check("swiglu_mlp_train_backward_int8", st)

@@ -164,3 +164,33 @@ def test_plan_probe():
             with pytest.raises(ValueError, match="invalid shape"):
                 sw.swiglu_probe_int8_plan(gemm, *bad)
     assert sw.lib().swiglu_probe_int8_plan(0, 4, 64, 72, None) == 0
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on the second GPU."""
+    device = torch.device("cuda:1")
+
+    def get_device(self):
+        return 1
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    from swiglu_gated_mlp_amd import int8
+    monkeypatch.setattr(int8, "_current_device", lambda: 0)
+    a8, a = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 64, dtype=torch.bfloat16)
+    w, v, r = torch.zeros(64, 72, dtype=torch.bfloat16), torch.zeros(72), torch.zeros(4)
+    wp = torch.zeros(sw.swiglu_packed_bytes_int8(64, 72), dtype=torch.int8)
+    w8, codes = torch.zeros(64, 72, dtype=torch.int8), torch.zeros(4, 3, 2, 32, dtype=torch.int8)
+    kept, dy = torch.zeros(3, 4, 2, dtype=torch.bfloat16), torch.zeros(4, 72, dtype=torch.bfloat16)
+    w3 = torch.zeros(72, 64, dtype=torch.bfloat16)
+    a8, a, w, w3, v, r, wp, w8, codes, kept, dy = (t.as_subclass(Elsewhere) for t in
+                                                   (a8, a, w, w3, v, r, wp, w8, codes, kept, dy))
+    for call in (lambda: sw.swiglu_quantize_rows_int8(a), lambda: sw.swiglu_quantize_columns_int8(w),
+                 lambda: sw.swiglu_pack_weights_int8(w8, w8), lambda: sw.swiglu_gemm_pack_weight_int8(w8),
+                 lambda: sw.swiglu_fused_packed_int8(a8, r, wp, v, v), lambda: sw.swiglu_gemm_packed_int8(a8, r, wp, v),
+                 lambda: sw.swiglu_mlp_packed_int8(a, wp, v[:64], v[:64], wp, v[:64]),
+                 lambda: sw.swiglu_train_forward_int8(a, w, w), lambda: sw.swiglu_dequantize_kept_int8(codes, kept, 72),
+                 lambda: sw.swiglu_train_backward_int8(dy, a, w, w, codes, kept),
+                 lambda: sw.swiglu_mlp_train_backward_int8(a, a, w, w, w3, codes, kept)):
+        with pytest.raises(ValueError, match="the current device is 0"):
+            call()
