@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _empty, _new, _ptr, _scratch, _shape, _stream, lib
+from . import _check, _empty, _ptr, _raw_stream, _scratch, _shape, _stream, lib
 
 _need: dict = {}
 
@@ -40,16 +40,25 @@ def swiglu_mlp_workspace_bytes_int8(M: int, K: int, N: int) -> int:
     return int(lib().swiglu_mlp_workspace_bytes_int8(M, K, N))
 
 
+# Small products are bound by the host (a launch 2.2 us, an output 1.3 us), so what a
+# call asks of torch it asks once, and in its cheapest form: quantized rows and their
+# product 15.6 us, with general checks and torch.cuda's own functions 19.6 us.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _dev(t, dtype, name: str) -> int:
-    """A contiguous tensor of dtype on the current GPU (plans, streams and launches are
-    that device's)."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous():
-        device = t.get_device()
-        if device >= 0 and device == _current_device():
-            return t.data_ptr()
+def _here() -> int:
+    """The current GPU: plans, streams and launches are its own."""
+    return _current_device() if torch.cuda.is_initialized() else -2   # a CPU tensor's is -1
+
+
+def _stream_at(here: int, stream) -> int:
+    return _raw_stream(here) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _dev(t, dtype, name: str, here: int) -> int:
+    """A contiguous tensor of dtype on the current GPU."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch tensor" % name)
     if t.device.type != "cuda":
@@ -58,17 +67,14 @@ def _dev(t, dtype, name: str) -> int:
         raise TypeError("%s must be %s (got %s)" % (name, str(dtype)[6:], t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    raise ValueError("%s is on %s, the current device is %d" % (name, t.device, _current_device()))
+    raise ValueError("%s is on %s, the current device is %d" % (name, t.device, here))
 
 
-def _dev_bf16(t, name: str) -> int:
-    return _dev(t, torch.bfloat16, name)
-
-
-def _vector(t, n: int, name: str) -> int:
-    if t.shape != (n,):
-        _shape(t, (n,), name)
-    return _dev(t, torch.float32, name)
+def _vector(t, n: int, name: str, here: int) -> int:
+    if t.dtype is torch.float32 and t.shape == (n,) and t.is_contiguous() and t.get_device() == here:
+        return t.data_ptr()
+    _shape(t, (n,), name)
+    return _dev(t, torch.float32, name, here)
 
 
 def _matrix(t, name: str):
@@ -80,17 +86,20 @@ def _matrix(t, name: str):
 def _out(t, shape, dtype, device, s: int, stream):
     if t is not None:
         return t
-    return torch.empty(shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, device, s)
+    return torch.empty(*shape, dtype=dtype, device=device) if stream is None else _empty(shape, dtype, device, s)
 
 
 def _quantize(fn: str, X, Q, scales, n: int, stream):
     R, C = X.shape
     _shape(Q, (R, C), "Q")
     _shape(scales, (n,), "scales")
-    x, s = _dev_bf16(X, "A" if fn == "swiglu_quantize_rows_int8" else "W"), _stream(stream)
-    Q = _out(Q, (R, C), torch.int8, X.device, s, stream)
-    scales = _out(scales, (n,), torch.float32, X.device, s, stream)
-    _check(fn, getattr(lib(), fn)(x, _dev(Q, torch.int8, "Q"), _dev(scales, torch.float32, "scales"), R, C, s))
+    here = _here()
+    x = _dev(X, torch.bfloat16, "A" if fn == "swiglu_quantize_rows_int8" else "W", here)
+    s, device = _stream_at(here, stream), X.device
+    Q = _out(Q, (R, C), torch.int8, device, s, stream)
+    scales = _out(scales, (n,), torch.float32, device, s, stream)
+    _check(fn, getattr(lib(), fn)(x, _dev(Q, torch.int8, "Q", here), _dev(scales, torch.float32, "scales", here), R, C,
+                                  s))
     return Q, scales
 
 
@@ -114,11 +123,12 @@ def _packed(fn: str, sizer, weights, Wp, name: str, stream):
     nbytes = _cached(sizer, K, N)
     if nbytes == 0:
         raise ValueError("invalid int8 weight shape [%d,%d] (K must be a multiple of 16, N of 8)" % (K, N))
-    ptrs, s = [_dev(t, torch.int8, n) for t, n in weights], _stream(stream)
+    here = _here()
+    ptrs, s = [_dev(t, torch.int8, n, here) for t, n in weights], _stream_at(here, stream)
     if Wp is not None and Wp.numel() < nbytes:
         raise ValueError("%s too small: need %d bytes" % (name, nbytes))
     Wp = _out(Wp, (nbytes,), torch.int8, W.device, s, stream)
-    _check(fn, getattr(lib(), fn)(*ptrs, _dev(Wp, torch.int8, name), K, N, s))
+    _check(fn, getattr(lib(), fn)(*ptrs, _dev(Wp, torch.int8, name, here), K, N, s))
     return Wp
 
 
@@ -146,12 +156,14 @@ def _product(fn: str, sizer, need_fn, A, sa, W, wname, scales, out, oname, works
     N = scales[0][0].shape[0]
     _weight_at_least(W, sizer, K, N, wname)
     _shape(out, (M, N), oname)
-    a, r, w = _dev(A, torch.int8, "A"), _vector(sa, M, "sa"), _dev(W, torch.int8, wname)
-    cols = [_vector(t, N, name) for t, name in scales]
-    s = _stream(stream)
-    out = _new((M, N), A.device, s, stream) if out is None else out
-    ws, ws_bytes = _scratch(workspace, _cached(need_fn, M, K, N, device=A.device), A.device, s)
-    _check(fn, getattr(lib(), fn)(a, r, w, *cols, _dev_bf16(out, oname), M, K, N, _ptr(ws), ws_bytes, s))
+    here = _here()
+    a, r, w = _dev(A, torch.int8, "A", here), _vector(sa, M, "sa", here), _dev(W, torch.int8, wname, here)
+    cols = [_vector(t, N, name, here) for t, name in scales]
+    s, device = _stream_at(here, stream), A.device
+    out = _out(out, (M, N), torch.bfloat16, device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(need_fn, M, K, N, device=device), device, s)
+    _check(fn, getattr(lib(), fn)(a, r, w, *cols, _dev(out, torch.bfloat16, oname, here), M, K, N, _ptr(ws), ws_bytes,
+                                  s))
     return out
 
 
@@ -182,13 +194,14 @@ def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, 
     _weight_at_least(W3g, swiglu_gemm_packed_bytes_int8, N, K, "W3g")
     _shape(Y, (M, N), "Y")
     _shape(Z, (M, K), "Z")
-    a, wp, w3 = _dev_bf16(A, "A"), _dev(Wp, torch.int8, "Wp"), _dev(W3g, torch.int8, "W3g")
-    p1, p2, p3 = _vector(s1, N, "s1"), _vector(s2, N, "s2"), _vector(s3, K, "s3")
-    s = _stream(stream)
-    Y = _new((M, N), A.device, s, stream) if Y is None else Y
-    Z = _new((M, K), A.device, s, stream) if Z is None else Z
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_mlp_workspace_bytes_int8, M, K, N, device=A.device), A.device, s)
-    st = lib().swiglu_mlp_packed_int8(a, wp, p1, p2, w3, p3, _dev_bf16(Y, "Y"), _dev_bf16(Z, "Z"), M, K, N, _ptr(ws),
-                                      ws_bytes, s)
+    here, bf16 = _here(), torch.bfloat16
+    a, wp, w3 = _dev(A, bf16, "A", here), _dev(Wp, torch.int8, "Wp", here), _dev(W3g, torch.int8, "W3g", here)
+    p1, p2, p3 = _vector(s1, N, "s1", here), _vector(s2, N, "s2", here), _vector(s3, K, "s3", here)
+    s, device = _stream_at(here, stream), A.device
+    Y = _out(Y, (M, N), bf16, device, s, stream)
+    Z = _out(Z, (M, K), bf16, device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_mlp_workspace_bytes_int8, M, K, N, device=device), device, s)
+    st = lib().swiglu_mlp_packed_int8(a, wp, p1, p2, w3, p3, _dev(Y, bf16, "Y", here), _dev(Z, bf16, "Z", here), M, K, N,
+                                      _ptr(ws), ws_bytes, s)
     _check("swiglu_mlp_packed_int8", st)
     return Y, Z

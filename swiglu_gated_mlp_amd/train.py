@@ -15,9 +15,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (_check, _dev_bf16, _empty, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
+from . import (_check, _dev_bf16, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
                swiglu_gemm_bf16)
-from .int8 import _dev, _dev_bf16 as _here
+from .int8 import _dev, _here, _out, _stream_at
 
 _need: dict = {}
 
@@ -149,6 +149,10 @@ def _kept_shapes(codes, scales, M: int, N: int):
     return groups
 
 
+def _bf16(t, name: str, here: int) -> int:
+    return _dev(t, torch.bfloat16, name, here)
+
+
 def swiglu_train_forward_int8(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, Y: torch.Tensor | None = None,
                               codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, workspace=None,
                               stream=None):
@@ -158,15 +162,15 @@ def swiglu_train_forward_int8(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tenso
     M, K, N = _weights(A, W1, W2)
     _shape(Y, (M, N), "Y")
     groups = _kept_shapes(codes, scales, M, N)
-    a, w1, w2 = _here(A, "A"), _here(W1, "W1"), _here(W2, "W2")
-    s = _stream(stream)
-    Y = _new((M, N), A.device, s, stream) if Y is None else Y
-    if codes is None:
-        codes = _empty((M, groups, 2, 32), torch.int8, A.device, s)
-    scales = _new((groups, M, 2), A.device, s, stream) if scales is None else scales
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, A.device), A.device, s)
-    st = lib().swiglu_train_forward_int8(a, w1, w2, _here(Y, "Y"), _dev(codes, torch.int8, "codes"),
-                                         _here(scales, "scales"), M, K, N, _ptr(ws), ws_bytes, s)
+    here = _here()
+    a, w1, w2 = _bf16(A, "A", here), _bf16(W1, "W1", here), _bf16(W2, "W2", here)
+    s, device = _stream_at(here, stream), A.device
+    Y = _out(Y, (M, N), torch.bfloat16, device, s, stream)
+    codes = _out(codes, (M, groups, 2, 32), torch.int8, device, s, stream)
+    scales = _out(scales, (groups, M, 2), torch.bfloat16, device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, device), device, s)
+    st = lib().swiglu_train_forward_int8(a, w1, w2, _bf16(Y, "Y", here), _dev(codes, torch.int8, "codes", here),
+                                         _bf16(scales, "scales", here), M, K, N, _ptr(ws), ws_bytes, s)
     _check("swiglu_train_forward_int8", st)
     return Y, codes, scales
 
@@ -178,11 +182,12 @@ def swiglu_dequantize_kept_int8(codes: torch.Tensor, scales: torch.Tensor, N: in
     _kept_shapes(codes, scales, M, N)
     for t, name in ((G, "G"), (U, "U")):
         _shape(t, (M, N), name)
-    c, sc = _dev(codes, torch.int8, "codes"), _here(scales, "scales")
-    s = _stream(stream)
-    G = _new((M, N), codes.device, s, stream) if G is None else G
-    U = _new((M, N), codes.device, s, stream) if U is None else U
-    st = lib().swiglu_dequantize_kept_int8(c, sc, _here(G, "G"), _here(U, "U"), M, N, s)
+    here = _here()
+    c, sc = _dev(codes, torch.int8, "codes", here), _bf16(scales, "scales", here)
+    s, device = _stream_at(here, stream), codes.device
+    G = _out(G, (M, N), torch.bfloat16, device, s, stream)
+    U = _out(U, (M, N), torch.bfloat16, device, s, stream)
+    st = lib().swiglu_dequantize_kept_int8(c, sc, _bf16(G, "G", here), _bf16(U, "U", here), M, N, s)
     _check("swiglu_dequantize_kept_int8", st)
     return G, U
 
@@ -195,13 +200,14 @@ def swiglu_train_backward_int8(dY: torch.Tensor, A: torch.Tensor, W1: torch.Tens
     M, K, N = _weights(A, W1, W2)
     _shape(dY, (M, N), "dY")
     _kept_shapes(codes, scales, M, N)
-    ins = [_here(t, n) for t, n in ((dY, "dY"), (A, "A"), (W1, "W1"), (W2, "W2"))]
-    ins += [_dev(codes, torch.int8, "codes"), _here(scales, "scales")]
-    s = _stream(stream)
-    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
-    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, A.device), A.device, s)
-    outs = [0 if t is None else _here(t, n) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
+    here = _here()
+    ins = [_bf16(t, n, here) for t, n in ((dY, "dY"), (A, "A"), (W1, "W1"), (W2, "W2"))]
+    ins += [_dev(codes, torch.int8, "codes", here), _bf16(scales, "scales", here)]
+    s, device = _stream_at(here, stream), A.device
+    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), device, s, stream)
+    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, device), device, s)
+    outs = [0 if t is None else _bf16(t, n, here) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
     st = lib().swiglu_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
     _check("swiglu_train_backward_int8", st)
     return dA, dW1, dW2
@@ -218,14 +224,15 @@ def swiglu_mlp_train_backward_int8(dZ: torch.Tensor, A: torch.Tensor, W1: torch.
     _shape(dZ, (M, K), "dZ")
     _shape(W3, (N, K), "W3")
     _kept_shapes(codes, scales, M, N)
-    ins = [_here(t, n) for t, n in ((dZ, "dZ"), (A, "A"), (W1, "W1"), (W2, "W2"), (W3, "W3"))]
-    ins += [_dev(codes, torch.int8, "codes"), _here(scales, "scales")]
-    s = _stream(stream)
-    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), A.device, s, stream)
-    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), A.device, s, stream)
-    dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), A.device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes_int8, M, K, N, A.device), A.device, s)
-    outs = [0 if t is None else _here(t, n)
+    here = _here()
+    ins = [_bf16(t, n, here) for t, n in ((dZ, "dZ"), (A, "A"), (W1, "W1"), (W2, "W2"), (W3, "W3"))]
+    ins += [_dev(codes, torch.int8, "codes", here), _bf16(scales, "scales", here)]
+    s, device = _stream_at(here, stream), A.device
+    dA, = _grads(need_dA, (dA,), (M, K), ("dA",), device, s, stream)
+    dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), device, s, stream)
+    dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), device, s, stream)
+    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes_int8, M, K, N, device), device, s)
+    outs = [0 if t is None else _bf16(t, n, here)
             for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"), (dW3, "dW3"))]
     st = lib().swiglu_mlp_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
     _check("swiglu_mlp_train_backward_int8", st)

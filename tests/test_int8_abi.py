@@ -175,8 +175,9 @@ class Elsewhere(torch.Tensor):
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
-    from swiglu_gated_mlp_amd import int8
-    monkeypatch.setattr(int8, "_current_device", lambda: 0)
+    from swiglu_gated_mlp_amd import int8, train
+    monkeypatch.setattr(int8, "_here", lambda: 0)
+    monkeypatch.setattr(train, "_here", lambda: 0)
     a8, a = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 64, dtype=torch.bfloat16)
     w, v, r = torch.zeros(64, 72, dtype=torch.bfloat16), torch.zeros(72), torch.zeros(4)
     wp = torch.zeros(sw.swiglu_packed_bytes_int8(64, 72), dtype=torch.int8)
