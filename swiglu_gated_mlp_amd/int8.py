@@ -10,8 +10,8 @@ from . import _check, _empty, _ptr, _raw_stream, _scratch, _shape, _stream, lib
 _need: dict = {}
 
 
-def _cached(fn, *args, device=None) -> int:
-    key = (fn, args, None if device is None else device.index)
+def _cached(fn, *args):
+    key = (fn, args)
     need = _need.get(key)
     if need is None:
         if len(_need) >= 4096:
@@ -42,7 +42,7 @@ def swiglu_mlp_workspace_bytes_int8(M: int, K: int, N: int) -> int:
 
 # Small products are bound by the host (a launch 2.2 us, an output 1.3 us), so what a
 # call asks of torch it asks once, and in its cheapest form: quantized rows and their
-# product 15.6 us, with general checks and torch.cuda's own functions 19.6 us.
+# product 15.3 us of host time, with general checks and torch.cuda's functions 19.6 us.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
@@ -143,44 +143,58 @@ def swiglu_gemm_pack_weight_int8(W: torch.Tensor, Wg: torch.Tensor | None = None
     return _packed("swiglu_gemm_pack_weight_int8", swiglu_gemm_packed_bytes_int8, [(W, "W")], Wg, "Wg", stream)
 
 
-def _weight_at_least(W, sizer, K: int, N: int, name: str) -> None:
-    need = _cached(sizer, K, N)
+def _weight_at_least(W, need: int, K: int, N: int, name: str) -> None:
     if need == 0:
         raise ValueError("invalid int8 weight shape [%d,%d]" % (K, N))
     if W.numel() < need:
         raise ValueError("%s holds %d codes; a packed int8 [%d,%d] weight needs %d" % (name, W.numel(), K, N, need))
 
 
-def _product(fn: str, sizer, need_fn, A, sa, W, wname, scales, out, oname, workspace, stream):
-    M, K = _matrix(A, "A")
-    N = scales[0][0].shape[0]
-    _weight_at_least(W, sizer, K, N, wname)
-    _shape(out, (M, N), oname)
-    here = _here()
-    a, r, w = _dev(A, torch.int8, "A", here), _vector(sa, M, "sa", here), _dev(W, torch.int8, wname, here)
-    cols = [_vector(t, N, name, here) for t, name in scales]
-    s, device = _stream_at(here, stream), A.device
-    out = _out(out, (M, N), torch.bfloat16, device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(need_fn, M, K, N, device=device), device, s)
-    _check(fn, getattr(lib(), fn)(a, r, w, *cols, _dev(out, torch.bfloat16, oname, here), M, K, N, _ptr(ws), ws_bytes,
-                                  s))
-    return out
+def _sizes(weights, need, M: int, K: int, N: int, here: int):
+    """(codes of the packed weights, workspace bytes on this device) of a call."""
+    key = (need, M, K, N, here)
+    sizes = _need.get(key)
+    if sizes is None:
+        if len(_need) >= 4096:
+            _need.clear()
+        sizes = _need[key] = (weights(K, N), need(M, K, N))
+    return sizes
 
 
 def swiglu_fused_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, s2: torch.Tensor,
                              Y: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
     """Y = SiLU(G) * U bf16 [M,N] from the codes A int8 [M,K], their rows' scales sa
     [M], the packed codes of W1 and W2 and their columns' scales s1, s2 [N] (fp32)."""
-    return _product("swiglu_fused_packed_int8", swiglu_packed_bytes_int8, swiglu_workspace_bytes_int8, A, sa, Wp,
-                    "Wp", [(s1, "s1"), (s2, "s2")], Y, "Y", workspace, stream)
+    (M, K), N, here = _matrix(A, "A"), s1.shape[0], _here()
+    least, need = _sizes(swiglu_packed_bytes_int8, swiglu_workspace_bytes_int8, M, K, N, here)
+    _weight_at_least(Wp, least, K, N, "Wp")
+    _shape(Y, (M, N), "Y")
+    a, r, w = _dev(A, torch.int8, "A", here), _vector(sa, M, "sa", here), _dev(Wp, torch.int8, "Wp", here)
+    p1, p2 = _vector(s1, N, "s1", here), _vector(s2, N, "s2", here)
+    s, device = _stream_at(here, stream), A.device
+    Y = _out(Y, (M, N), torch.bfloat16, device, s, stream)
+    ws, ws_bytes = _scratch(workspace, need, device, s)
+    _check("swiglu_fused_packed_int8", lib().swiglu_fused_packed_int8(
+        a, r, w, p1, p2, _dev(Y, torch.bfloat16, "Y", here), M, K, N, _ptr(ws), ws_bytes, s))
+    return Y
 
 
 def swiglu_gemm_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wg: torch.Tensor, sw: torch.Tensor,
                             C: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
     """C = A @ W bf16 [M,N] from the codes A int8 [M,K], sa [M], one weight's packed
     codes and its columns' scales sw [N] (fp32)."""
-    return _product("swiglu_gemm_packed_int8", swiglu_gemm_packed_bytes_int8, swiglu_gemm_workspace_bytes_int8, A, sa,
-                    Wg, "Wg", [(sw, "sw")], C, "C", workspace, stream)
+    (M, K), N, here = _matrix(A, "A"), sw.shape[0], _here()
+    least, need = _sizes(swiglu_gemm_packed_bytes_int8, swiglu_gemm_workspace_bytes_int8, M, K, N, here)
+    _weight_at_least(Wg, least, K, N, "Wg")
+    _shape(C, (M, N), "C")
+    a, r, w = _dev(A, torch.int8, "A", here), _vector(sa, M, "sa", here), _dev(Wg, torch.int8, "Wg", here)
+    p = _vector(sw, N, "sw", here)
+    s, device = _stream_at(here, stream), A.device
+    C = _out(C, (M, N), torch.bfloat16, device, s, stream)
+    ws, ws_bytes = _scratch(workspace, need, device, s)
+    _check("swiglu_gemm_packed_int8", lib().swiglu_gemm_packed_int8(
+        a, r, w, p, _dev(C, torch.bfloat16, "C", here), M, K, N, _ptr(ws), ws_bytes, s))
+    return C
 
 
 def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, s2: torch.Tensor, W3g: torch.Tensor,
@@ -188,19 +202,19 @@ def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, 
                            workspace=None, stream=None):
     """The gated MLP block from A bf16 [M,K]: its rows quantized, Y = SiLU(G) * U
     (bf16), Y's rows quantized, Z = Y @ W3.  Returns (Y, Z)."""
-    M, K = _matrix(A, "A")
-    N = s1.shape[0]
-    _weight_at_least(Wp, swiglu_packed_bytes_int8, K, N, "Wp")
-    _weight_at_least(W3g, swiglu_gemm_packed_bytes_int8, N, K, "W3g")
+    (M, K), N, here = _matrix(A, "A"), s1.shape[0], _here()
+    least, need = _sizes(swiglu_packed_bytes_int8, swiglu_mlp_workspace_bytes_int8, M, K, N, here)
+    _weight_at_least(Wp, least, K, N, "Wp")
+    _weight_at_least(W3g, _cached(swiglu_gemm_packed_bytes_int8, N, K), N, K, "W3g")
     _shape(Y, (M, N), "Y")
     _shape(Z, (M, K), "Z")
-    here, bf16 = _here(), torch.bfloat16
+    bf16 = torch.bfloat16
     a, wp, w3 = _dev(A, bf16, "A", here), _dev(Wp, torch.int8, "Wp", here), _dev(W3g, torch.int8, "W3g", here)
     p1, p2, p3 = _vector(s1, N, "s1", here), _vector(s2, N, "s2", here), _vector(s3, K, "s3", here)
     s, device = _stream_at(here, stream), A.device
     Y = _out(Y, (M, N), bf16, device, s, stream)
     Z = _out(Z, (M, K), bf16, device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_mlp_workspace_bytes_int8, M, K, N, device=device), device, s)
+    ws, ws_bytes = _scratch(workspace, need, device, s)
     st = lib().swiglu_mlp_packed_int8(a, wp, p1, p2, w3, p3, _dev(Y, bf16, "Y", here), _dev(Z, bf16, "Z", here), M, K, N,
                                       _ptr(ws), ws_bytes, s)
     _check("swiglu_mlp_packed_int8", st)
