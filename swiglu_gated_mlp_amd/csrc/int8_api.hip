@@ -68,8 +68,8 @@ bool in_chunks(int64_t M, int64_t K) { return M > stream_rows_limit(K, 1); }
 // fastest.
 //   The estimates are microseconds of a launch on an idle device with the weights in
 // HBM and the caches full of something else's outputs, and only their order matters.
-// Fitted to this chip over 126 shapes (33 .. 2048 rows, K 896 .. 29568, N 896 .. 29568)
-// with every tile and up to 16 parts, and to the same launches one after another: off
+// Fitted to this chip over 236 shapes (33 .. 4096 rows, K 128 .. 29568, N 512 .. 29568)
+// with every tile and up to 12 parts, 126 of them also launched one after another: off
 // by 10 % in the root mean square, and the choice costs 2 to 3 % over the best on
 // average.
 // ---------------------------------------------------------------------------
@@ -83,21 +83,24 @@ struct Plan8 {
     size_t part_bytes;
 };
 
-// Tiles: rows, waves and 32-row weight blocks a wave.  Counts of waves that divide no
-// power of two fill the CUs where the others leave a round nearly empty: 7B width, 128
-// rows, fused <128,4,2> 33, <128,6,1> 30, 64 rows <64,4,1> 30, <64,5,1> 25 us.  Without
-// the fused product's 6 and 5 the choice costs 4 % over the best on average, with one
-// tile of each height 9 %.  One weight gains nothing from them.
+// Tiles: rows, waves and 32-row weight blocks a wave.  One block a wave leaves registers
+// for two workgroups a CU (three of 64 rows), so that one's last stores overlap the
+// next's products: 2048 rows, K=896 N=4864, fused <128,4,2> 29, <128,4,1> 25 us; two
+// reuse the activations' fragments: 7B width, 256 rows, one weight 32 and 39 us.  Counts
+// of waves that divide no power of two fill the CUs where the others leave a round
+// nearly empty: 7B width, 128 rows, fused <128,4,2> 33, <128,6,1> 30, 64 rows <64,4,1>
+// 30, <64,5,1> 25 us.  Leaving out one tile costs 0.5 (<64,5,1>) to 3 % on average.
 struct NarrowTile {
     int bm, waves, wt;
     bool gemm;
-    int blocks() const { return waves * wt; }
-    // microseconds outside the stages, and a stage (128 k) on a CU that has one workgroup
-    double once() const { return bm == 128 ? 8.9 : 8.2; }
-    double stage() const { return bm == 128 ? 0.2 + 0.052 * blocks() : 0.07 + 0.063 * blocks(); }
+    // microseconds outside the items, a stage (128 k) of an item and of each of its
+    // blocks, and a block's sums when they are finished
+    double once, stage, block, finish;
 };
-constexpr NarrowTile kNarrow[] = {{128, 4, 2, true}, {128, 3, 1, true}, {128, 6, 1, false},
-                                  {64, 4, 1, true},  {64, 3, 1, true},  {64, 5, 1, false}};
+constexpr NarrowTile kNarrow[] = {
+    {128, 4, 2, true, 5.9, 0.172, 0.043, 0.68},  {128, 4, 1, true, 7.5, 0.177, 0.046, 0.46},
+    {128, 6, 1, false, 7.5, 0.177, 0.046, 0.46}, {64, 4, 1, true, 7.8, 0.121, 0.037, 0.18},
+    {64, 3, 1, true, 7.8, 0.121, 0.037, 0.18},   {64, 5, 1, false, 7.8, 0.121, 0.037, 0.18}};
 
 // A CU's stages, the weights from HBM and the matrix cores overlap in part.
 double overlapped(double cu, double hbm, double mfma) { return std::sqrt(cu * cu + hbm * hbm + mfma * mfma); }
@@ -110,11 +113,14 @@ double rounds_of(int64_t items, int cus) {
 double narrow_us(const Plan8& p, int64_t K, int64_t M) {
     const NarrowTile& t = kNarrow[p.tile];
     const int64_t items = (int64_t)p.tiles_m * p.groups * p.splits;
-    const double rows = (double)p.groups * t.blocks() * 32;   // packed
-    return t.once() +
-           overlapped(rounds_of(items, p.cus) * p.kb_per_split * t.stage(), (rows + M) * K / 7.9e6,
-                      2.0 * p.tiles_m * t.bm * rows * K / 2.28e9) +
-           (p.splits > 1 ? 2.5 + p.part_bytes / 3.6e6 : 0.0);
+    const double rows = (double)p.groups * t.waves * t.wt * 32;   // packed
+    // where CUs have several items, the SIMD with the most waves sets the pace
+    const int64_t waves = items > 2 * (int64_t)p.cus ? ceil_div(t.waves, 4) * 4 : t.waves;
+    const double blocks = (double)waves * t.wt;
+    return t.once +
+           overlapped(rounds_of(items, p.cus) * (p.kb_per_split * (t.stage + t.block * blocks) + t.finish * blocks),
+                      (rows + M) * K / 6.7e6, 2.0 * p.tiles_m * t.bm * rows * K / 2.44e9) +
+           (p.splits > 1 ? 2.7 + p.part_bytes / 4.0e6 : 0.0);
 }
 
 double stream_us(const Plan& p, int64_t M, int64_t K) {
@@ -175,12 +181,12 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
         p.tiles_m = (int)ceil_div(M, t.bm);
         p.groups = (int)ceil_div(p.units, t.waves);
         // weights that fit the last-level cache beside others stay there; see Narrow::ONCE
-        p.once = (int64_t)p.groups * t.blocks() * 32 * KB * 128 > ((int64_t)32 << 20) && p.tiles_m <= (t.bm == 64 ? 2 : 4);
+        p.once = (int64_t)p.groups * t.waves * t.wt * 32 * KB * 128 > ((int64_t)32 << 20) && p.tiles_m <= (t.bm == 64 ? 2 : 4);
         for (int s : kSplits) {
             if (s > 1 && 3 * s > KB) break;
             p.kb_per_split = (int)ceil_div(KB, s);
             p.splits = (int)ceil_div(KB, p.kb_per_split);
-            p.part_bytes = p.splits > 1 ? (size_t)p.splits * p.groups * p.tiles_m * t.blocks() * t.bm * 128
+            p.part_bytes = p.splits > 1 ? (size_t)p.splits * p.groups * p.tiles_m * t.waves * t.wt * t.bm * 128
                                         : 0;
             const double us = narrow_us(p, K, M);
             if (us < best_us) {
@@ -285,7 +291,7 @@ hipError_t run_rows(const Product8& q, const Plan8& p, hipStream_t s) {
         const NarrowTile& t = kNarrow[p.tile];
         if (t.bm == 128) {
             if (t.wt == 2) return launch_narrow<128, 4, 2, GEMM>(a, p.once, s);
-            if (t.waves == 3) return launch_narrow<128, 3, 1, GEMM>(a, p.once, s);
+            if (t.waves == 4) return launch_narrow<128, 4, 1, GEMM>(a, p.once, s);
             if constexpr (!GEMM) return launch_narrow<128, 6, 1, false>(a, p.once, s);
         } else {
             if (t.waves == 4) return launch_narrow<64, 4, 1, GEMM>(a, p.once, s);
@@ -541,7 +547,7 @@ int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N, int32_t* p
     const Plan8 p = plan_int8(gemm != 0, M, K, N);
     const bool narrow = p.how == Plan8::NARROW;
     const int rows = p.how == Plan8::DECODE ? (M <= 16 ? 16 : M <= 32 ? 32 : 64) : narrow ? kNarrow[p.tile].bm : 256;
-    const int cols = narrow ? 32 * kNarrow[p.tile].blocks() : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
+    const int cols = narrow ? 32 * kNarrow[p.tile].waves * kNarrow[p.tile].wt : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
     const int32_t v[5] = {p.how, rows, cols, narrow ? p.splits : 1, narrow && p.once};
     std::copy(v, v + 5, plan);
     return 1;

@@ -194,7 +194,8 @@ SHAPES = [(1, 16, 8), (1, 896, 4864), (4, 1040, 520), (5, 2064, 520), (7, 144, 1
           (1030, 4112, 1000), (33, 18416, 1056), (174, 16, 5160), (33, 1232, 14568), (259, 6368, 56), (36, 7408, 4128),
           (65, 23584, 1040), (73, 13408, 1624), (334, 10736, 1432), (70, 11952, 4144), (1513, 15248, 256),
           (69, 19024, 6264), (70, 2576, 12960), (35, 5984, 8320), (66, 10032, 4360), (1359, 14736, 488),
-          (65, 15200, 8368)]
+          (65, 15200, 8368), (4197, 9584, 88), (70, 20016, 4112), (602, 16, 6464), (2067, 22896, 200), (4169, 9056, 440),
+          (65, 12736, 16488)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -214,7 +215,7 @@ def test_every_kernel_is_met(dev):
             p = sw.swiglu_probe_int8_plan(gemm, *shape)
             met.add((gemm, p["kernel"], p["rows"], p["cols"], p["splits"] > 1, p["once"]))
     for gemm in (False, True):
-        for tile in ((64, 96), (64, 128), (128, 96), (128, 256)) + (() if gemm else ((64, 160), (128, 192))):
+        for tile in ((64, 96), (64, 128), (128, 128), (128, 256)) + (() if gemm else ((64, 160), (128, 192))):
             for parts in (False, True):
                 for once in (False, True):
                     assert (gemm, "narrow") + tile + (parts, once) in met, (gemm, tile, parts, once)
