@@ -69,9 +69,9 @@ bool in_chunks(int64_t M, int64_t K) { return M > stream_rows_limit(K, 1); }
 //   The estimates are microseconds of a launch on an idle device with the weights in
 // HBM and the caches full of something else's outputs, and only their order matters.
 // Fitted to this chip over 236 shapes (33 .. 4096 rows, K 128 .. 29568, N 512 .. 29568)
-// with every tile and up to 12 parts, 126 of them also launched one after another: off
-// by 10 % in the root mean square, and the choice costs 2 to 3 % over the best on
-// average.
+// with every tile and up to 12 parts, 126 of them also launched one after another, and
+// over 84 of 1 .. 28 rows: off by 7 to 10 % in the root mean square, and the choice costs
+// 2 to 3 % over the best on average.
 // ---------------------------------------------------------------------------
 struct Plan8 {
     enum How { DECODE, NARROW, STREAM } how;
@@ -90,6 +90,7 @@ struct Plan8 {
 // of waves that divide no power of two fill the CUs where the others leave a round
 // nearly empty: 7B width, 128 rows, fused <128,4,2> 33, <128,6,1> 30, 64 rows <64,4,1>
 // 30, <64,5,1> 25 us.  Leaving out one tile costs 0.5 (<64,5,1>) to 3 % on average.
+// 32 rows: batches of up to 32, against the decode kernel (see decode_us).
 struct NarrowTile {
     int bm, waves, wt;
     bool gemm;
@@ -100,7 +101,9 @@ struct NarrowTile {
 constexpr NarrowTile kNarrow[] = {
     {128, 4, 2, true, 5.9, 0.172, 0.043, 0.68},  {128, 4, 1, true, 7.5, 0.177, 0.046, 0.46},
     {128, 6, 1, false, 7.5, 0.177, 0.046, 0.46}, {64, 4, 1, true, 7.8, 0.121, 0.037, 0.18},
-    {64, 3, 1, true, 7.8, 0.121, 0.037, 0.18},   {64, 5, 1, false, 7.8, 0.121, 0.037, 0.18}};
+    {64, 3, 1, true, 7.8, 0.121, 0.037, 0.18},   {64, 5, 1, false, 7.8, 0.121, 0.037, 0.18},
+    {32, 4, 1, true, 7.8, 0.070, 0.047, 0.25},   {32, 3, 1, true, 7.8, 0.070, 0.047, 0.25},
+    {32, 5, 1, false, 7.8, 0.070, 0.047, 0.25}};
 
 // A CU's stages, the weights from HBM and the matrix cores overlap in part.
 double overlapped(double cu, double hbm, double mfma) { return std::sqrt(cu * cu + hbm * hbm + mfma * mfma); }
@@ -120,7 +123,7 @@ double narrow_us(const Plan8& p, int64_t K, int64_t M) {
     return t.once +
            overlapped(rounds_of(items, p.cus) * (p.kb_per_split * (t.stage + t.block * blocks) + t.finish * blocks),
                       (rows + M) * K / 6.7e6, 2.0 * p.tiles_m * t.bm * rows * K / 2.44e9) +
-           (p.splits > 1 ? 2.7 + p.part_bytes / 4.0e6 : 0.0);
+           (p.splits > 1 ? 2.2 + 0.13 * p.splits + p.part_bytes / 4.0e6 : 0.0);
 }
 
 double stream_us(const Plan& p, int64_t M, int64_t K) {
@@ -134,9 +137,25 @@ double stream_us(const Plan& p, int64_t M, int64_t K) {
                             2.0 * p.tiles_m * 256 * rows * K / 3.3e9);
 }
 
-// 33 to 64 rows on the decode kernel (see run_decode)
-double decode_us(bool gemm, int64_t KB, int64_t nt, int cus) {
-    return gemm ? 5.0 + 0.16 * KB * ceil_div(2 * ceil_div(nt, 16), cus) : 5.4 + 0.49 * KB * ceil_div(ceil_div(nt, 32), cus);
+// The fused product on eight column groups a workgroup, one weight on two (see run_decode)
+bool decode_wide(bool gemm, int64_t nt, int cus) {
+    return gemm ? ceil_div(nt, 16) >= cus : 4 * ceil_div(nt, 128) >= 3 * (int64_t)cus;
+}
+
+// The decode kernel as run_decode launches it, up to 64 rows.  Its workgroups read all
+// activations, so that long contractions with few columns are narrow_kernel's, whose
+// parts read theirs (one weight K=24352 N=848: 28 rows 24.7 and 13.0 us, 1 row 10.7 and
+// 12.5), and those that fill a round and a little (K=16384 N=5120, 8 rows 21.8 and 18.7).
+double decode_us(bool gemm, int64_t M, int64_t K, int64_t nt, int cus) {
+    const int64_t KB = ceil_div(K, 128), groups = ceil_div(nt, 16);
+    if (M > 32) return gemm ? 5.0 + 0.16 * KB * ceil_div(2 * groups, cus) : 5.4 + 0.49 * KB * ceil_div(ceil_div(nt, 32), cus);
+    const bool wide = decode_wide(gemm, nt, cus);
+    if (!gemm && wide) return 5.6 + 2.0 * nt * K / 6.85e6;
+    const bool pairs = gemm && wide && M > 8 && M <= 16;   // two groups a workgroup
+    // a workgroup's 128 k
+    const double block = gemm ? (M <= 4 ? 0.038 : M <= 16 ? (0.042 + 0.0016 * M) * (pairs ? 1.7 : 1.0) : 0.093)
+                              : (M <= 8 ? 0.086 : M <= 16 ? 0.098 : 0.142);
+    return 7.9 + overlapped(block * KB * ceil_div(gemm && !pairs ? 2 * groups : groups, cus), 2.0 * nt * K / 8.0e6, 0.0);
 }
 
 // The streaming kernel at any M, without a workspace.
@@ -167,12 +186,11 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
     double best_us = stream_us(best.stream, M, K);
     if (M <= 64) {
         best.how = Plan8::DECODE;
-        if (M <= 32) return best;
-        best_us = decode_us(gemm, KB, gemm ? gemm_tiled_cols(N) : N, best.cus);
+        best_us = decode_us(gemm, M, K, gemm ? gemm_tiled_cols(N) : N, best.cus);
     }
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 16};
     for (const NarrowTile& t : kNarrow) {
-        if (gemm && !t.gemm) continue;
+        if ((gemm && !t.gemm) || (t.bm == 32) != (M <= 32)) continue;
         Plan8 p = best;
         p.how = Plan8::NARROW;
         p.tile = (int)(&t - kNarrow);
@@ -181,7 +199,7 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
         p.tiles_m = (int)ceil_div(M, t.bm);
         p.groups = (int)ceil_div(p.units, t.waves);
         // weights that fit the last-level cache beside others stay there; see Narrow::ONCE
-        p.once = (int64_t)p.groups * t.waves * t.wt * 32 * KB * 128 > ((int64_t)32 << 20) && p.tiles_m <= (t.bm == 64 ? 2 : 4);
+        p.once = (int64_t)p.groups * t.waves * t.wt * 32 * KB * 128 > ((int64_t)32 << 20) && p.tiles_m <= (t.bm == 128 ? 4 : 2);
         for (int s : kSplits) {
             if (s > 1 && 3 * s > KB) break;
             p.kb_per_split = (int)ceil_div(KB, s);
@@ -240,19 +258,18 @@ hipError_t launch_decode8(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t
 //   K=4864 N=896    M=64: 8 waves <4,1,1,L> 7.9, 4 waves 10.4 (narrow_kernel 9.5)
 template <bool GEMM>
 hipError_t run_decode(const swk::DecodeArgs& d, int64_t nt, int cus, hipStream_t s) {
+    const bool wide = decode_wide(GEMM, nt, cus);
     if constexpr (GEMM) {
         if (d.M > 32) return launch_decode8<4, 1, 1, true, true, true, 8>(d, nt, s);
-        const bool wide = ceil_div(nt, 16) >= cus;   // two workgroups of one group a CU
-        if (d.M <= 16) {
-            if (wide && d.M > 8) return launch_decode8<1, 2, 4, true, true, false, 8>(d, nt, s);
-            return d.M > 4 ? launch_decode8<1, 1, 4, true, true, true, 8>(d, nt, s)
-                           : launch_decode8<1, 1, 4, true, true, false, 8>(d, nt, s);
-        }
-        return wide ? launch_decode8<2, 2, 2, true, true, false, 4>(d, nt, s)
-                    : launch_decode8<2, 1, 2, true, true, true, 8>(d, nt, s);
+        if (d.M > 16)
+            return wide ? launch_decode8<2, 2, 2, true, true, false, 4>(d, nt, s)
+                        : launch_decode8<2, 1, 2, true, true, true, 8>(d, nt, s);
+        if (wide && d.M > 8) return launch_decode8<1, 2, 4, true, true, false, 8>(d, nt, s);
+        return d.M > 4 ? launch_decode8<1, 1, 4, true, true, true, 8>(d, nt, s)
+                       : launch_decode8<1, 1, 4, true, true, false, 8>(d, nt, s);
     } else {
         if (d.M > 32) return launch_decode8<4, 2, 1, false, false, true, 4>(d, nt, s);
-        if (4 * ceil_div(nt, 128) >= 3 * (int64_t)cus) return launch_decode8<2, 8, 1, false, false, false, 4>(d, nt, s);
+        if (wide) return launch_decode8<2, 8, 1, false, false, false, 4>(d, nt, s);
         if (d.M <= 8) return launch_decode8<1, 1, 8, false, false, false, 4>(d, nt, s);
         return d.M <= 16 ? launch_decode8<1, 1, 4, false, false, true, 8>(d, nt, s)
                          : launch_decode8<2, 1, 4, false, false, true, 4>(d, nt, s);
@@ -269,7 +286,7 @@ hipError_t launch_narrow_as(const swq::NarrowArgs& a, hipStream_t s) {
                                          dim3((unsigned)(a.tiles_m * a.groups * a.splits)), dim3(64 * WAVES), kargs, 0, s);
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t jobs = (int64_t)a.tiles_m * a.groups * WAVES * (GEMM ? WT : 1) * P::TM;
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_reduce_kernel<P>),
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_reduce_kernel<swq::Narrow<BM, WAVES, WT, 4, GEMM, false>>),
                            dim3((unsigned)ceil_div(jobs, 4)), dim3(256), kargs, 0, s);
 }
 
@@ -293,6 +310,10 @@ hipError_t run_rows(const Product8& q, const Plan8& p, hipStream_t s) {
             if (t.wt == 2) return launch_narrow<128, 4, 2, GEMM>(a, p.once, s);
             if (t.waves == 4) return launch_narrow<128, 4, 1, GEMM>(a, p.once, s);
             if constexpr (!GEMM) return launch_narrow<128, 6, 1, false>(a, p.once, s);
+        } else if (t.bm == 32) {
+            if (t.waves == 4) return launch_narrow<32, 4, 1, GEMM>(a, p.once, s);
+            if (t.waves == 3) return launch_narrow<32, 3, 1, GEMM>(a, p.once, s);
+            if constexpr (!GEMM) return launch_narrow<32, 5, 1, false>(a, p.once, s);
         } else {
             if (t.waves == 4) return launch_narrow<64, 4, 1, GEMM>(a, p.once, s);
             if (t.waves == 3) return launch_narrow<64, 3, 1, GEMM>(a, p.once, s);

@@ -1,7 +1,7 @@
-// Int8 products of up to some hundred rows: small row tiles, the contraction split
-// over workgroups, and as many loads in flight as registers and LDS hold.
+// Int8 products of up to some thousand rows: small row tiles, the contraction split over
+// workgroups, and as many loads in flight as registers and LDS hold.
 //
-// There a product is bound by reading its weights once (7B width, 128 rows: 136 MB
+// Of few rows a product is bound by reading its weights once (7B width, 128 rows: 136 MB
 // against 35 GOP, which the matrix cores do in a third of the time), and a CU reaches
 // its share of HBM's rate only with some 50 KB in flight.  So
 //  - a workgroup takes BM rows and WAVES x WT blocks of 32 packed weight rows, and a
@@ -10,6 +10,9 @@
 //    straight to registers (each is needed by one wave), both NBUF - 1 stages ahead;
 //  - parts leave their int32 sums in the lanes' own order (1 KiB runs), and a second
 //    launch adds them: whole numbers, so in any order the same.
+// Of many rows and a short contraction it is bound by what follows the products (scales,
+// SiLU, stores): there two or three workgroups share a CU, and one's end overlaps the
+// next's loads and products (see NarrowTile).
 // WT 2: a wave has the Gate and the Up block of the same 32 columns (or, GEMM, columns
 // 128 apart of one weight).  WT 1: one block; the fused product's holds the Gate and Up
 // rows of 16 columns, so that a lane has both sums of a column.

@@ -195,7 +195,9 @@ SHAPES = [(1, 16, 8), (1, 896, 4864), (4, 1040, 520), (5, 2064, 520), (7, 144, 1
           (65, 23584, 1040), (73, 13408, 1624), (334, 10736, 1432), (70, 11952, 4144), (1513, 15248, 256),
           (69, 19024, 6264), (70, 2576, 12960), (35, 5984, 8320), (66, 10032, 4360), (1359, 14736, 488),
           (65, 15200, 8368), (4197, 9584, 88), (70, 20016, 4112), (602, 16, 6464), (2067, 22896, 200), (4169, 9056, 440),
-          (65, 12736, 16488)]
+          (65, 12736, 16488), (19, 14832, 4240), (20, 16, 17144), (21, 9504, 8272), (22, 656, 22720), (26, 1200, 13120),
+          (30, 16, 13512), (32, 9440, 4096), (529, 4592, 440), (28, 24352, 848), (8, 16384, 1024), (1, 16384, 5120),
+          (25, 5712, 4224), (26, 400, 17032), (31, 416, 12664)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
@@ -213,16 +215,18 @@ def test_every_kernel_is_met(dev):
     for gemm in (False, True):
         for shape in SHAPES:
             p = sw.swiglu_probe_int8_plan(gemm, *shape)
-            met.add((gemm, p["kernel"], p["rows"], p["cols"], p["splits"] > 1, p["once"]))
+            tile = (gemm, p["kernel"], p["rows"], p["cols"])
+            met |= {tile, tile + ("parts", p["splits"] > 1), tile + ("once", p["once"])}
     for gemm in (False, True):
-        for tile in ((64, 96), (64, 128), (128, 128), (128, 256)) + (() if gemm else ((64, 160), (128, 192))):
-            for parts in (False, True):
-                for once in (False, True):
-                    assert (gemm, "narrow") + tile + (parts, once) in met, (gemm, tile, parts, once)
+        for rows, cols in ((32, 96), (32, 128), (64, 96), (64, 128), (128, 128), (128, 256)) + (
+                () if gemm else ((32, 160), (64, 160), (128, 192))):
+            for what in ("parts", "once"):
+                for yes in (False, True):
+                    assert (gemm, "narrow", rows, cols, what, yes) in met, (gemm, rows, cols, what, yes)
         for rows in (16, 32, 64):
-            assert (gemm, "decode", rows, 256, False, False) in met
-        assert (gemm, "stream", 256, 256, False, False) in met
-    assert (False, "stream", 256, 64, False, False) in met
+            assert (gemm, "decode", rows, 256) in met
+        assert (gemm, "stream", 256, 256) in met
+    assert (False, "stream", 256, 64) in met
 
 
 @pytest.mark.parametrize("M", [1, 40, 100, 300])
