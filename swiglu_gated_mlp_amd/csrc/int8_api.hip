@@ -204,6 +204,8 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
             if (s > 1 && 3 * s > KB) break;
             p.kb_per_split = (int)ceil_div(KB, s);
             p.splits = (int)ceil_div(KB, p.kb_per_split);
+            // a launch's threads are counted in 32 bits
+            if ((int64_t)p.tiles_m * p.groups * p.splits * t.waves * 64 > INT32_MAX) break;
             p.part_bytes = p.splits > 1 ? (size_t)p.splits * p.groups * p.tiles_m * t.waves * t.wt * t.bm * 128
                                         : 0;
             const double us = narrow_us(p, K, M);
@@ -568,7 +570,8 @@ int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N, int32_t* p
     const Plan8 p = plan_int8(gemm != 0, M, K, N);
     const bool narrow = p.how == Plan8::NARROW;
     const int rows = p.how == Plan8::DECODE ? (M <= 16 ? 16 : M <= 32 ? 32 : 64) : narrow ? kNarrow[p.tile].bm : 256;
-    const int cols = narrow ? 32 * kNarrow[p.tile].waves * kNarrow[p.tile].wt : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
+    const int cols = narrow ? 32 * kNarrow[p.tile].waves * kNarrow[p.tile].wt
+                            : p.how == Plan8::STREAM && p.stream.panels > 0 ? 64 : 256;
     const int32_t v[5] = {p.how, rows, cols, narrow ? p.splits : 1, narrow && p.once};
     std::copy(v, v + 5, plan);
     return 1;

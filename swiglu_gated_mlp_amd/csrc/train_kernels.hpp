@@ -248,11 +248,11 @@ __device__ __forceinline__ void row_to_codes(u32x4 v, unsigned (&d)[4]) {
     swap32(d[0], d[2]);
     swap32(d[1], d[3]);
 }
-// four codes times their scale: bytes as 0 .. 255 and one exact fma
+// four codes times their scale, exactly (bytes as 0 .. 255, less 128)
 __device__ __forceinline__ void code_values(unsigned d, float s, float* v) {
     const unsigned u = d ^ 0x80808080u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = fmaf((float)((u >> (8 * e)) & 255u), s, -128.0f * s);
+    for (int e = 0; e < 4; ++e) v[e] = ((float)((u >> (8 * e)) & 255u) - 128.0f) * s;
 }
 // A block of kept Gate and Up seen from its group's codes and scales of the tile's first
 // row: byte offsets of the lane's Gate codes, Up codes and scales of row r0 + (l & 31),

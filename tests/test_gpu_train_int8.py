@@ -91,6 +91,16 @@ def test_dequantized(dev, M, N):
     assert torch.equal(G, g.float().to(torch.bfloat16)) and torch.equal(U, u.float().to(torch.bfloat16))
 
 
+def test_dequantized_largest(dev):
+    """127 times the largest scale that bf16 holds it with: -128 times it is infinite."""
+    codes = torch.full((3, 1, 2, 32), 127, dtype=torch.int8, device=dev)
+    codes[1] = -127
+    codes[2] = 0
+    s = torch.full((1, 3, 2), 2.0 ** 121, dtype=torch.bfloat16, device=dev)
+    for x in sw.swiglu_dequantize_kept_int8(codes, s, 32):
+        assert torch.equal(x.double(), codes[:, 0, 0].double() * 2.0 ** 121)
+
+
 @pytest.mark.parametrize("M,K,N", SIZES + LARGE)
 def test_backward(dev, M, K, N):
     t = kept_case(dev, M, K, N)
