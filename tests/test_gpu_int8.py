@@ -352,3 +352,28 @@ def test_activations_past_2gib(dev):
     for r in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)):
         check_gemm(C[r], A[r], sa[r], W, s, "gemm")
         check_fused(Y[r], A[r], sa[r], W, s, W, s, "fused")
+
+
+@pytest.mark.parametrize("M,K,N", [(140000, 64, 16384), (1100000, 16, 2056)])
+def test_outputs_past_2gib(dev, M, K, N):
+    """Offsets of an output pass 31 bits; over a million rows."""
+    A, sa, W1, s1, W2, s2 = pair(dev, M, K, N, 9)
+    Y = sw.swiglu_fused_packed_int8(A, sa, sw.swiglu_pack_weights_int8(W1, W2), s1, s2)
+    C = sw.swiglu_gemm_packed_int8(A, sa, sw.swiglu_gemm_pack_weight_int8(W1), s1)
+    for r in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)):
+        check_fused(Y[r], A[r], sa[r], W1, s1, W2, s2, "fused")
+        check_gemm(C[r], A[r], sa[r], W1, s1, "gemm")
+
+
+def test_quantizing_past_2gib(dev):
+    """Over a million short rows, and elements past 31 bits."""
+    for M, K in ((1100000, 16), (70000, 32768)):
+        A = activations(dev, M, K, 1)
+        Q, s = sw.swiglu_quantize_rows_int8(A)
+        for r in (slice(0, 300), slice(M // 2, M // 2 + 300), slice(M - 300, M)):
+            q, t = quantized(A[r], 1)
+            assert torch.equal(Q[r], q) and torch.equal(s[r], t)
+    Q, s = sw.swiglu_quantize_columns_int8(A)
+    for c in (slice(0, 64), slice(K // 2, K // 2 + 64), slice(K - 64, K)):
+        q, t = quantized(A[:, c], 0)
+        assert torch.equal(Q[:, c], q) and torch.equal(s[c], t)
