@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _empty, _ptr, _raw_stream, _scratch, _shape, _stream, lib
+from . import _check, _empty, _raw_stream, _scratch, _shape, _stream, lib
 
 _need: dict = {}
 
@@ -81,6 +81,16 @@ def _matrix(t, name: str):
     if t.dim() != 2:
         raise ValueError("%s must be a matrix (got %s)" % (name, list(t.shape)))
     return t.shape
+
+
+def _space(workspace, need: int, device, s: int, here: int):
+    """The workspace's address and bytes."""
+    ws, ws_bytes = _scratch(workspace, need, device, s)
+    if ws is None:
+        return 0, 0
+    if ws.get_device() != here:
+        raise ValueError("the workspace is on %s, the current device is %d" % (ws.device, here))
+    return ws.data_ptr(), ws_bytes
 
 
 def _out(t, shape, dtype, device, s: int, stream):
@@ -173,9 +183,9 @@ def swiglu_fused_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wp: torch.Tensor
     p1, p2 = _vector(s1, N, "s1", here), _vector(s2, N, "s2", here)
     s, device = _stream_at(here, stream), A.device
     Y = _out(Y, (M, N), torch.bfloat16, device, s, stream)
-    ws, ws_bytes = _scratch(workspace, need, device, s)
+    ws, ws_bytes = _space(workspace, need, device, s, here)
     _check("swiglu_fused_packed_int8", lib().swiglu_fused_packed_int8(
-        a, r, w, p1, p2, _dev(Y, torch.bfloat16, "Y", here), M, K, N, _ptr(ws), ws_bytes, s))
+        a, r, w, p1, p2, _dev(Y, torch.bfloat16, "Y", here), M, K, N, ws, ws_bytes, s))
     return Y
 
 
@@ -191,9 +201,9 @@ def swiglu_gemm_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wg: torch.Tensor,
     p = _vector(sw, N, "sw", here)
     s, device = _stream_at(here, stream), A.device
     C = _out(C, (M, N), torch.bfloat16, device, s, stream)
-    ws, ws_bytes = _scratch(workspace, need, device, s)
+    ws, ws_bytes = _space(workspace, need, device, s, here)
     _check("swiglu_gemm_packed_int8", lib().swiglu_gemm_packed_int8(
-        a, r, w, p, _dev(C, torch.bfloat16, "C", here), M, K, N, _ptr(ws), ws_bytes, s))
+        a, r, w, p, _dev(C, torch.bfloat16, "C", here), M, K, N, ws, ws_bytes, s))
     return C
 
 
@@ -214,8 +224,8 @@ def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, 
     s, device = _stream_at(here, stream), A.device
     Y = _out(Y, (M, N), bf16, device, s, stream)
     Z = _out(Z, (M, K), bf16, device, s, stream)
-    ws, ws_bytes = _scratch(workspace, need, device, s)
-    st = lib().swiglu_mlp_packed_int8(a, wp, p1, p2, w3, p3, _dev(Y, bf16, "Y", here), _dev(Z, bf16, "Z", here), M, K, N,
-                                      _ptr(ws), ws_bytes, s)
+    ws, ws_bytes = _space(workspace, need, device, s, here)
+    st = lib().swiglu_mlp_packed_int8(a, wp, p1, p2, w3, p3, _dev(Y, bf16, "Y", here), _dev(Z, bf16, "Z", here), M, K,
+                                      N, ws, ws_bytes, s)
     _check("swiglu_mlp_packed_int8", st)
     return Y, Z

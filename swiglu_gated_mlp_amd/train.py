@@ -17,7 +17,7 @@ import torch
 
 from . import (_check, _dev_bf16, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
                swiglu_gemm_bf16)
-from .int8 import _dev, _here, _out, _stream_at
+from .int8 import _dev, _here, _out, _space, _stream_at
 
 _need: dict = {}
 
@@ -168,9 +168,9 @@ def swiglu_train_forward_int8(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tenso
     Y = _out(Y, (M, N), torch.bfloat16, device, s, stream)
     codes = _out(codes, (M, groups, 2, 32), torch.int8, device, s, stream)
     scales = _out(scales, (groups, M, 2), torch.bfloat16, device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, device), device, s)
+    ws, ws_bytes = _space(workspace, _cached(swiglu_train_forward_workspace_bytes, M, K, N, device), device, s, here)
     st = lib().swiglu_train_forward_int8(a, w1, w2, _bf16(Y, "Y", here), _dev(codes, torch.int8, "codes", here),
-                                         _bf16(scales, "scales", here), M, K, N, _ptr(ws), ws_bytes, s)
+                                         _bf16(scales, "scales", here), M, K, N, ws, ws_bytes, s)
     _check("swiglu_train_forward_int8", st)
     return Y, codes, scales
 
@@ -206,9 +206,9 @@ def swiglu_train_backward_int8(dY: torch.Tensor, A: torch.Tensor, W1: torch.Tens
     s, device = _stream_at(here, stream), A.device
     dA, = _grads(need_dA, (dA,), (M, K), ("dA",), device, s, stream)
     dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, device), device, s)
+    ws, ws_bytes = _space(workspace, _cached(swiglu_train_workspace_bytes, M, K, N, device), device, s, here)
     outs = [0 if t is None else _bf16(t, n, here) for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"))]
-    st = lib().swiglu_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
+    st = lib().swiglu_train_backward_int8(*ins, *outs, M, K, N, ws, ws_bytes, s)
     _check("swiglu_train_backward_int8", st)
     return dA, dW1, dW2
 
@@ -231,10 +231,10 @@ def swiglu_mlp_train_backward_int8(dZ: torch.Tensor, A: torch.Tensor, W1: torch.
     dA, = _grads(need_dA, (dA,), (M, K), ("dA",), device, s, stream)
     dW1, dW2 = _grads(need_dW, (dW1, dW2), (K, N), ("dW1", "dW2"), device, s, stream)
     dW3, = _grads(need_dW, (dW3,), (N, K), ("dW3",), device, s, stream)
-    ws, ws_bytes = _scratch(workspace, _cached(swiglu_train_workspace_bytes_int8, M, K, N, device), device, s)
+    ws, ws_bytes = _space(workspace, _cached(swiglu_train_workspace_bytes_int8, M, K, N, device), device, s, here)
     outs = [0 if t is None else _bf16(t, n, here)
             for t, n in ((dA, "dA"), (dW1, "dW1"), (dW2, "dW2"), (dW3, "dW3"))]
-    st = lib().swiglu_mlp_train_backward_int8(*ins, *outs, M, K, N, _ptr(ws), ws_bytes, s)
+    st = lib().swiglu_mlp_train_backward_int8(*ins, *outs, M, K, N, ws, ws_bytes, s)
     _check("swiglu_mlp_train_backward_int8", st)
     return dA, dW1, dW2, dW3
 

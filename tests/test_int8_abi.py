@@ -195,3 +195,12 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                  lambda: sw.swiglu_mlp_train_backward_int8(a, a, w, w, w3, codes, kept)):
         with pytest.raises(ValueError, match="the current device is 0"):
             call()
+
+
+def test_a_workspace_of_another_device_is_refused():
+    from swiglu_gated_mlp_amd import int8
+    elsewhere, here = torch.zeros(64, dtype=torch.uint8).as_subclass(Elsewhere), torch.zeros(64, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace is on cuda:1, the current device is 0"):
+        int8._space(elsewhere, 64, torch.device("cuda:0"), 0, 0)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        int8._space(here, 64, torch.device("cuda:0"), 0, 0)
