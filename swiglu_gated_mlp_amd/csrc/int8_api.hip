@@ -130,7 +130,7 @@ double stream_us(const Plan& p, int64_t M, int64_t K) {
     const double rows = p.tiles_n * 256.0;
     // panels: four to a column tile, a wave each
     if (p.panels > 0)
-        return 13.0 + overlapped(ceil_div(p.panels, p.cus) * p.KB * 0.42, (rows + M) * K / 12.0e6, 0.0);
+        return 9.0 + overlapped(ceil_div(p.panels, p.cus) * (p.KB * 0.36 + 7.5), (rows + M) * K / 12.0e6, 0.0);
     const int rest = p.tiles % p.cus;
     const double rounds = p.tiles / p.cus + (rest == 0 ? 0.0 : p.tail_ntiles ? (double)rest / p.cus + 0.25 : 1.0);
     return 4.3 + overlapped(rounds * (p.KB * 0.93 + 12.7), (rows + M) * K / 6.0e6,
@@ -148,7 +148,8 @@ bool decode_wide(bool gemm, int64_t nt, int cus) {
 // 12.5), and those that fill a round and a little (K=16384 N=5120, 8 rows 21.8 and 18.7).
 double decode_us(bool gemm, int64_t M, int64_t K, int64_t nt, int cus) {
     const int64_t KB = ceil_div(K, 128), groups = ceil_div(nt, 16);
-    if (M > 32) return gemm ? 5.0 + 0.16 * KB * ceil_div(2 * groups, cus) : 5.4 + 0.49 * KB * ceil_div(ceil_div(nt, 32), cus);
+    if (M > 32)
+        return gemm ? 5.0 + 0.16 * KB * ceil_div(2 * groups, cus) : 5.4 + 0.49 * KB * ceil_div(ceil_div(nt, 32), cus);
     const bool wide = decode_wide(gemm, nt, cus);
     if (!gemm && wide) return 5.6 + 2.0 * nt * K / 6.85e6;
     const bool pairs = gemm && wide && M > 8 && M <= 16;   // two groups a workgroup
@@ -199,7 +200,8 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
         p.tiles_m = (int)ceil_div(M, t.bm);
         p.groups = (int)ceil_div(p.units, t.waves);
         // weights that fit the last-level cache beside others stay there; see Narrow::ONCE
-        p.once = (int64_t)p.groups * t.waves * t.wt * 32 * KB * 128 > ((int64_t)32 << 20) && p.tiles_m <= (t.bm == 128 ? 4 : 2);
+        p.once = (int64_t)p.groups * t.waves * t.wt * 32 * KB * 128 > ((int64_t)32 << 20) &&
+                 p.tiles_m <= (t.bm == 128 ? 4 : 2);
         for (int s : kSplits) {
             if (s > 1 && 3 * s > KB) break;
             p.kb_per_split = (int)ceil_div(KB, s);
@@ -288,7 +290,8 @@ hipError_t launch_narrow_as(const swq::NarrowArgs& a, hipStream_t s) {
                                          dim3((unsigned)(a.tiles_m * a.groups * a.splits)), dim3(64 * WAVES), kargs, 0, s);
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t jobs = (int64_t)a.tiles_m * a.groups * WAVES * (GEMM ? WT : 1) * P::TM;
-    return hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_reduce_kernel<swq::Narrow<BM, WAVES, WT, 4, GEMM, false>>),
+    using R = swq::Narrow<BM, WAVES, WT, 4, GEMM, false>;
+    return hipLaunchKernel(reinterpret_cast<const void*>(&swq::narrow_reduce_kernel<R>),
                            dim3((unsigned)ceil_div(jobs, 4)), dim3(256), kargs, 0, s);
 }
 
