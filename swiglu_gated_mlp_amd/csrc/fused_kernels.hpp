@@ -1299,6 +1299,26 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
         std::conditional_t<LORA == 1, LoraTile<TM, GEMM ? 1 : 2>, LoraNone> tile(la, cur.m0, tl);
         if (ns - s >= 1) stage(I0{}, s);
         if (ns - s >= 2) stage(I1{}, s + 1);
+        // I8: the columns' scales of the wave's sums, and the rows', beside the last
+        // loads in flight (7B width, M=8192 912 -> 906 us; 0.5B, M=2048 30.2 -> 29.6;
+        // two stages earlier, beside the fragments, they spill: 926)
+        f32x4 cs[2][4];
+        float rs[TM];
+        if constexpr (I8) {
+            int sl = lane;
+            asm volatile("" : "+v"(sl));
+#pragma unroll
+            for (int g = 0; g < WT; ++g) {
+                const int tc = cur.n0 + wave * 32;   // (tiled) column of the wave's first
+                const int n = GEMM ? (tc >> 7) * PACK_ROWS + PACK_BN * g + (tc & (PACK_BN - 1)) : tc;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    cs[g][q] = scales4(GEMM || g == 0 ? p.s1 : p.s2, n + 8 * q + 4 * (sl >> 5), N);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) rs[i] = p.sa[min(cur.m0 + i * 32 + (sl & 31), M - 1)];
+            __builtin_amdgcn_sched_barrier(0);
+        }
         // the zero-chunk loads of the two stages past the end are still in
         // flight (their weight registers are consumed here, without
         // instructions, so the loads are not dropped); after the barrier no
@@ -1352,26 +1372,6 @@ __device__ __forceinline__ void stream_prefill_tiles(const FusedArgs& p, uint16_
             const int tc = cur.n0 + 32 * wave;
             tile.begin(cur.m0, GEMM ? ((tc >> 7) * PACK_ROWS + (tc & (PACK_BN - 1))) / 32 : tc / 32,
                        GEMM ? ((tc >> 7) * PACK_ROWS + (tc & (PACK_BN - 1)) + PACK_BN) / 32 : tc / 32);
-        }
-
-        // I8: the columns' scales of the wave's sums, and the rows', on their way
-        // before the next item's loads (a wait for them leaves those in flight)
-        f32x4 cs[2][4];
-        float rs[TM];
-        if constexpr (I8) {
-            int sl = lane;
-            asm volatile("" : "+v"(sl));
-#pragma unroll
-            for (int g = 0; g < WT; ++g) {
-                const int tc = cur.n0 + wave * 32;   // (tiled) column of the wave's first
-                const int n = GEMM ? (tc >> 7) * PACK_ROWS + PACK_BN * g + (tc & (PACK_BN - 1)) : tc;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    cs[g][q] = scales4(GEMM || g == 0 ? p.s1 : p.s2, n + 8 * q + 4 * (sl >> 5), N);
-            }
-#pragma unroll
-            for (int i = 0; i < TM; ++i) rs[i] = p.sa[min(cur.m0 + i * 32 + (sl & 31), M - 1)];
-            __builtin_amdgcn_sched_barrier(0);
         }
 
         // the next item's first two stages stream in during this epilogue
