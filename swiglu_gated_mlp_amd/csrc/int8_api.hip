@@ -69,9 +69,9 @@ bool in_chunks(int64_t M, int64_t K) { return M > stream_rows_limit(K, 1); }
 //   The estimates are microseconds of a launch on an idle device with the weights in
 // HBM and the caches full of something else's outputs, and only their order matters.
 // Fitted to this chip over 236 shapes (33 .. 4096 rows, K 128 .. 29568, N 512 .. 29568)
-// with every tile and up to 12 parts, 126 of them also launched one after another, and
-// over 84 of 1 .. 28 rows: off by 7 to 10 % in the root mean square, and the choice costs
-// 2 to 3 % over the best on average.
+// with every tile and up to 12 parts, 126 of them also launched one after another, over
+// 84 of 1 .. 28 rows and over 71 small ones of 40 .. 256: off by 7 to 10 % in the root
+// mean square, and the choice costs 2 to 3 % over the best on average.
 // ---------------------------------------------------------------------------
 struct Plan8 {
     enum How { DECODE, NARROW, STREAM } how;
@@ -90,7 +90,8 @@ struct Plan8 {
 // of waves that divide no power of two fill the CUs where the others leave a round
 // nearly empty: 7B width, 128 rows, fused <128,4,2> 33, <128,6,1> 30, 64 rows <64,4,1>
 // 30, <64,5,1> 25 us.  Leaving out one tile costs 0.5 (<64,5,1>) to 3 % on average.
-// 32 rows: batches of up to 32, against the decode kernel (see decode_us).
+// 32 rows: batches of up to 32, against the decode kernel (see decode_us), and small
+// products of up to 256 (0.5B width, 64 rows, fused <64,3,1> 6.0 us, <32,3,1> 5.5).
 struct NarrowTile {
     int bm, waves, wt;
     bool gemm;
@@ -100,10 +101,10 @@ struct NarrowTile {
 };
 constexpr NarrowTile kNarrow[] = {
     {128, 4, 2, true, 5.9, 0.172, 0.043, 0.68},  {128, 4, 1, true, 7.5, 0.177, 0.046, 0.46},
-    {128, 6, 1, false, 7.5, 0.177, 0.046, 0.46}, {64, 4, 1, true, 7.8, 0.121, 0.037, 0.18},
-    {64, 3, 1, true, 7.8, 0.121, 0.037, 0.18},   {64, 5, 1, false, 7.8, 0.121, 0.037, 0.18},
-    {32, 4, 1, true, 7.8, 0.070, 0.047, 0.25},   {32, 3, 1, true, 7.8, 0.070, 0.047, 0.25},
-    {32, 5, 1, false, 7.8, 0.070, 0.047, 0.25}};
+    {128, 6, 1, false, 7.5, 0.177, 0.046, 0.46}, {64, 4, 1, true, 7.8, 0.138, 0.031, 0.30},
+    {64, 3, 1, true, 7.8, 0.138, 0.031, 0.30},   {64, 5, 1, false, 7.8, 0.138, 0.031, 0.30},
+    {32, 4, 1, true, 8.2, 0.091, 0.042, 0.07},   {32, 3, 1, true, 8.2, 0.091, 0.042, 0.07},
+    {32, 5, 1, false, 8.2, 0.091, 0.042, 0.07}};
 
 // A CU's stages, the weights from HBM and the matrix cores overlap in part.
 double overlapped(double cu, double hbm, double mfma) { return std::sqrt(cu * cu + hbm * hbm + mfma * mfma); }
@@ -123,7 +124,7 @@ double narrow_us(const Plan8& p, int64_t K, int64_t M) {
     return t.once +
            overlapped(rounds_of(items, p.cus) * (p.kb_per_split * (t.stage + t.block * blocks) + t.finish * blocks),
                       (rows + M) * K / 6.7e6, 2.0 * p.tiles_m * t.bm * rows * K / 2.44e9) +
-           (p.splits > 1 ? 2.2 + 0.13 * p.splits + p.part_bytes / 4.0e6 : 0.0);
+           (p.splits > 1 ? 2.6 + 0.13 * p.splits + p.part_bytes / 4.0e6 : 0.0);
 }
 
 double stream_us(const Plan& p, int64_t M, int64_t K) {
@@ -142,14 +143,13 @@ bool decode_wide(bool gemm, int64_t nt, int cus) {
     return gemm ? ceil_div(nt, 16) >= cus : 4 * ceil_div(nt, 128) >= 3 * (int64_t)cus;
 }
 
-// The decode kernel as run_decode launches it, up to 64 rows.  Its workgroups read all
+// The decode kernel as run_decode launches it, up to 32 rows (one weight: 64).  Its workgroups read all
 // activations, so that long contractions with few columns are narrow_kernel's, whose
 // parts read theirs (one weight K=24352 N=848: 28 rows 24.7 and 13.0 us, 1 row 10.7 and
 // 12.5), and those that fill a round and a little (K=16384 N=5120, 8 rows 21.8 and 18.7).
 double decode_us(bool gemm, int64_t M, int64_t K, int64_t nt, int cus) {
     const int64_t KB = ceil_div(K, 128), groups = ceil_div(nt, 16);
-    if (M > 32)
-        return gemm ? 5.0 + 0.16 * KB * ceil_div(2 * groups, cus) : 5.4 + 0.49 * KB * ceil_div(ceil_div(nt, 32), cus);
+    if (M > 32) return 7.8 + (0.115 + 0.0005 * M) * KB * ceil_div(2 * groups, cus);
     const bool wide = decode_wide(gemm, nt, cus);
     if (!gemm && wide) return 5.6 + 2.0 * nt * K / 6.85e6;
     const bool pairs = gemm && wide && M > 8 && M <= 16;   // two groups a workgroup
@@ -185,13 +185,13 @@ Plan8 plan_int8(bool gemm, int64_t M, int64_t K, int64_t N) {
     if (in_chunks(M, K)) return best;
     const int64_t KB = ceil_div(K, 128);
     double best_us = stream_us(best.stream, M, K);
-    if (M <= 64) {
+    if (M <= (gemm ? 64 : 32)) {
         best.how = Plan8::DECODE;
         best_us = decode_us(gemm, M, K, gemm ? gemm_tiled_cols(N) : N, best.cus);
     }
     static const int kSplits[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 16};
     for (const NarrowTile& t : kNarrow) {
-        if ((gemm && !t.gemm) || (t.bm == 32) != (M <= 32)) continue;
+        if ((gemm && !t.gemm) || (t.bm == 32 ? M > 256 : M <= 32)) continue;
         Plan8 p = best;
         p.how = Plan8::NARROW;
         p.tile = (int)(&t - kNarrow);
@@ -257,9 +257,10 @@ hipError_t launch_decode8(const swk::DecodeArgs& a, int64_t n_tiled, hipStream_t
 //   K=29568 N=8192  M=1 / 16: <1,2,4> 38.4 / 40.3, <1,1,4> 37.3 / 49.2, <1,1,4,L> 38.7 / 42.9
 //                   M=32: 4 waves <2,2,2> 49.0, <2,1,2,L> 55.2
 //   K=4864 N=896    M=1 / 16 / 32: <1,1,4> 4.3, <1,1,4,L> 5.2 (16), <2,1,2,L> 6.5 (32)
-// 33 to 64 rows, on products that are too small for narrow_kernel to fill the CUs:
-//   K=896 N=4864    M=64: <4,2,1,L> 6.1, 8 waves <4,1,1,L> 7.3 (narrow_kernel 7.4)
-//   K=4864 N=896    M=64: 8 waves <4,1,1,L> 7.9, 4 waves 10.4 (narrow_kernel 9.5)
+// 33 to 64 rows of one weight, where narrow_kernel needs parts to fill the CUs:
+//   K=4864 N=896    M=40 / 64: <4,1,1,L> 8.0 / 8.6, 4 waves 10.4 (narrow_kernel 8.8 / 9.0)
+//   K=1024 N=3584   M=40 / 64: <4,1,1,L> 4.2 / 4.5 (narrow_kernel 5.2 / 5.2)
+// (the fused product: K=896 N=4864 6.2 / 6.4, narrow_kernel 5.3 / 5.5)
 template <bool GEMM>
 hipError_t run_decode(const swk::DecodeArgs& d, int64_t nt, int cus, hipStream_t s) {
     const bool wide = decode_wide(GEMM, nt, cus);
@@ -272,7 +273,6 @@ hipError_t run_decode(const swk::DecodeArgs& d, int64_t nt, int cus, hipStream_t
         return d.M > 4 ? launch_decode8<1, 1, 4, true, true, true, 8>(d, nt, s)
                        : launch_decode8<1, 1, 4, true, true, false, 8>(d, nt, s);
     } else {
-        if (d.M > 32) return launch_decode8<4, 2, 1, false, false, true, 4>(d, nt, s);
         if (wide) return launch_decode8<2, 8, 1, false, false, false, 4>(d, nt, s);
         if (d.M <= 8) return launch_decode8<1, 1, 8, false, false, false, 4>(d, nt, s);
         return d.M <= 16 ? launch_decode8<1, 1, 4, false, false, true, 8>(d, nt, s)

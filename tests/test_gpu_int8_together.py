@@ -59,7 +59,7 @@ def test_trained_quantized_served(dev):  # noqa: F811
 
 def test_two_streams_at_once(dev):  # noqa: F811
     """Calls that run side by side, each with a workspace of its own."""
-    K, N = 3584, 1040   # K long enough that the products of 100 rows are split
+    K, N = 14336, 528   # K long enough that the product of 100 rows is split
     W = [randn(dev, 7 + i, *s).bfloat16() for i, s in enumerate(((K, N), (K, N), (N, K)))]
     W8 = [sw.swiglu_quantize_columns_int8(w) for w in W]
     w = (sw.swiglu_pack_weights_int8(W8[0][0], W8[1][0]), W8[0][1], W8[1][1],
