@@ -270,9 +270,13 @@ __global__ __launch_bounds__(64 * P::WAVES) void narrow_kernel(NarrowArgs p) {
     for (int t = 0; t < WT; ++t) narrow_scales<P>(p, u, t, lane, cs[t]);
 #pragma unroll
     for (int i = 0; i < TM; ++i) rs[i] = p.sa[min(m0 + 32 * i + (lane & 31), p.M - 1)];
+    __builtin_amdgcn_sched_barrier(0);
+    // each stage's loads stay behind the one's before: the wait leaves as many in flight
+    // as the later stages have, whichever they are
     each(Upto<NBUF - 1>{}, [&](auto qc) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) issue(j, decltype(qc)::value, qc);
+        __builtin_amdgcn_sched_barrier(0);
     });
     __builtin_amdgcn_s_waitcnt(waitcnt_imm((NBUF - 2) * LOADS, 0));
     __builtin_amdgcn_s_barrier();
