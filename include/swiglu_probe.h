@@ -59,6 +59,14 @@ int swiglu_probe_train_plan(int launch, int64_t M, int64_t K, int64_t N, int32_t
 int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N,
                            int32_t plan[5]);
 
+/* Which form of that kernel (host call): form receives, for many rows, the column tiles
+ * run as 128-row tiles behind the 256-row ones and the panels (0 without); for the
+ * decode kernel, whether workgroups take its many column groups; and whether K ends
+ * inside a block of 128.  Activations of 2 GiB and more: the first chunk's.  Returns
+ * as swiglu_probe_int8_plan. */
+int swiglu_probe_int8_form(int gemm, int64_t M, int64_t K, int64_t N,
+                           int32_t form[4]);
+
 #ifdef __cplusplus
 }
 #endif

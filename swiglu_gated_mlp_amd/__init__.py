@@ -101,6 +101,7 @@ SIGNATURES = {
     "swiglu_probe_mfma": ([_P, ctypes.c_int, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_read": ([_P, ctypes.c_size_t, _P, ctypes.c_int, _P], ctypes.c_int),
     "swiglu_probe_int8_plan": ([ctypes.c_int, _I64, _I64, _I64, _P], ctypes.c_int),
+    "swiglu_probe_int8_form": ([ctypes.c_int, _I64, _I64, _I64, _P], ctypes.c_int),
     "swiglu_probe_train_plan": ([ctypes.c_int, _I64, _I64, _I64, _P], ctypes.c_int),
 }
 
@@ -741,6 +742,15 @@ def swiglu_probe_int8_plan(gemm: bool, M: int, K: int, N: int) -> dict:
         raise ValueError("invalid shape M=%d K=%d N=%d" % (M, K, N))
     return dict(kernel=("decode", "narrow", "stream")[out[0]], rows=out[1], cols=out[2], splits=out[3],
                 once=bool(out[4]))
+
+
+def swiglu_probe_int8_form(gemm: bool, M: int, K: int, N: int) -> dict:
+    """Which form of that kernel: 128-row column tiles behind the 256-row ones, panels,
+    whether decode workgroups are wide, whether K ends inside a block."""
+    out = (ctypes.c_int32 * 4)()
+    if lib().swiglu_probe_int8_form(int(bool(gemm)), M, K, N, out) == 0:
+        raise ValueError("invalid shape M=%d K=%d N=%d" % (M, K, N))
+    return dict(tail=out[0], panels=out[1], wide=bool(out[2]), ragged=bool(out[3]))
 
 
 # training (gradients and differentiable forms of the product and the block)

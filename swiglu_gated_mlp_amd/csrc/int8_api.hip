@@ -580,4 +580,17 @@ int swiglu_probe_int8_plan(int gemm, int64_t M, int64_t K, int64_t N, int32_t* p
     return 1;
 }
 
+int swiglu_probe_int8_form(int gemm, int64_t M, int64_t K, int64_t N, int32_t* form) {
+    if (check_shape_int8(M, K, N) != SWIGLU_OK || M == 0 || !form) return 0;
+    const Plan8 p = in_chunks(M, K) ? stream_plan(gemm != 0, balanced_chunk(M, stream_rows_limit(K, 1)), K, N)
+                                    : plan_int8(gemm != 0, M, K, N);
+    const bool stream = p.how == Plan8::STREAM;
+    const int panels = stream ? p.stream.panels : 0;
+    const int32_t v[4] = {stream && panels == 0 ? p.stream.tail_ntiles : 0, panels,
+                          p.how == Plan8::DECODE && decode_wide(gemm != 0, gemm ? gemm_tiled_cols(N) : N, p.cus),
+                          K % 128 != 0};
+    std::copy(v, v + 4, form);
+    return 1;
+}
+
 }  // extern "C"
