@@ -498,8 +498,9 @@ swiglu_status swiglu_mlp_train_backward(
  *     s = max(max |x| / 127 rounded up to bf16, 2^-126),  code = round(x / s)
  * of the fp32 sums x, within 2^-16 of a step exact; the backward calls compute from
  * G = code s and U alike, and Y = bf16(SiLU(G) U) of those for dW3.  A kept element
- * is off by at most half a step, max |x| of its group / 253.  A group that holds an
- * infinity or NaN has the scale NaN: what is computed from it is NaN.
+ * is off by about half a step at most: max |x| of its group / 252 (rounding a scale
+ * up widens the step by up to 2^-7 of it), or 2^-127 where that is more.  A group that
+ * holds an infinity or NaN has the scale NaN: what is computed from it is NaN.
  *   codes  int8 [M][groups][2][32], groups = ceil(N / 32): Gate's codes of a group,
  *          then Up's; codes of columns past N are 0
  *   scales bf16 [groups][M][2]: Gate's, Up's
