@@ -615,7 +615,9 @@ swiglu_status swiglu_gemm_packed_lora(const swiglu_bf16 *A, const swiglu_bf16 *W
  * (int32, exact in any order), scaled once in fp32:
  *     C[m,n] = bf16_RNE((fp32(sum_k a8 w8) * sw[n]) * sa[m]),
  *     Y[m,n] = bf16_RNE(SiLU(G) * U),  G, U alike from W1 and W2,
- * on v_mfma_i32_32x32x32_i8 and v_mfma_i32_16x16x64_i8.
+ * on v_mfma_i32_32x32x32_i8 and v_mfma_i32_16x16x64_i8.  Both products are fp32 steps:
+ * where the sum times sw[n] overflows (sw[n] of 2^97 and more), the result is infinite
+ * or NaN, however small sa[m] is.
  *
  * swiglu_quantize_rows_int8: A [M,K] bf16 -> codes Q [M,K] and scales [M] with
  *   t = max(max_k |A[m,k]|, 2^-96): scales = t / 127, Q = round(A * (127 / t)),

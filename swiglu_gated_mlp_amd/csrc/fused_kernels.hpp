@@ -130,8 +130,9 @@ __device__ __forceinline__ f32x4 scales4(const float* s, int n, int N) {
     typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
     return *reinterpret_cast<const f32x4u*>(s + min(n, N - 4));
 }
-// An int32 sum's value: the column's scale first, as weights are small, so that
-// only a result that overflows overflows.
+// An int32 sum's value: the column's scale first, as weights are small.  The sum times
+// it is rounded to fp32 on the way, so it has to be finite (any scale below 2^97 is
+// enough); a small row scale does not bring an infinity back.
 __device__ __forceinline__ float scaled(int sum, float col, float row) { return ((float)sum * col) * row; }
 
 // ---------------------------------------------------------------------------
