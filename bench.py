@@ -158,8 +158,8 @@ def run_context():
 def kernel_source_sha256():
     import hashlib
     h = hashlib.sha256()
-    for f in ("device_common.hpp", "lora_device.hpp", "fused_kernels.hpp", "host_common.hpp", "launch.hpp",
-              "swiglu_api.hip"):
+    for f in ("device_common.hpp", "lora_device.hpp", "fused_kernels.hpp", "product_kernels.hpp", "host_common.hpp",
+              "launch.hpp", "swiglu_api.hip"):
         with open(os.path.join(ROOT, "swiglu_gated_mlp_amd", "csrc", f), "rb") as fh:
             h.update(fh.read())
     return h.hexdigest()

@@ -1,6 +1,6 @@
-// Device kernels of the int8 products' own (swiglu_*_int8): quantizing rows and
-// columns, the weight packs, and the splits' reduction.  The products themselves
-// run on the packed kernels of fused_kernels.hpp with I8.
+// Device kernels of the int8 calls besides the products (swiglu_*_int8): quantizing
+// rows and columns, and the weight packs.  The products run on the packed kernels of
+// fused_kernels.hpp with I8 and on narrow_kernel (int8_narrow.hpp).
 //
 // Symmetric quantization: x = s q, q whole in -127 .. 127, one s for a row of
 // activations (token) or a column of a weight (channel).  Then

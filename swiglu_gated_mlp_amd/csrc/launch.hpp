@@ -12,7 +12,7 @@
 
 #include "fused_kernels.hpp"
 #include "host_common.hpp"
-#include "lora_kernels.hpp"
+#include "lora_stream.hpp"
 
 namespace swl {
 

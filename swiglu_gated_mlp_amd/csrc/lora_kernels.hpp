@@ -1,6 +1,7 @@
-// Kernels of the low-rank adapters: the pack, the factor t = s_i (A La_i), the
-// reduction of splits with adapters, and the adapted forms of the streaming and
-// decode kernels (their adapter step is lora_device.hpp).
+// Kernels of the low-rank adapters: the pack, the factor t = s_i (A La_i) and the
+// reduction of splits with adapters.  The adapted forms of the streaming and decode
+// kernels are in lora_stream.hpp and fused_kernels.hpp, their adapter step in
+// lora_device.hpp.
 #pragma once
 
 #include "fused_kernels.hpp"
@@ -19,7 +20,7 @@ namespace swk {
 //   flags   [adapter] int32: 1 where the adapter's Lb holds an infinity or NaN
 // one thread per 16 bytes, padding zero; the flags, zero before, by a second launch.
 // ---------------------------------------------------------------------------
-[[maybe_unused]] static __global__ __launch_bounds__(256) void lora_pack_kernel(const uint16_t* __restrict__ La1,
+__global__ __launch_bounds__(256) void lora_pack_kernel(const uint16_t* __restrict__ La1,
                                                         const uint16_t* __restrict__ La2,
                                                         const uint16_t* __restrict__ Lb1,
                                                         const uint16_t* __restrict__ Lb2, uint16_t* __restrict__ out,
@@ -68,7 +69,7 @@ namespace swk {
 
 // pieces: 16-byte pieces of an adapter's Lb; `share` workgroups an adapter, and all
 // that find one store the same 1.
-[[maybe_unused]] static __global__ __launch_bounds__(256) void lora_flag_kernel(const uint16_t* __restrict__ B, int* __restrict__ flags,
+__global__ __launch_bounds__(256) void lora_flag_kernel(const uint16_t* __restrict__ B, int* __restrict__ flags,
                                                         long long pieces, int share, int adapters) {
     for (int l = blockIdx.x / share; l < adapters; l += gridDim.x / share) {
         const u32x4* b = reinterpret_cast<const u32x4*>(B) + l * pieces;
@@ -335,31 +336,6 @@ __global__ __launch_bounds__(256) void lora_reduce_kernel(const float* __restric
                 u32x2{pack2(silu_f(g[t][0]) * u[t][0], silu_f(g[t][1]) * u[t][1]),
                       pack2(silu_f(g[t][2]) * u[t][2], silu_f(g[t][3]) * u[t][3])};
         }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// The streaming kernels with adapters (the decode kernel takes LoraArgs itself).
-// ---------------------------------------------------------------------------
-template <int BM, bool RAGGED, bool PANELS, bool GEMM, int LORA>
-__global__ __launch_bounds__(256) void stream_lora_kernel(FusedArgs p, LoraArgs la, int total) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[stream_smem_elems<BM>()];
-    stream_prefill_tiles<BM, false, RAGGED, PANELS, false, false, false, GEMM, LORA>(p, smem, blockIdx.x, gridDim.x,
-                                                                                    total, &la);
-}
-
-template <bool RAGGED, bool GEMM>
-__global__ __launch_bounds__(256) void stream_lora_mixed_kernel(FusedArgs big, FusedArgs tail, LoraArgs la, int n_pers,
-                                                                int n_big) {
-    __shared__ __attribute__((aligned(16))) uint16_t smem[stream_smem_elems<256>()];
-    const int b = blockIdx.x;
-    if (b < n_pers) {
-        stream_prefill_tiles<256, false, RAGGED, false, false, false, false, GEMM, 1>(big, smem, b, n_pers, n_big,
-                                                                                        &la);
-    } else {
-        const int n_tail = gridDim.x - n_pers;
-        stream_prefill_tiles<128, false, RAGGED, false, false, false, false, GEMM, 1>(tail, smem, b - n_pers, n_tail,
-                                                                                        n_tail, &la);
     }
 }
 

@@ -20,6 +20,7 @@
 #include "launch.hpp"
 #include "lora_kernels.hpp"
 #include "probe_kernels.hpp"
+#include "product_kernels.hpp"
 
 // Device scratch of swiglu_fused_packed_noalloc: the split-K partial sums of
 // callers that cannot allocate.  One copy per device, held from the

@@ -1,5 +1,5 @@
 """Checks of the int8 kernels' compiled code that no run shows: waits that count loads
-rely on the loads' order."""
+rely on the loads' order, and a kernel that nothing launches is never run."""
 import os
 import re
 import subprocess
@@ -63,3 +63,14 @@ def test_narrow_kernels_issue_a_stage_after_the_other(kernels):
             assert sorted(loads[at:at + len(stage)]) == sorted(stage), (name, loads, i)
         assert left == len(stage) * (stages - 2), (name, left)
     assert found >= 20
+
+
+def test_every_kernel_is_launched(kernels):
+    """The unit holds no kernel that its host code does not launch."""
+    host = ""
+    for name in ("int8_api.hip", "launch.hpp"):
+        with open(os.path.join(build.CSRC, name)) as f:
+            host += f.read()
+    launched = set(re.findall(r"&sw[kq]::(\w+)", host))
+    for name in kernels:
+        assert re.search(r"sw[kq]::(\w+)", name).group(1) in launched, name
