@@ -1629,6 +1629,7 @@ __global__ __launch_bounds__(64 * WAVES) void decode_kernel(DecodeArgs p, Lora..
     constexpr int NH = HALF ? 1 : 2;    // weight halves per workgroup
     constexpr int AROWS = 16 * MT;      // activation rows per K block
     static_assert(!I8 || sizeof...(Lora) == 0, "adapters: bf16 operands");
+    static_assert(!I8 || GEMM == HALF, "int8: one weight by halves");
     __shared__ Acc4<I8> red[WAVES][MT][CG][NH][64];
     __shared__ __attribute__((aligned(16))) uint16_t sA[LDSA ? WAVES * UNROLL * AROWS * PACK_BK : 8];
 
@@ -1778,9 +1779,9 @@ __global__ __launch_bounds__(64 * WAVES) void decode_kernel(DecodeArgs p, Lora..
         const int n = n0 + 16 * c + 4 * kq;
         f32x4 g, u;
         if constexpr (I8) {
-            const int col = GEMM ? (n / PACK_BN) * PACK_ROWS + n % PACK_BN + (HALF ? PACK_BN * half : 0) : n;
+            const int col = HALF ? (n / PACK_BN) * PACK_ROWS + n % PACK_BN + PACK_BN * half : n;
             const f32x4 c1 = scales4(p.s1, col, N);
-            const f32x4 c2 = HALF ? c1 : GEMM ? scales4(p.s1, col + PACK_BN, N) : scales4(p.s2, col, N);
+            const f32x4 c2 = HALF ? c1 : scales4(p.s2, col, N);
             const float row = p.sa[min(m, M - 1)];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
