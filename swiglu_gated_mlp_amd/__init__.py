@@ -159,10 +159,18 @@ def _dev_bf16(t: torch.Tensor, name: str) -> int:
     raise ValueError("%s must be contiguous" % name)
 
 
+def _tensor(t, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+
+
 def _shape(t, shape, name: str) -> None:
     """A tensor the library reads or writes must hold exactly this shape (the C
     ABI takes bare pointers and trusts the sizes)."""
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is None:
+        return
+    _tensor(t, name)
+    if tuple(t.shape) != tuple(shape):
         raise ValueError("%s must be %s (got %s)" % (name, list(shape), list(t.shape)))
 
 

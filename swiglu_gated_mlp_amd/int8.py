@@ -5,7 +5,7 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _empty, _raw_stream, _scratch, _shape, _stream, lib
+from . import _check, _empty, _raw_stream, _scratch, _shape, _stream, _tensor, lib
 
 _need: dict = {}
 
@@ -59,8 +59,7 @@ def _dev(t, dtype, name: str, here: int) -> int:
     """A contiguous tensor of dtype on the current GPU."""
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous() and t.get_device() == here:
         return t.data_ptr()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
+    _tensor(t, name)
     if t.device.type != "cuda":
         raise ValueError("%s must be a GPU tensor (got %s)" % (name, t.device))
     if t.dtype != dtype:
@@ -71,16 +70,25 @@ def _dev(t, dtype, name: str, here: int) -> int:
 
 
 def _vector(t, n: int, name: str, here: int) -> int:
-    if t.dtype is torch.float32 and t.shape == (n,) and t.is_contiguous() and t.get_device() == here:
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == (n,) and t.is_contiguous()
+            and t.get_device() == here):
         return t.data_ptr()
     _shape(t, (n,), name)
     return _dev(t, torch.float32, name, here)
 
 
 def _matrix(t, name: str):
+    _tensor(t, name)
     if t.dim() != 2:
         raise ValueError("%s must be a matrix (got %s)" % (name, list(t.shape)))
     return t.shape
+
+
+def _length(t, name: str) -> int:
+    _tensor(t, name)
+    if t.dim() != 1:
+        raise ValueError("%s must be a vector (got %s)" % (name, list(t.shape)))
+    return t.shape[0]
 
 
 def _space(workspace, need: int, device, s: int, here: int):
@@ -135,8 +143,10 @@ def _packed(fn: str, sizer, weights, Wp, name: str, stream):
         raise ValueError("invalid int8 weight shape [%d,%d] (K must be a multiple of 16, N of 8)" % (K, N))
     here = _here()
     ptrs, s = [_dev(t, torch.int8, n, here) for t, n in weights], _stream_at(here, stream)
-    if Wp is not None and Wp.numel() < nbytes:
-        raise ValueError("%s too small: need %d bytes" % (name, nbytes))
+    if Wp is not None:
+        _tensor(Wp, name)
+        if Wp.numel() < nbytes:
+            raise ValueError("%s too small: need %d bytes" % (name, nbytes))
     Wp = _out(Wp, (nbytes,), torch.int8, W.device, s, stream)
     _check(fn, getattr(lib(), fn)(*ptrs, _dev(Wp, torch.int8, name, here), K, N, s))
     return Wp
@@ -154,6 +164,7 @@ def swiglu_gemm_pack_weight_int8(W: torch.Tensor, Wg: torch.Tensor | None = None
 
 
 def _weight_at_least(W, need: int, K: int, N: int, name: str) -> None:
+    _tensor(W, name)
     if need == 0:
         raise ValueError("invalid int8 weight shape [%d,%d]" % (K, N))
     if W.numel() < need:
@@ -175,7 +186,7 @@ def swiglu_fused_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wp: torch.Tensor
                              Y: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
     """Y = SiLU(G) * U bf16 [M,N] from the codes A int8 [M,K], their rows' scales sa
     [M], the packed codes of W1 and W2 and their columns' scales s1, s2 [N] (fp32)."""
-    (M, K), N, here = _matrix(A, "A"), s1.shape[0], _here()
+    (M, K), N, here = _matrix(A, "A"), _length(s1, "s1"), _here()
     least, need = _sizes(swiglu_packed_bytes_int8, swiglu_workspace_bytes_int8, M, K, N, here)
     _weight_at_least(Wp, least, K, N, "Wp")
     _shape(Y, (M, N), "Y")
@@ -193,7 +204,7 @@ def swiglu_gemm_packed_int8(A: torch.Tensor, sa: torch.Tensor, Wg: torch.Tensor,
                             C: torch.Tensor | None = None, workspace=None, stream=None) -> torch.Tensor:
     """C = A @ W bf16 [M,N] from the codes A int8 [M,K], sa [M], one weight's packed
     codes and its columns' scales sw [N] (fp32)."""
-    (M, K), N, here = _matrix(A, "A"), sw.shape[0], _here()
+    (M, K), N, here = _matrix(A, "A"), _length(sw, "sw"), _here()
     least, need = _sizes(swiglu_gemm_packed_bytes_int8, swiglu_gemm_workspace_bytes_int8, M, K, N, here)
     _weight_at_least(Wg, least, K, N, "Wg")
     _shape(C, (M, N), "C")
@@ -212,7 +223,7 @@ def swiglu_mlp_packed_int8(A: torch.Tensor, Wp: torch.Tensor, s1: torch.Tensor, 
                            workspace=None, stream=None):
     """The gated MLP block from A bf16 [M,K]: its rows quantized, Y = SiLU(G) * U
     (bf16), Y's rows quantized, Z = Y @ W3.  Returns (Y, Z)."""
-    (M, K), N, here = _matrix(A, "A"), s1.shape[0], _here()
+    (M, K), N, here = _matrix(A, "A"), _length(s1, "s1"), _here()
     least, need = _sizes(swiglu_packed_bytes_int8, swiglu_mlp_workspace_bytes_int8, M, K, N, here)
     _weight_at_least(Wp, least, K, N, "Wp")
     _weight_at_least(W3g, _cached(swiglu_gemm_packed_bytes_int8, N, K), N, K, "W3g")

@@ -15,7 +15,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (_check, _dev_bf16, _new, _ptr, _scratch, _shape, _stream, lib, swiglu_fused,
+from . import (_check, _dev_bf16, _new, _ptr, _scratch, _shape, _stream, _tensor, lib, swiglu_fused,
                swiglu_gemm_bf16)
 from .int8 import _dev, _here, _out, _space, _stream_at
 
@@ -41,6 +41,8 @@ def _cached(fn, M: int, K: int, N: int, device) -> int:
 
 
 def _weights(A, W1, W2):
+    _tensor(A, "A")
+    _tensor(W1, "W1")
     if A.dim() != 2 or W1.dim() != 2:
         raise ValueError("A must be [M,K] and W1, W2 [K,N]")
     M, K = A.shape
@@ -178,7 +180,8 @@ def swiglu_train_forward_int8(A: torch.Tensor, W1: torch.Tensor, W2: torch.Tenso
 def swiglu_dequantize_kept_int8(codes: torch.Tensor, scales: torch.Tensor, N: int, G: torch.Tensor | None = None,
                                 U: torch.Tensor | None = None, stream=None):
     """(G, U) bf16 [M,N] of what swiglu_train_forward_int8 kept."""
-    M = codes.shape[0]
+    _tensor(codes, "codes")
+    M = codes.shape[0] if codes.dim() else 0
     _kept_shapes(codes, scales, M, N)
     for t, name in ((G, "G"), (U, "U")):
         _shape(t, (M, N), name)
