@@ -4,9 +4,10 @@
 
 Three translation units, compiled side by side, export the C ABI of
 include/swiglu.h: csrc/swiglu_api.hip (the products, kernels in
-csrc/fused_kernels.hpp), csrc/train_api.hip (training, kernels in
+csrc/fused_kernels.hpp and csrc/product_kernels.hpp, adapters in
+csrc/lora_*.hpp), csrc/train_api.hip (training, kernels in
 csrc/train_kernels.hpp) and csrc/int8_api.hip (the int8 products, kernels in
-csrc/int8_kernels.hpp and csrc/fused_kernels.hpp).
+csrc/int8_*.hpp and csrc/fused_kernels.hpp).
 """
 from __future__ import annotations
 

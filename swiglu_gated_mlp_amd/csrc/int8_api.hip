@@ -68,10 +68,11 @@ bool in_chunks(int64_t M, int64_t K) { return M > stream_rows_limit(K, 1); }
 // fastest.
 //   The estimates are microseconds of a launch on an idle device with the weights in
 // HBM and the caches full of something else's outputs, and only their order matters.
-// Fitted to this chip over 236 shapes (33 .. 4096 rows, K 128 .. 29568, N 512 .. 29568)
-// with every tile and up to 12 parts, 126 of them also launched one after another, over
-// 84 of 1 .. 28 rows and over 71 small ones of 40 .. 256: off by 7 to 10 % in the root
-// mean square, and the choice costs 2 to 3 % over the best on average.
+// Their constants are this chip's (256 CUs), fitted over some 390 shapes with every tile
+// and up to 12 parts.  On 160 other shapes, drawn at random (1 .. 4096 rows, K and N 128
+// .. 29568), they are off by 13 % in the root mean square, those of few rows all alike,
+// and the chosen plan takes 1.3 % longer than the fastest measured one on average (144
+// shapes within 5 %, 18 % at worst).
 // ---------------------------------------------------------------------------
 struct Plan8 {
     enum How { DECODE, NARROW, STREAM } how;
