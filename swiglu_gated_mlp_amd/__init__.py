@@ -167,10 +167,8 @@ def _tensor(t, name: str) -> None:
 def _shape(t, shape, name: str) -> None:
     """A tensor the library reads or writes must hold exactly this shape (the C
     ABI takes bare pointers and trusts the sizes)."""
-    if t is None:
-        return
-    _tensor(t, name)
-    if tuple(t.shape) != tuple(shape):
+    if t is not None and tuple(getattr(t, "shape", ())) != tuple(shape):
+        _tensor(t, name)
         raise ValueError("%s must be %s (got %s)" % (name, list(shape), list(t.shape)))
 
 

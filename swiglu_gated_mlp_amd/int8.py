@@ -69,26 +69,36 @@ def _dev(t, dtype, name: str, here: int) -> int:
     raise ValueError("%s is on %s, the current device is %d" % (name, t.device, here))
 
 
+# What is no tensor lacks these attributes, or fails a comparison: only then is its type
+# looked at (asked first, it took 0.4 us a call).
 def _vector(t, n: int, name: str, here: int) -> int:
-    if (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == (n,) and t.is_contiguous()
-            and t.get_device() == here):
-        return t.data_ptr()
+    try:
+        if t.dtype is torch.float32 and t.shape == (n,) and t.is_contiguous() and t.get_device() == here:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _shape(t, (n,), name)
     return _dev(t, torch.float32, name, here)
 
 
 def _matrix(t, name: str):
-    _tensor(t, name)
-    if t.dim() != 2:
+    try:
+        flat = t.dim() == 2
+    except AttributeError:
+        _tensor(t, name)
+        raise
+    if not flat:
         raise ValueError("%s must be a matrix (got %s)" % (name, list(t.shape)))
     return t.shape
 
 
 def _length(t, name: str) -> int:
-    _tensor(t, name)
-    if t.dim() != 1:
+    try:
+        n, = t.shape
+    except (AttributeError, ValueError):
+        _tensor(t, name)
         raise ValueError("%s must be a vector (got %s)" % (name, list(t.shape)))
-    return t.shape[0]
+    return n
 
 
 def _space(workspace, need: int, device, s: int, here: int):
@@ -164,11 +174,15 @@ def swiglu_gemm_pack_weight_int8(W: torch.Tensor, Wg: torch.Tensor | None = None
 
 
 def _weight_at_least(W, need: int, K: int, N: int, name: str) -> None:
-    _tensor(W, name)
+    try:
+        n = W.numel()
+    except AttributeError:
+        _tensor(W, name)
+        raise
     if need == 0:
         raise ValueError("invalid int8 weight shape [%d,%d]" % (K, N))
-    if W.numel() < need:
-        raise ValueError("%s holds %d codes; a packed int8 [%d,%d] weight needs %d" % (name, W.numel(), K, N, need))
+    if n < need:
+        raise ValueError("%s holds %d codes; a packed int8 [%d,%d] weight needs %d" % (name, n, K, N, need))
 
 
 def _sizes(weights, need, M: int, K: int, N: int, here: int):

@@ -41,9 +41,13 @@ def _cached(fn, M: int, K: int, N: int, device) -> int:
 
 
 def _weights(A, W1, W2):
-    _tensor(A, "A")
-    _tensor(W1, "W1")
-    if A.dim() != 2 or W1.dim() != 2:
+    try:
+        flat = A.dim() == 2 and W1.dim() == 2
+    except AttributeError:
+        _tensor(A, "A")
+        _tensor(W1, "W1")
+        raise
+    if not flat:
         raise ValueError("A must be [M,K] and W1, W2 [K,N]")
     M, K = A.shape
     N = W1.shape[1]

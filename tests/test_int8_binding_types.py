@@ -42,6 +42,7 @@ def on_the_cpu(monkeypatch):
     for m in (int8, train):
         monkeypatch.setattr(m, "_here", lambda: -1)
         monkeypatch.setattr(m, "_stream_at", lambda here, stream: 0)
+        monkeypatch.setattr(m, "_space", lambda *rest: (0, 0))
     monkeypatch.setattr(int8, "_out", lambda t, *rest: torch.zeros(1) if t is None else t)
     monkeypatch.setattr(train, "_out", lambda t, *rest: torch.zeros(1) if t is None else t)
     monkeypatch.setattr(train, "_new", lambda *rest: torch.zeros(1))
